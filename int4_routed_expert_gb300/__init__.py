@@ -2,8 +2,16 @@
 
 The layer lives in the C-ABI library ``libmoe.so`` (include/moe.h); this
 package holds its CUDA sources (``csrc/``), the in-tree build
-(``build.py``) and the ctypes binding (``moe.py``).
+(``build.py``) and the ctypes bindings: ``moe.py`` (the layer, the expert
+tier) and ``attn.py`` (rotary positions, the 8-bit paged cache and attention
+over it, include/moe_attn.h).
 """
+from .attn import (  # noqa: F401
+    KVCache,
+    Rope,
+    SeqBatch,
+    rope_frequencies,
+)
 from .moe import (  # noqa: F401
     EXPORTED,
     ExpertTier,

@@ -1,0 +1,347 @@
+"""ctypes binding of include/moe_attn.h: rotary positions, the 8-bit paged cache and attention over it.
+
+A decoder layer next to the MoE layer calls, per step:
+    q, k = rope.apply(q, positions, k=k)         # Rope
+    cache.write(k, v, batch)                      # KVCache: quantise into the pages
+    out = cache.attend(q, batch)                  # attention over the cache, the new tokens included
+``SeqBatch`` describes the step's tokens (device arrays and the host's bounds).  As in moe.py, torch supplies
+device memory and streams only; every step runs in the library's kernels and there is no fallback.
+"""
+from __future__ import annotations
+
+import ctypes as C
+import math
+
+from . import moe
+from .moe import MOE_BF16, MOE_F32, MOE_OK, MoeError
+
+
+class moe_rope_tensor_t(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("y", C.c_void_p), ("n_heads", C.c_int), ("x_stride", C.c_int64),
+                ("y_stride", C.c_int64)]
+
+
+class moe_kv_config_t(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("n_q_heads", "n_kv_heads", "head_dim", "page_size", "n_pages", "max_seqs",
+                                       "max_tokens", "max_kv_len")]
+
+
+class moe_kv_store_t(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("k", "v", "k_scale", "v_scale")]
+
+
+class moe_kv_batch_t(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("n_seqs", "n_tokens", "max_q_len", "max_kv_len", "table_stride")] + \
+               [(n, C.c_void_p) for n in ("cu_q", "kv_len", "page_table")]
+
+
+class moe_kv_mask_t(C.Structure):
+    _fields_ = [("scale", C.c_float), ("causal", C.c_int), ("window", C.c_int), ("sinks", C.c_int)]
+
+
+EXPORTED = ("moe_rope_create", "moe_rope_apply", "moe_rope_destroy", "moe_kv_create", "moe_kv_workspace_bytes",
+            "moe_kv_last_error", "moe_kv_destroy", "moe_kv_write", "moe_kv_read", "moe_kv_attend",
+            "moe_kv_device_status")
+
+# bits of moe_kv_device_status
+KV_WAIT_GAVE_UP, KV_BAD_BATCH, KV_NON_FINITE = 1, 2, 4
+
+_lib = None
+
+
+def _load() -> C.CDLL:
+    global _lib
+    if _lib is not None:
+        return _lib
+    L = moe.load()
+    vp, i32, i64 = C.c_void_p, C.c_int, C.c_int64
+    sig = {
+        "moe_rope_create": (i32, [i32, C.POINTER(C.c_double), C.c_float, i32, C.POINTER(vp)]),
+        "moe_rope_apply": (i32, [vp, C.POINTER(moe_rope_tensor_t), C.POINTER(moe_rope_tensor_t), i32, i32, vp, i32, vp]),
+        "moe_rope_destroy": (None, [vp]),
+        "moe_kv_create": (i32, [C.POINTER(moe_kv_config_t), C.POINTER(moe_kv_store_t), C.POINTER(vp)]),
+        "moe_kv_workspace_bytes": (C.c_size_t, [C.POINTER(moe_kv_config_t)]),
+        "moe_kv_last_error": (C.c_char_p, [vp]),
+        "moe_kv_destroy": (None, [vp]),
+        "moe_kv_write": (i32, [vp, vp, i64, vp, i64, i32, C.POINTER(moe_kv_batch_t), vp]),
+        "moe_kv_read": (i32, [vp, vp, vp, i32, C.POINTER(moe_kv_batch_t), vp]),
+        "moe_kv_attend": (i32, [vp, vp, i64, vp, vp, C.POINTER(moe_kv_mask_t), C.POINTER(moe_kv_batch_t), vp]),
+        "moe_kv_device_status": (i32, [vp, C.POINTER(C.c_int32)]),
+    }
+    for name, (res, args) in sig.items():
+        fn = getattr(L, name)
+        fn.restype, fn.argtypes = res, args
+    _lib = L
+    return L
+
+
+def _dtype(t, name: str) -> int:
+    import torch
+    if t == torch.bfloat16:
+        return MOE_BF16
+    if t == torch.float32:
+        return MOE_F32
+    raise TypeError(f"{name} must be fp32 or bf16, got {t}")
+
+
+def _stream(stream) -> int:
+    import torch
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _rows(x, name: str, heads: int, dim: int, device) -> int:
+    """Checks a [tokens][heads][dim] (or [tokens][heads * dim]) CUDA tensor whose tokens may be strided and
+    whose rows are whole; returns the elements between tokens."""
+    if x.device != device:
+        raise ValueError(f"{name} must be on {device}, got {x.device}")
+    ok = (x.dim() == 3 and x.shape[1] == heads and x.shape[2] == dim and x.stride(2) == 1
+          and (heads == 1 or x.stride(1) == dim)) or \
+         (x.dim() == 2 and x.shape[1] == heads * dim and x.stride(1) == 1)
+    if not ok:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}] with contiguous rows, got {tuple(x.shape)} "
+                         f"with strides {x.stride()}")
+    return x.stride(0) if x.shape[0] > 1 else heads * dim
+
+
+def rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """Radians per position of each of rot_dim / 2 pairs, and the amplitude of their sine and cosine.
+      None      theta^(-2i / rot_dim)
+      "linear"  divided by factor (position interpolation)
+      "ntk"     theta raised to theta * factor^(rot_dim / (rot_dim - 2))
+      "yarn"    pairs that make more than beta_fast turns over original_len keep their frequency, those below
+                beta_slow are divided by factor, a ramp between; amplitude 0.1 ln(factor) + 1
+    """
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
+    if not theta > 1 or not factor >= 1:
+        raise ValueError("theta must be above 1 and factor at least 1")
+    half = rot_dim // 2
+    base = theta * factor ** (rot_dim / (rot_dim - 2)) if scaling == "ntk" else theta
+    f = [base ** (-2.0 * i / rot_dim) for i in range(half)]
+    if scaling == "linear":
+        return [x / factor for x in f], 1.0
+    if scaling != "yarn":
+        return f, 1.0
+    if original_len < 1:
+        raise ValueError("yarn needs original_len")
+
+    def pair_of(turns: float) -> float:
+        return rot_dim * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(theta))
+
+    low, high = max(math.floor(pair_of(beta_fast)), 0), min(math.ceil(pair_of(beta_slow)), rot_dim - 1)
+    ramp = [min(max((i - low) / max(high - low, 1e-3), 0.0), 1.0) for i in range(half)]
+    return [x * (1 - r) + x / factor * r for x, r in zip(f, ramp)], 0.1 * math.log(factor) + 1.0
+
+
+class Rope:
+    """Rotary positions (moe_rope_*).  Frequencies by rope_frequencies, or given (radians per position)."""
+
+    def __init__(self, rot_dim: int, theta: float = 10000.0, interleaved: bool = False, scaling: str | None = None,
+                 factor: float = 1.0, original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 inv_freq=None, amplitude: float | None = None):
+        self.h = None
+        if inv_freq is None:
+            inv_freq, amp = rope_frequencies(rot_dim, theta, scaling, factor, original_len, beta_fast, beta_slow)
+        else:
+            inv_freq, amp = [float(x) for x in inv_freq], 1.0
+        if len(inv_freq) != rot_dim // 2:
+            raise ValueError(f"inv_freq must have {rot_dim // 2} entries, got {len(inv_freq)}")
+        self.rot_dim, self.interleaved = rot_dim, interleaved
+        self.inv_freq, self.amplitude = inv_freq, amp if amplitude is None else amplitude
+        h = C.c_void_p()
+        st = _load().moe_rope_create(rot_dim, (C.c_double * max(1, len(inv_freq)))(*inv_freq), self.amplitude,
+                                     1 if interleaved else 0, C.byref(h))
+        if st != MOE_OK:
+            raise MoeError(st, moe.moe_last_error(None))
+        self.h = h
+
+    def apply(self, q, positions, k=None, q_out=None, k_out=None, stream=None):
+        """Rotates q [tokens, heads, head_dim] (and k) at positions [tokens] int32; returns q's result, or
+        (q's, k's) when k is given.  Tokens may be strided (parts of one projection); q_out is q rotates in
+        place."""
+        import torch
+        if q.dim() != 3 or not q.is_cuda:
+            raise ValueError(f"q must be a CUDA tensor [tokens, heads, head_dim], got {tuple(q.shape)} on {q.device}")
+        T, _, D = q.shape
+        dt = _dtype(q.dtype, "q")
+        if positions.device != q.device or positions.dtype != torch.int32 or positions.shape != (T,) \
+                or not positions.is_contiguous():
+            raise ValueError(f"positions must be a contiguous int32 tensor of {T} entries on {q.device}")
+        ts, outs = [], []
+        for name, x, y in (("q", q, q_out), ("k", k, k_out)):
+            if x is None:
+                if y is not None:
+                    raise ValueError("k_out needs k")
+                continue
+            if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D or x.dtype != q.dtype:
+                raise ValueError(f"{name} must be [{T}, heads, {D}] of {q.dtype}")
+            xs = _rows(x, name, x.shape[1], D, q.device)
+            if y is None:
+                y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            elif y.shape != x.shape or y.dtype != x.dtype:
+                raise ValueError(f"{name}_out must be {tuple(x.shape)} of {x.dtype}")
+            ys = _rows(y, name + "_out", x.shape[1], D, q.device)
+            ts.append(moe_rope_tensor_t(x.data_ptr(), y.data_ptr(), x.shape[1], xs, ys))
+            outs.append(y)
+        if T:
+            st = _load().moe_rope_apply(self.h, C.byref(ts[0]), C.byref(ts[1]) if len(ts) > 1 else None, D, dt,
+                                        positions.data_ptr(), T, _stream(stream))
+            if st != MOE_OK:
+                raise MoeError(st, moe.moe_last_error(None))
+        return outs[0] if k is None else tuple(outs)
+
+    def close(self):
+        if self.h:
+            _load().moe_rope_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class SeqBatch:
+    """The tokens of one call: sequence b has kv_len[b] cached tokens, the last cu_q[b + 1] - cu_q[b] of them are
+    the call's (rows cu_q[b] onwards), token t lies in page page_table[b][t // page_size].  The three int32
+    tensors stay on the device and may change between calls (also between replays of a captured graph) within
+    the host's bounds: n_tokens rows, max_q_len new and max_kv_len cached tokens of any sequence."""
+
+    def __init__(self, cu_q, kv_len, page_table, n_tokens: int, max_q_len: int, max_kv_len: int):
+        import torch
+        for name, t, dims in (("cu_q", cu_q, 1), ("kv_len", kv_len, 1), ("page_table", page_table, 2)):
+            if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous() or t.device != cu_q.device:
+                raise ValueError(f"{name} must be a contiguous {dims}-D int32 tensor on {cu_q.device}")
+        n = kv_len.shape[0]
+        if cu_q.shape[0] != n + 1 or page_table.shape[0] != n:
+            raise ValueError(f"{n} sequences need cu_q of {n + 1} entries and page_table of {n} rows")
+        self.cu_q, self.kv_len, self.page_table = cu_q, kv_len, page_table
+        self.n_tokens, self.device = n_tokens, cu_q.device
+        self.c = moe_kv_batch_t(n, n_tokens, max_q_len, max_kv_len, page_table.shape[1], cu_q.data_ptr(),
+                                kv_len.data_ptr(), page_table.data_ptr())
+
+
+class KVCache:
+    """The 8-bit paged cache (moe_kv_*): wraps codes [pages, kv heads, page_size, head_dim] (torch.float8_e4m3fn
+    or uint8) and scales [pages, kv heads] fp32 of keys and values; ``KVCache.empty`` allocates them."""
+
+    def __init__(self, k_codes, v_codes, k_scale, v_scale, n_q_heads: int, max_seqs: int, max_tokens: int,
+                 max_kv_len: int):
+        import torch
+        self.h = None
+        if k_codes.dim() != 4:
+            raise ValueError("codes must be [pages, kv heads, page_size, head_dim]")
+        P, H, S, D = k_codes.shape
+        for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
+            if t.shape != k_codes.shape or t.dtype not in (torch.uint8, torch.float8_e4m3fn) or not t.is_contiguous() \
+                    or not t.is_cuda or t.device != k_codes.device:
+                raise ValueError(f"{name} must be a contiguous uint8 or float8_e4m3fn CUDA tensor {(P, H, S, D)}")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t.shape != (P, H) or t.dtype != torch.float32 or not t.is_contiguous() or t.device != k_codes.device:
+                raise ValueError(f"{name} must be a contiguous fp32 tensor {(P, H)} on {k_codes.device}")
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size = n_q_heads, H, D, S
+        self.device = k_codes.device
+        self.default_scale = D ** -0.5
+        cfg = moe_kv_config_t(n_q_heads, H, D, S, P, max_seqs, max_tokens, max_kv_len)
+        store = moe_kv_store_t(*(t.data_ptr() for t in (k_codes, v_codes, k_scale, v_scale)))
+        h = C.c_void_p()
+        with torch.cuda.device(self.device):
+            st = _load().moe_kv_create(C.byref(cfg), C.byref(store), C.byref(h))
+        if st != MOE_OK:
+            raise MoeError(st, moe.moe_last_error(None))
+        self.h = h
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, n_q_heads: int, max_seqs: int,
+              max_tokens: int, max_kv_len: int, device="cuda"):
+        import torch
+        shape = (n_pages, n_kv_heads, page_size, head_dim)
+        codes = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2)]
+        scales = [torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*codes, *scales, n_q_heads, max_seqs, max_tokens, max_kv_len)
+
+    def _check(self, st):
+        if st != MOE_OK:
+            raise MoeError(st, (_load().moe_kv_last_error(self.h) or b"").decode())
+
+    def _batch(self, batch):
+        if batch.device != self.device:
+            raise ValueError(f"the batch must be on {self.device}, got {batch.device}")
+        return C.byref(batch.c)
+
+    def _tokens(self, x, name, heads, batch):
+        s = _rows(x, name, heads, self.head_dim, self.device)
+        if x.shape[0] != batch.n_tokens:
+            raise ValueError(f"{name} must have the batch's {batch.n_tokens} tokens, got {x.shape[0]}")
+        return s
+
+    def write(self, k, v, batch: SeqBatch, stream=None) -> None:
+        """Quantises the batch's new keys and values [tokens, kv heads, head_dim] into their pages."""
+        ks = self._tokens(k, "k", self.n_kv_heads, batch)
+        vs = self._tokens(v, "v", self.n_kv_heads, batch)
+        if k.dtype != v.dtype:
+            raise TypeError("k and v must have one dtype")
+        self._check(_load().moe_kv_write(self.h, k.data_ptr(), ks, v.data_ptr(), vs, _dtype(k.dtype, "k"),
+                                         self._batch(batch), _stream(stream)))
+
+    def read(self, batch: SeqBatch, dtype=None, k_out=None, v_out=None, stream=None):
+        """The batch's new tokens as values: (keys, values) [tokens, kv heads, head_dim] (bf16 by default)."""
+        import torch
+        shape = (batch.n_tokens, self.n_kv_heads, self.head_dim)
+        dtype = dtype or (k_out.dtype if k_out is not None else torch.bfloat16)
+        code = _dtype(dtype, "dtype")
+        outs = []
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is None:
+                t = torch.empty(shape, dtype=dtype, device=self.device)
+            elif t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.device != self.device:
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {self.device}")
+            outs.append(t)
+        self._check(_load().moe_kv_read(self.h, outs[0].data_ptr(), outs[1].data_ptr(), code, self._batch(batch),
+                                        _stream(stream)))
+        return outs[0], outs[1]
+
+    def attend(self, q, batch: SeqBatch, out=None, lse=None, scale: float | None = None, causal: bool = True,
+               window: int = 0, sinks: int = 0, stream=None):
+        """Attention of the batch's new tokens q [tokens, q heads, head_dim] bf16 over their sequences' cached
+        tokens (write the new ones first).  window > 0: a token sees the last ``window`` tokens, itself
+        included, and the first ``sinks`` ones.  Returns out [tokens, q heads, head_dim] bf16; lse, when given,
+        is filled with the natural logarithms of the softmax denominators [tokens, q heads] fp32."""
+        import torch
+        qs = self._tokens(q, "q", self.n_q_heads, batch)
+        if q.dtype != torch.bfloat16:
+            raise TypeError(f"q must be bf16, got {q.dtype}")
+        shape = (batch.n_tokens, self.n_q_heads, self.head_dim)
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        elif out.numel() != batch.n_tokens * self.n_q_heads * self.head_dim or out.dtype != torch.bfloat16 \
+                or not out.is_contiguous() or out.device != self.device:
+            raise ValueError(f"out must be a contiguous bf16 tensor {shape} on {self.device}")
+        if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()
+                                or lse.device != self.device):
+            raise ValueError(f"lse must be a contiguous fp32 tensor {shape[:2]} on {self.device}")
+        mask = moe_kv_mask_t(self.default_scale if scale is None else scale, 1 if causal else 0, window, sinks)
+        self._check(_load().moe_kv_attend(self.h, q.data_ptr(), qs, out.data_ptr(),
+                                          lse.data_ptr() if lse is not None else None, C.byref(mask),
+                                          self._batch(batch), _stream(stream)))
+        return out
+
+    def device_status(self) -> int:
+        """Device error word (0 = fine; synchronous, clears it); raises MoeError when it is set."""
+        f = C.c_int32(0)
+        self._check(_load().moe_kv_device_status(self.h, C.byref(f)))
+        return f.value
+
+    def close(self):
+        if self.h:
+            _load().moe_kv_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
