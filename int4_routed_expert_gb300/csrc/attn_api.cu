@@ -84,9 +84,10 @@ const char* check_kv_config(const moe_kv_config_t* c) {
   return nullptr;
 }
 
-// Rows of partial results: 2^16 are four rounds of two CTAs of 16 rows a SM
-// twice over; the splits of a call are limited to what fits.
-constexpr size_t kPartRows = 1u << 16;
+// Rows of partial results: 2^17 hold two CTAs of 256 rows a SM and more than
+// eight rounds of two CTAs of 16 rows; the splits of a call are limited to
+// what fits.
+constexpr size_t kPartRows = 1u << 17;
 
 struct KvLayout {
   size_t o, ml, count, err, total;
@@ -458,7 +459,9 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
   a.sinks = a.window ? mask->sinks : 0;
   a.hq = h->cfg.n_q_heads;
   a.G = h->cfg.n_q_heads / h->cfg.n_kv_heads;
-  return launched(h, moe::attn_rows_launch(c, a, h->ws, h->n_sm, static_cast<cudaStream_t>(stream)),
+  const bool tiles = static_cast<int64_t>(c.max_q) * a.G >= 128;
+  return launched(h, (tiles ? moe::attn_tiles_launch : moe::attn_rows_launch)(
+                         c, a, h->ws, h->n_sm, static_cast<cudaStream_t>(stream)),
                   "moe_kv_attend");
 }
 

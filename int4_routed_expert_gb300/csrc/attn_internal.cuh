@@ -87,4 +87,7 @@ cudaError_t kv_read_launch(const KvView& c, void* k, void* v, moe_dtype_t dt, cu
 cudaError_t attn_rows_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, int n_sm,
                              cudaStream_t s);
 
+cudaError_t attn_tiles_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, int n_sm,
+                              cudaStream_t s);
+
 }  // namespace moe

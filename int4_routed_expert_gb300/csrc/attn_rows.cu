@@ -26,7 +26,7 @@
 // Bound by memory: 2 D bytes a key and kv head, 16 rows share them.
 #include <climits>
 
-#include "attn_internal.cuh"
+#include "attn_common.cuh"
 #include "smem_opt_in.cuh"
 #include "stream_common.cuh"
 
@@ -37,9 +37,6 @@ constexpr int kRows = 16;    // rows of a CTA (one m16 fragment)
 constexpr int kTile = 32;    // keys of a warp's tile
 constexpr int kWarps = 4;
 constexpr int kStages = 3;
-// Weights are taken relative to 2^-kLift of the row's reference, which moves when it would grow by more than
-// 2^kRescale: f16 weights lie below 2^15 and keep all their bits down to 2^-24 of the largest.
-constexpr float kLift = 10.f, kRescale = 5.f;
 
 template <int D>
 struct Lay {
@@ -86,16 +83,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                : "memory");
 }
 
-// Two e4m3 codes (low half word) as f16x2, exactly.
-__device__ __forceinline__ void codes_to_half(uint32_t four, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 l, h;\n\t"
-      "mov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(four));
-}
-
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
   asm volatile(
@@ -103,24 +90,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// 2^(14 - floor(log2 amax)), the power of two that brings a query row to
-// [2^14, 2^15); rows below 2^-87 keep that of 2^-87.
-__device__ __forceinline__ float row_factor(float amax) {
-  const int e = max(static_cast<int>(__float_as_uint(amax) >> 23), 40);
-  return __uint_as_float(static_cast<uint32_t>(min(127 + 14 + 127 - e, 254)) << 23);
 }
 
 struct Plan {
@@ -148,13 +117,8 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int r1 = min(R, r0 + kRows);
   const int base_p = q.L - q.n;
   const int p0 = base_p + r0 / a.G, p1 = base_p + (r1 - 1) / a.G;
-  // the tiles of keys that some row sees: those of the sinks, then those from
-  // the window's start to hi
-  const int hi = a.causal ? max(p1 + 1, 0) : q.L;
-  const int lo = a.window ? max(p0 - a.window + 1, 0) : 0;
-  int n_a = (min(a.sinks, hi) + kTile - 1) / kTile, t_b = lo / kTile;
-  if (t_b <= n_a) n_a = t_b = 0;
-  const int n_t = n_a + max((hi + kTile - 1) / kTile - t_b, 0);
+  const KeyTiles kt_ = key_tiles<kTile>(a, q.L, p0, p1);
+  const int hi = kt_.hi, lo = kt_.lo, n_t = kt_.n_t;
   const int n_split = max((n_t + pl.tiles_per_split - 1) / pl.tiles_per_split, 1);
   if (split >= n_split) return;
   const int tile_end = min(n_t, (split + 1) * pl.tiles_per_split);
@@ -162,7 +126,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 
   char* ring = smem + warp * L_::kWarpBytes;
   const uint32_t ring_u = smem_u32(ring);
-  auto tile_base = [&](int t) { return (t < n_a ? t : t_b + t - n_a) * kTile; };
+  auto tile_base = [&](int t) { return kt_.base(t); };
   // page ids of the next tile to load, read one tile ahead
   int pg0 = -1, pg1 = -1;
   auto next_pages = [&](int t) {
@@ -210,13 +174,13 @@ __global__ void __launch_bounds__(kWarps * 32)
   // the query fragments of rows g and g + 8: chunk x holds dims 16 x + 4 i4 ..
   uint32_t qa[C][4];
   float lscale[2];  // logit scale of the row, its power of two undone
-  int rp[2];        // the rows' positions
+  RowSees see[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int r = r0 + g + 8 * h;
     const bool ok = r < r1;
     const int tok = ok ? r / a.G : 0;
-    rp[h] = ok ? base_p + tok : INT_MIN;
+    see[h] = row_sees(a, q.L, base_p + tok, ok);
     const __nv_bfloat16* src = a.q + (static_cast<int64_t>(q.q0) + tok) * a.q_stride +
                                (static_cast<int64_t>(hk) * a.G + (ok ? r - tok * a.G : 0)) * D + 4 * i4;
     uint2 raw[C];
@@ -292,9 +256,7 @@ __global__ void __launch_bounds__(kWarps * 32)
         float x = fmaf(s[j][k], lscale[h] * ks, lv[j >> 1]);
         if (!whole) {
           const int tok = base + 8 * j + 2 * i4 + (k & 1);
-          const bool sees = a.causal ? tok <= rp[h] && (a.window == 0 || tok > rp[h] - a.window ||
-                                                        tok < a.sinks)
-                                     : tok < q.L;
+          const bool sees = see[h](tok);
           x = sees ? x : -INFINITY;
         }
         s[j][k] = x;
@@ -378,15 +340,9 @@ __global__ void __launch_bounds__(kWarps * 32)
 
   const size_t tile_id = (static_cast<size_t>(b) * c.hkv + hk) * pl.row_tiles + rt;
   const size_t prow = (tile_id * pl.splits + split) * kRows;
-  auto finish = [&](int r, int d4, const float4& v, float mm, float ll) {
-    const int tok = (r0 + r) / a.G, head = hk * a.G + (r0 + r) % a.G;
-    const size_t row = (static_cast<size_t>(q.q0) + tok) * a.hq + head;
-    const float f = ll > 0.f || ll != ll ? 1.f / ll : 0.f;
-    const __nv_bfloat162 x0 = __floats2bfloat162_rn(v.x * f, v.y * f);
-    const __nv_bfloat162 x1 = __floats2bfloat162_rn(v.z * f, v.w * f);
-    *reinterpret_cast<uint2*>(a.out + row * D + 4 * d4) = make_uint2(
-        *reinterpret_cast<const uint32_t*>(&x0), *reinterpret_cast<const uint32_t*>(&x1));
-    if (a.lse && d4 == 0) a.lse[row] = ll > 0.f || ll != ll ? (mm - kLift + log2f(ll)) * 0.693147180559945f : -INFINITY;
+  auto out_row = [&](int r) {
+    const int tok = (r0 + r) / a.G;
+    return (static_cast<size_t>(q.q0) + tok) * a.hq + hk * a.G + (r0 + r) - tok * a.G;
   };
   for (int e = threadIdx.x; e < (r1 - r0) * (D / 4); e += kWarps * 32) {
     const int r = e / (D / 4), d4 = e % (D / 4);
@@ -407,7 +363,7 @@ __global__ void __launch_bounds__(kWarps * 32)
       v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
     }
     if (n_split == 1) {
-      finish(r, d4, v, mm, ll);
+      finish_row<D>(a, out_row(r), d4, v, mm, ll);
     } else {
       *reinterpret_cast<float4*>(ws.o + (prow + r) * D + 4 * d4) = v;
       if (d4 == 0) ws.ml[prow + r] = make_float2(mm, ll);
@@ -429,20 +385,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   const size_t first = tile_id * pl.splits * kRows;
   for (int e = threadIdx.x; e < (r1 - r0) * (D / 4); e += kWarps * 32) {
     const int r = e / (D / 4), d4 = e % (D / 4);
-    float mm = -INFINITY;
-    for (int s = 0; s < n_split; ++s) mm = fmaxf(mm, __ldcg(&ws.ml[first + s * kRows + r]).x);
-    const float ref = mm == -INFINITY ? 0.f : mm;
-    float ll = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < n_split; ++s) {
-      const float2 x = __ldcg(&ws.ml[first + s * kRows + r]);
-      const float f = ex2(x.x - ref);
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(ws.o + (first + s * kRows + r) * D + 4 * d4));
-      ll = fmaf(x.y, f, ll);
-      v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y);
-      v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
-    }
-    finish(r, d4, v, mm, ll);
+    join_row<D>(a, ws, first + r, kRows, n_split, out_row(r), d4);
   }
 }
 
@@ -455,10 +398,7 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, int n_s
   const int64_t rows = static_cast<int64_t>(c.max_q) * a.G;
   pl.row_tiles = static_cast<int>((rows + kRows - 1) / kRows);
   const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
-  // tiles of the keys that a row tile can see
-  int64_t keys = c.max_kv;
-  if (a.window) keys = std::min<int64_t>(keys, static_cast<int64_t>(a.window) + kRows + a.sinks + 3 * kTile);
-  const int64_t tiles = std::max<int64_t>((keys + kTile - 1) / kTile, 1);
+  const int64_t tiles = max_key_tiles(c, a, kRows, kTile);
   // enough CTAs for four rounds of two a SM (ragged lengths), at least two
   // tiles a warp, and no more partial rows than the workspace has
   int64_t splits = (8LL * n_sm + base - 1) / base;
