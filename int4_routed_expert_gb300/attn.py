@@ -47,12 +47,16 @@ EXPORTED = ("moe_rope_create", "moe_rope_apply", "moe_rope_destroy", "moe_kv_cre
 KV_WAIT_GAVE_UP, KV_BAD_BATCH, KV_NON_FINITE = 1, 2, 4
 
 _lib = None
+torch = None    # imported with the library: a call costs a few microseconds, and a module lookup is part of it
+_codes = {}     # torch dtype -> moe_dtype_t
+_raw_stream = None
 
 
 def _load() -> C.CDLL:
-    global _lib
+    global _lib, torch, _raw_stream
     if _lib is not None:
         return _lib
+    import torch as _torch
     L = moe.load()
     vp, i32, i64 = C.c_void_p, C.c_int, C.c_int64
     sig = {
@@ -71,36 +75,38 @@ def _load() -> C.CDLL:
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
         fn.restype, fn.argtypes = res, args
+    torch = _torch
+    _codes.update({torch.bfloat16: MOE_BF16, torch.float32: MOE_F32})
+    # the stream's handle alone; torch.cuda.current_stream() builds an object, 3 us
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda index: torch.cuda.current_stream(index).cuda_stream)
     _lib = L
     return L
 
 
 def _dtype(t, name: str) -> int:
-    import torch
-    if t == torch.bfloat16:
-        return MOE_BF16
-    if t == torch.float32:
-        return MOE_F32
-    raise TypeError(f"{name} must be fp32 or bf16, got {t}")
+    code = _codes.get(t)
+    if code is None:
+        raise TypeError(f"{name} must be fp32 or bf16, got {t}")
+    return code
 
 
-def _stream(stream) -> int:
-    import torch
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+def _stream(stream, device) -> int:
+    return _raw_stream(device.index) if stream is None else stream.cuda_stream
 
 
 def _rows(x, name: str, heads: int, dim: int, device) -> int:
     """Checks a [tokens][heads][dim] (or [tokens][heads * dim]) CUDA tensor whose tokens may be strided and
     whose rows are whole; returns the elements between tokens."""
-    if x.device != device:
-        raise ValueError(f"{name} must be on {device}, got {x.device}")
-    ok = (x.dim() == 3 and x.shape[1] == heads and x.shape[2] == dim and x.stride(2) == 1
-          and (heads == 1 or x.stride(1) == dim)) or \
-         (x.dim() == 2 and x.shape[1] == heads * dim and x.stride(1) == 1)
-    if not ok:
-        raise ValueError(f"{name} must be [tokens, {heads}, {dim}] with contiguous rows, got {tuple(x.shape)} "
-                         f"with strides {x.stride()}")
-    return x.stride(0) if x.shape[0] > 1 else heads * dim
+    shape, stride = x.shape, x.stride()
+    if len(shape) == 3:
+        ok = shape[1] == heads and shape[2] == dim and stride[2] == 1 and (heads == 1 or stride[1] == dim)
+    else:
+        ok = len(shape) == 2 and shape[1] == heads * dim and stride[1] == 1
+    if not ok or x.device != device:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}] on {device} with contiguous rows, got "
+                         f"{tuple(shape)} with strides {stride} on {x.device}")
+    return stride[0] if shape[0] > 1 else heads * dim
 
 
 def rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -160,36 +166,42 @@ class Rope:
         """Rotates q [tokens, heads, head_dim] (and k) at positions [tokens] int32; returns q's result, or
         (q's, k's) when k is given.  Tokens may be strided (parts of one projection); q_out is q rotates in
         place."""
-        import torch
+        dev, dtype = q.device, q.dtype
         if q.dim() != 3 or not q.is_cuda:
-            raise ValueError(f"q must be a CUDA tensor [tokens, heads, head_dim], got {tuple(q.shape)} on {q.device}")
-        T, _, D = q.shape
-        dt = _dtype(q.dtype, "q")
-        if positions.device != q.device or positions.dtype != torch.int32 or positions.shape != (T,) \
-                or not positions.is_contiguous():
-            raise ValueError(f"positions must be a contiguous int32 tensor of {T} entries on {q.device}")
-        ts, outs = [], []
-        for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-            if x is None:
-                if y is not None:
-                    raise ValueError("k_out needs k")
-                continue
-            if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D or x.dtype != q.dtype:
-                raise ValueError(f"{name} must be [{T}, heads, {D}] of {q.dtype}")
-            xs = _rows(x, name, x.shape[1], D, q.device)
-            if y is None:
-                y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            elif y.shape != x.shape or y.dtype != x.dtype:
-                raise ValueError(f"{name}_out must be {tuple(x.shape)} of {x.dtype}")
-            ys = _rows(y, name + "_out", x.shape[1], D, q.device)
-            ts.append(moe_rope_tensor_t(x.data_ptr(), y.data_ptr(), x.shape[1], xs, ys))
-            outs.append(y)
+            raise ValueError(f"q must be a CUDA tensor [tokens, heads, head_dim], got {tuple(q.shape)} on {dev}")
+        T, H, D = q.shape
+        dt = _codes.get(dtype)
+        if dt is None:
+            raise TypeError(f"q must be fp32 or bf16, got {dtype}")
+        if positions.dtype != torch.int32 or positions.dim() != 1 or positions.shape[0] != T \
+                or positions.device != dev or not positions.is_contiguous():
+            raise ValueError(f"positions must be a contiguous int32 tensor of {T} entries on {dev}")
+        tq, q_out = self._pair("q", q, q_out, T, H, D, dtype, dev)
+        tk = None
+        if k is not None:
+            if k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or k.dtype != dtype:
+                raise ValueError(f"k must be [{T}, heads, {D}] of {dtype}")
+            tk, k_out = self._pair("k", k, k_out, T, k.shape[1], D, dtype, dev)
+        elif k_out is not None:
+            raise ValueError("k_out needs k")
         if T:
-            st = _load().moe_rope_apply(self.h, C.byref(ts[0]), C.byref(ts[1]) if len(ts) > 1 else None, D, dt,
-                                        positions.data_ptr(), T, _stream(stream))
+            st = _lib.moe_rope_apply(self.h, tq, tk, D, dt, positions.data_ptr(), T, _stream(stream, dev))
             if st != MOE_OK:
                 raise MoeError(st, moe.moe_last_error(None))
-        return outs[0] if k is None else tuple(outs)
+        return q_out if k is None else (q_out, k_out)
+
+    @staticmethod
+    def _pair(name, x, y, T, H, D, dtype, dev):
+        xs = ys = H * D
+        if not x.is_contiguous() or x.device != dev:
+            xs = _rows(x, name, H, D, dev)
+        if y is None:
+            y = torch.empty_like(x) if xs == ys else torch.empty((T, H, D), dtype=dtype, device=dev)
+        else:
+            if y.shape != x.shape or y.dtype != dtype:
+                raise ValueError(f"{name}_out must be {(T, H, D)} of {dtype}")
+            ys = _rows(y, name + "_out", H, D, dev)
+        return moe_rope_tensor_t(x.data_ptr(), y.data_ptr(), H, xs, ys), y
 
     def close(self):
         if self.h:
@@ -210,7 +222,7 @@ class SeqBatch:
     the host's bounds: n_tokens rows, max_q_len new and max_kv_len cached tokens of any sequence."""
 
     def __init__(self, cu_q, kv_len, page_table, n_tokens: int, max_q_len: int, max_kv_len: int):
-        import torch
+        _load()
         for name, t, dims in (("cu_q", cu_q, 1), ("kv_len", kv_len, 1), ("page_table", page_table, 2)):
             if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous() or t.device != cu_q.device:
                 raise ValueError(f"{name} must be a contiguous {dims}-D int32 tensor on {cu_q.device}")
@@ -229,8 +241,8 @@ class KVCache:
 
     def __init__(self, k_codes, v_codes, k_scale, v_scale, n_q_heads: int, max_seqs: int, max_tokens: int,
                  max_kv_len: int):
-        import torch
         self.h = None
+        _load()
         if k_codes.dim() != 4:
             raise ValueError("codes must be [pages, kv heads, page_size, head_dim]")
         P, H, S, D = k_codes.shape
@@ -257,7 +269,7 @@ class KVCache:
     @classmethod
     def empty(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, n_q_heads: int, max_seqs: int,
               max_tokens: int, max_kv_len: int, device="cuda"):
-        import torch
+        _load()
         shape = (n_pages, n_kv_heads, page_size, head_dim)
         codes = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2)]
         scales = [torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2)]
@@ -265,17 +277,13 @@ class KVCache:
 
     def _check(self, st):
         if st != MOE_OK:
-            raise MoeError(st, (_load().moe_kv_last_error(self.h) or b"").decode())
-
-    def _batch(self, batch):
-        if batch.device != self.device:
-            raise ValueError(f"the batch must be on {self.device}, got {batch.device}")
-        return C.byref(batch.c)
+            raise MoeError(st, (_lib.moe_kv_last_error(self.h) or b"").decode())
 
     def _tokens(self, x, name, heads, batch):
         s = _rows(x, name, heads, self.head_dim, self.device)
-        if x.shape[0] != batch.n_tokens:
-            raise ValueError(f"{name} must have the batch's {batch.n_tokens} tokens, got {x.shape[0]}")
+        if x.shape[0] != batch.n_tokens or batch.device != self.device:
+            raise ValueError(f"{name} and the batch must have the same tokens and device, got {x.shape[0]} on "
+                             f"{self.device} and {batch.n_tokens} on {batch.device}")
         return s
 
     def write(self, k, v, batch: SeqBatch, stream=None) -> None:
@@ -284,25 +292,26 @@ class KVCache:
         vs = self._tokens(v, "v", self.n_kv_heads, batch)
         if k.dtype != v.dtype:
             raise TypeError("k and v must have one dtype")
-        self._check(_load().moe_kv_write(self.h, k.data_ptr(), ks, v.data_ptr(), vs, _dtype(k.dtype, "k"),
-                                         self._batch(batch), _stream(stream)))
+        self._check(_lib.moe_kv_write(self.h, k.data_ptr(), ks, v.data_ptr(), vs, _dtype(k.dtype, "k"), batch.c,
+                                      _stream(stream, self.device)))
 
     def read(self, batch: SeqBatch, dtype=None, k_out=None, v_out=None, stream=None):
         """The batch's new tokens as values: (keys, values) [tokens, kv heads, head_dim] (bf16 by default)."""
-        import torch
-        shape = (batch.n_tokens, self.n_kv_heads, self.head_dim)
-        dtype = dtype or (k_out.dtype if k_out is not None else torch.bfloat16)
+        shape, dev = (batch.n_tokens, self.n_kv_heads, self.head_dim), self.device
+        if dtype is None:
+            dtype = k_out.dtype if k_out is not None else torch.bfloat16
         code = _dtype(dtype, "dtype")
-        outs = []
+        if batch.device != dev:
+            raise ValueError(f"the batch must be on {dev}, got {batch.device}")
         for name, t in (("k_out", k_out), ("v_out", v_out)):
-            if t is None:
-                t = torch.empty(shape, dtype=dtype, device=self.device)
-            elif t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.device != self.device:
-                raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {self.device}")
-            outs.append(t)
-        self._check(_load().moe_kv_read(self.h, outs[0].data_ptr(), outs[1].data_ptr(), code, self._batch(batch),
-                                        _stream(stream)))
-        return outs[0], outs[1]
+            if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.device != dev):
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {dev}")
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=dtype, device=dev)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=dtype, device=dev)
+        self._check(_lib.moe_kv_read(self.h, k_out.data_ptr(), v_out.data_ptr(), code, batch.c, _stream(stream, dev)))
+        return k_out, v_out
 
     def attend(self, q, batch: SeqBatch, out=None, lse=None, scale: float | None = None, causal: bool = True,
                window: int = 0, sinks: int = 0, stream=None):
@@ -310,23 +319,25 @@ class KVCache:
         tokens (write the new ones first).  window > 0: a token sees the last ``window`` tokens, itself
         included, and the first ``sinks`` ones.  Returns out [tokens, q heads, head_dim] bf16; lse, when given,
         is filled with the natural logarithms of the softmax denominators [tokens, q heads] fp32."""
-        import torch
-        qs = self._tokens(q, "q", self.n_q_heads, batch)
-        if q.dtype != torch.bfloat16:
+        dev, H = self.device, self.n_q_heads
+        qs = self._tokens(q, "q", H, batch)
+        bf16 = torch.bfloat16
+        if q.dtype != bf16:
             raise TypeError(f"q must be bf16, got {q.dtype}")
-        shape = (batch.n_tokens, self.n_q_heads, self.head_dim)
+        shape = (batch.n_tokens, H, self.head_dim)
         if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-        elif out.numel() != batch.n_tokens * self.n_q_heads * self.head_dim or out.dtype != torch.bfloat16 \
-                or not out.is_contiguous() or out.device != self.device:
-            raise ValueError(f"out must be a contiguous bf16 tensor {shape} on {self.device}")
+            out = torch.empty_like(q) if q.is_contiguous() and q.dim() == 3 else \
+                torch.empty(shape, dtype=bf16, device=dev)
+        elif out.numel() != shape[0] * shape[1] * shape[2] or out.dtype != bf16 or not out.is_contiguous() \
+                or out.device != dev:
+            raise ValueError(f"out must be a contiguous bf16 tensor {shape} on {dev}")
         if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()
-                                or lse.device != self.device):
-            raise ValueError(f"lse must be a contiguous fp32 tensor {shape[:2]} on {self.device}")
+                                or lse.device != dev):
+            raise ValueError(f"lse must be a contiguous fp32 tensor {shape[:2]} on {dev}")
         mask = moe_kv_mask_t(self.default_scale if scale is None else scale, 1 if causal else 0, window, sinks)
-        self._check(_load().moe_kv_attend(self.h, q.data_ptr(), qs, out.data_ptr(),
-                                          lse.data_ptr() if lse is not None else None, C.byref(mask),
-                                          self._batch(batch), _stream(stream)))
+        self._check(_lib.moe_kv_attend(self.h, q.data_ptr(), qs, out.data_ptr(),
+                                       lse.data_ptr() if lse is not None else None, mask, batch.c,
+                                       _stream(stream, dev)))
         return out
 
     def device_status(self) -> int:

@@ -22,6 +22,7 @@ struct moe_kv {
   int device, n_sm;
   void* base;  // workspace
   moe::AttnWs ws;
+  moe::KvMaps maps;
   size_t count_bytes;
   int* err;  // device error word
   char msg[512];
@@ -174,6 +175,40 @@ moe_status_t launched(moe_kv_t* h, cudaError_t e, const char* what) {
 }
 
 }  // namespace
+
+namespace moe {
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
+                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                   CUtensorMapFloatOOBfill);
+
+bool kv_create_maps(const moe_kv_config_t& cfg, const moe_kv_store_t& st, KvMaps* m) {
+  void* p = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) !=
+          cudaSuccess ||
+      q != cudaDriverEntryPointSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  const EncodeTiledFn encode = reinterpret_cast<EncodeTiledFn>(p);
+  const cuuint64_t D = cfg.head_dim, rows = static_cast<cuuint64_t>(cfg.n_kv_heads) * cfg.page_size;
+  const cuuint64_t dims[3] = {D, rows, static_cast<cuuint64_t>(cfg.n_pages)};
+  const cuuint64_t strides[2] = {D, rows * D};
+  const cuuint32_t es[3] = {1, 1, 1};
+  auto make = [&](CUtensorMap* map, uint8_t* base, int box_rows) {
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(D), static_cast<cuuint32_t>(box_rows), 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, base, dims, strides, box, es,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const int small = cfg.page_size < 32 ? cfg.page_size : 32;
+  return make(&m->k_tile, st.k, cfg.page_size) && make(&m->k_rows, st.k, small) && make(&m->v_rows, st.v, small);
+}
+
+}  // namespace moe
 
 extern "C" {
 
@@ -359,6 +394,12 @@ moe_status_t moe_kv_create(const moe_kv_config_t* cfg, const moe_kv_store_t* sto
     delete h;
     return MOE_ERR_CUDA;
   }
+  if (!moe::kv_create_maps(h->cfg, h->st, &h->maps)) {
+    fail(nullptr, "the TMA maps of the store could not be made");
+    cudaFree(h->base);
+    delete h;
+    return MOE_ERR_CUDA;
+  }
   *out = h;
   return MOE_OK;
 }
@@ -460,8 +501,9 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
   a.hq = h->cfg.n_q_heads;
   a.G = h->cfg.n_q_heads / h->cfg.n_kv_heads;
   const bool tiles = static_cast<int64_t>(c.max_q) * a.G >= 128;
-  return launched(h, (tiles ? moe::attn_tiles_launch : moe::attn_rows_launch)(
-                         c, a, h->ws, h->n_sm, static_cast<cudaStream_t>(stream)),
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return launched(h, tiles ? moe::attn_tiles_launch(c, a, h->ws, h->maps, h->n_sm, s)
+                           : moe::attn_rows_launch(c, a, h->ws, h->n_sm, s),
                   "moe_kv_attend");
 }
 

@@ -78,11 +78,12 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 2^(14 - floor(log2 amax)), the power of two that brings a query row to
-// [2^14, 2^15); rows below 2^-87 keep that of 2^-87.
+// 2^(TOP - floor(log2 amax)), the power of two that brings a query row to
+// [2^TOP, 2^(TOP + 1)); rows below 2^-87 keep that of 2^-87.
+template <int TOP>
 __device__ __forceinline__ float row_factor(float amax) {
   const int e = max(static_cast<int>(__float_as_uint(amax) >> 23), 40);
-  return __uint_as_float(static_cast<uint32_t>(min(127 + 14 + 127 - e, 254)) << 23);
+  return __uint_as_float(static_cast<uint32_t>(min(127 + TOP + 127 - e, 254)) << 23);
 }
 
 // Row `row` of the output (and of lse): sums over sum of weights, both

@@ -1,6 +1,7 @@
 // Internal declarations of the attention-side operators (include/moe_attn.h).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -58,6 +59,17 @@ __device__ __forceinline__ int load_page(const KvView& c, int b, int i) {
   return -1;
 }
 
+// The same in two steps, so that a prefetched entry is looked at only when it
+// is used: the entry as it is, then its check.
+__device__ __forceinline__ int raw_page(const KvView& c, int b, int i) {
+  return __ldg(c.table + static_cast<size_t>(b) * c.table_stride + i);
+}
+__device__ __forceinline__ int checked_page(const KvView& c, int p, bool& bad) {
+  const bool ok = static_cast<unsigned>(p) < static_cast<unsigned>(c.n_pages);
+  bad |= !ok;
+  return ok ? p : -1;
+}
+
 // Workspace of attend: partial results of row tiles whose keys are split over
 // several CTAs, and the tiles' arrival counters (0 between calls: the last
 // CTA of a tile resets its counter).
@@ -87,7 +99,13 @@ cudaError_t kv_read_launch(const KvView& c, void* k, void* v, moe_dtype_t dt, cu
 cudaError_t attn_rows_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, int n_sm,
                              cudaStream_t s);
 
-cudaError_t attn_tiles_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, int n_sm,
-                              cudaStream_t s);
+// TMA maps of the code arrays as [n_pages][n_kv_heads * page_size][D] bytes:
+// boxes of one page of one head (k_tile), or of at most 32 of its tokens.
+struct KvMaps {
+  CUtensorMap k_tile, k_rows, v_rows;
+};
+bool kv_create_maps(const moe_kv_config_t& cfg, const moe_kv_store_t& st, KvMaps* m);
+cudaError_t attn_tiles_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const KvMaps& maps,
+                              int n_sm, cudaStream_t s);
 
 }  // namespace moe

@@ -127,18 +127,19 @@ __global__ void __launch_bounds__(kWarps * 32)
   char* ring = smem + warp * L_::kWarpBytes;
   const uint32_t ring_u = smem_u32(ring);
   auto tile_base = [&](int t) { return kt_.base(t); };
-  // page ids of the next tile to load, read one tile ahead
-  int pg0 = -1, pg1 = -1;
+  // table entries of the next tile to load, read one tile ahead
+  int raw0 = 0, raw1 = 0;
+  bool bad = false;
   auto next_pages = [&](int t) {
     if (t >= tile_end) return;
     const int base = tile_base(t);
-    pg0 = load_page(c, b, base >> c.page_log2);
-    pg1 = pg0;
-    if (c.page < kTile && base + 16 < hi) pg1 = load_page(c, b, (base + 16) >> c.page_log2);
+    raw0 = raw_page(c, b, base >> c.page_log2);
+    raw1 = c.page < kTile && base + 16 < hi ? raw_page(c, b, (base + 16) >> c.page_log2) : raw0;
   };
   auto issue = [&](int t, int stage) {
     if (t < tile_end) {
       const int base = tile_base(t);
+      const int pg0 = checked_page(c, raw0, bad), pg1 = checked_page(c, raw1, bad);
       const uint32_t dst = ring_u + stage * L_::kStageBytes;
       constexpr int kPer = 32 / C;  // rows a pass of the warp
       const int c16 = lane % C;
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const float f = row_factor(amax);
+    const float f = row_factor<14>(amax);
     lscale[h] = a.scale_log2 / f;
 #pragma unroll
     for (int x = 0; x < C; ++x) {
@@ -316,6 +317,8 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
     stage = stage == kStages - 1 ? 0 : stage + 1;
   }
+
+  if (bad) atomicOr(c.err, kErrBadBatch);
 
   // the warps' results, each relative to its own reference, meet in shared memory
   cp_wait<0>();

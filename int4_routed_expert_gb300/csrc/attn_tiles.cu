@@ -5,15 +5,20 @@
 // online softmax whose reference m moves only when it would grow by 2^5.
 //
 // One CTA takes 256 rows (a row is a query head of a token; the heads that
-// share a kv head are packed into the rows, so K and V are converted once for
-// all of them) as two M = 128 tiles, and walks over 128-key tiles:
-//   4 warps   e4m3 codes -> f16 (exact), global -> registers -> the 128-byte
-//             swizzled layout in shared memory; the next tile's codes are in
-//             flight in registers meanwhile
-//   1 thread  tcgen05.mma: S = Q K^T (both K-major, from shared memory), then
-//             O += P V (P from tensor memory, V as it lies, MN-major)
+// share a kv head are packed into the rows, so K and V are read once for all
+// of them) as two M = 128 tiles, and walks over 128-key tiles:
+//   1 warp    TMA: key codes into the swizzled operand layout (three stages),
+//             value codes as they lie (two stages), the blocks' scales
+//   4 warps   value codes -> f16 (exact) in the swizzled operand layout
+//   1 thread  tcgen05.mma: S = Q K^T in e4m3, then O += P V in f16 (P from
+//             tensor memory, V as it lies, MN-major)
 //   2 x 4     softmax warps, one group a M tile, a thread a row: S from tensor
 //             memory, weights back as f16 over S
+// Keys are multiplied as they are stored: a bf16 query (8 bits) is the sum of
+// two e4m3 numbers of 4 bits each, exact down to 2^-18 of the row's largest,
+// and e4m3 products run at twice the rate of f16 ones, so the two terms cost
+// what one f16 product would and no key is converted.  Values stay f16
+// operands: a weight of 11 bits would be three e4m3 terms.
 // The two M tiles take turns, so one's softmax runs under the other's products.
 // Tensor memory: S0, S1 (P in their first half), O0, O1: 512 columns.
 // Bound by the tensor pipe: 2 * 2 * 128 * 128 * D flops a tile and M tile.
@@ -33,31 +38,66 @@ constexpr int kM = 128;        // rows of an M tile
 constexpr int kRows = 2 * kM;  // rows of a CTA
 constexpr int kTile = 128;     // keys of a tile
 constexpr float kTiny = 1e-37f;  // keeps what is hidden at -inf where a block's scale is 0
-constexpr int kThreads = 416;  // 4 + 4 softmax warps, 4 conversion warps, 1 MMA warp
+constexpr int kThreads = 448;  // 4 + 4 softmax warps, 4 conversion warps, MMA warp, load warp
+constexpr int kKStages = 3;
 
 template <int D>
 struct Lay {
   static constexpr int kHalf = kTile * 128;        // 128 rows x 64 f16, swizzled
-  static constexpr int kMat = kHalf * (D / 64);    // one operand tile
-  static constexpr int kQ = 0;                     // two M tiles
-  static constexpr int kK = kQ + 2 * kMat;         // two stages
-  static constexpr int kV = kK + 2 * kMat;         // two stages
-  static constexpr int kConst = kV + 2 * kMat;     // [4][8] float4: scales of a tile's 16-key groups
+  static constexpr int kMat8 = kTile * D;          // an operand tile of codes
+  static constexpr int kMat = kHalf * (D / 64);    // an operand tile of f16
+  static constexpr int kQ = 0;                     // two M tiles of two terms
+  static constexpr int kK = kQ + 4 * kMat8;
+  static constexpr int kV = kK + kKStages * kMat8; // two stages of f16
+  static constexpr int kRaw = kV + 2 * kMat;       // two stages of value codes
+  static constexpr int kConst = kRaw + 2 * kMat8;  // [4][8] float4: scales of a tile's 16-key groups
   static constexpr int kBar = kConst + 4 * 8 * 16;
   static constexpr int kEnd = kBar + 32 * 8;
   static constexpr int kSmem = kEnd + 1024;        // the base is rounded up to 1024
 };
 
-enum Bar { kQFull = 0, kKFull = 1, kKEmpty = 3, kVFull = 5, kVEmpty = 7, kSFull = 9, kPFull = 11, kOFull = 13, kBars = 15 };
+enum Bar {
+  kQFull = 0,
+  kKFull = 1,    // [3] bytes + the scales' writers
+  kKEmpty = 4,   // [3]
+  kRFull = 7,    // [2] value codes
+  kREmpty = 9,   // [2]
+  kVFull = 11,   // [2] values
+  kVEmpty = 13,  // [2]
+  kSFull = 15,   // [2] by M tile
+  kPFull = 17,
+  kOFull = 19,
+  kBars = 21
+};
 
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
+// D[tmem] (+)= A[smem] * B[smem], e4m3 operands, f32 accumulator.
+__device__ __forceinline__ void mma_ss_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// K-major operand of D-byte rows in the D-byte swizzled layout (D = 64, 128):
+// 8-row atoms of 8 D bytes.
+template <int D>
+__device__ __forceinline__ uint64_t sdesc_k(uint32_t smem_addr) {
+  if constexpr (D == 128) return sdesc_sw128(smem_addr);
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(1u) << 16;
+  d |= static_cast<uint64_t>(512u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(4u) << 61;  // 64-byte swizzle
+  return d;
+}
+// Byte offset of 16-byte chunk c of row r in that layout.
+template <int D>
+__device__ __forceinline__ uint32_t k_off(int r, int c) {
+  return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
 // MN-major operand in the 128-byte swizzled layout: K rows of 128 bytes (64
@@ -97,6 +137,27 @@ __device__ __forceinline__ void tmem_wait_ld32(float* v) {
                : "memory");
 }
 
+// Two fp32 operations an instruction.
+__device__ __forceinline__ void fma2(float& x, float& y, float a0, float a1, float b, float c) {
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\tmov.b64 c, {%5, %5};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a0, float a1) {
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%0, %1};\n\t"
+      "add.rn.f32x2 b, b, a;\n\tmov.b64 {%0, %1}, b;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 struct Plan {
   int row_tiles, splits, tiles_per_split;
 };
@@ -125,72 +186,16 @@ __device__ __forceinline__ bool work_of(const KvView& c, const AttnArgs& a, cons
   return true;
 }
 
-// ---- conversion warps --------------------------------------------------------
-template <int D>
-struct Converter {
-  static constexpr int kChunks = D / 16;                 // 16-code chunks of a key
-  static constexpr int kPer = 128 / kChunks;             // keys a pass
-  static constexpr int kPasses = kTile / kPer;
-  int pid[kPasses] = {};  // pages of the thread's keys of the tile to load
-  int gpid = -1;          // page of 16-key group t (threads 0 .. 7)
-
-  __device__ __forceinline__ void pages(const KvView& c, const AttnArgs& a, const Work& w, int t, int end, int tid) {
-    if (t >= end) return;
-    const int base = w.k.base(t);
-#pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-      const int tok = base + p * kPer + tid / kChunks;
-      // what no row sees reads as zero: a NaN there would reach the rows through 0 * NaN
-      pid[p] = tok < w.k.hi && (tok >= w.k.lo || tok < a.sinks) ? load_page(c, w.b, tok >> c.page_log2) : -1;
-    }
-    if (tid < 8) {
-      const int tok = base + 16 * tid;
-      gpid = tok < w.k.hi ? load_page(c, w.b, tok >> c.page_log2) : -1;
-    }
-  }
-  __device__ __forceinline__ void load(const KvView& c, const Work& w, const uint8_t* src, int t, int tid,
-                                       uint4 (&raw)[kPasses]) const {
-    const int base = w.k.base(t);
-#pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-      const int tok = base + p * kPer + tid / kChunks;
-      raw[p] = make_uint4(0, 0, 0, 0);
-      if (pid[p] >= 0)
-        raw[p] = __ldg(reinterpret_cast<const uint4*>(
-            src + ((static_cast<size_t>(pid[p]) * c.hkv + w.hk) * c.page + (tok & (c.page - 1))) * D +
-            (tid % kChunks) * 16));
-    }
-  }
-  __device__ __forceinline__ void store(char* dst, int tid, const uint4 (&raw)[kPasses]) const {
-    const int ch = tid % kChunks, half = ch >> 2;
-#pragma unroll
-    for (int p = 0; p < kPasses; ++p) {
-      const int row = p * kPer + tid / kChunks;
-      uint32_t h[8];
-      codes_to_half(raw[p].x, h[0], h[1]);
-      codes_to_half(raw[p].y, h[2], h[3]);
-      codes_to_half(raw[p].z, h[4], h[5]);
-      codes_to_half(raw[p].w, h[6], h[7]);
-      char* line = dst + half * Lay<D>::kHalf + row * 128;
-      const int c0 = 2 * (ch & 3);
-      // lanes of the two halves take their two chunks in opposite order: no bank conflicts
-      const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-      const bool swap = half != 0;
-      *reinterpret_cast<uint4*>(line + (((c0 + (swap ? 1 : 0)) ^ (row & 7)) << 4)) = swap ? hi : lo;
-      *reinterpret_cast<uint4*>(line + (((c0 + (swap ? 0 : 1)) ^ (row & 7)) << 4)) = swap ? lo : hi;
-    }
-  }
-};
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_tiles_kernel(const KvView c, const AttnArgs a, const AttnWs ws, const Plan pl) {
+    attn_tiles_kernel(const KvView c, const AttnArgs a, const AttnWs ws, const Plan pl,
+                      const __grid_constant__ CUtensorMap k_map) {
   using L_ = Lay<D>;
   extern __shared__ char smem_raw[];
   __shared__ uint32_t s_tmem;
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t base_u = smem_u32(smem);
-  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), wg = warp >> 2;  // uniform
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), wg = warp >> 2, lane = threadIdx.x & 31;
 
   // long tiles first: the last rows of a causal prompt see the most keys
   int idx = blockIdx.x;
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   auto bar = [&](int i) { return base_u + L_::kBar + 8 * i; };
   if (threadIdx.x == 0) {
-    const int count[kBars] = {128 * n_mt, 128, 128, 1, 1, 128, 128, 1, 1, 1, 1, 128, 128, 1, 1};
+    const int count[kBars] = {128 * n_mt, 9, 9, 9, 1, 1, 1, 1, 1, 128, 128, 128, 128, 1, 1, 1, 1, 128, 128, 1, 1};
 #pragma unroll
     for (int i = 0; i < kBars; ++i) mbar_init(bar(i), count[i]);
     fence_barrier_init();
@@ -223,17 +228,77 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after_sync();
   const uint32_t tmem = s_tmem;
 
-  if (wg == 3) {
-    if ((threadIdx.x & 31) == 0 && n > 0) {
-      constexpr uint32_t id_s = idesc_f16(kM, kTile);
+  if (warp == 13) {
+    // lane g (0 .. 7) looks after 16-key group g; the first group of a page
+    // issues the page's copies
+    if (lane < 8 && n > 0) {
+      bool ok = true, bad = false;
+      const int per = c.page >> 4;  // groups of a page
+      const uint32_t bytes = static_cast<uint32_t>(c.page) * D;
+      auto seen = [&](int t) {  // whether some row sees a key of the group's page
+        const int tok = w.k.base(t) + 16 * (lane & ~(per - 1));
+        return tok < w.k.hi && (tok + c.page > w.k.lo || tok < a.sinks);
+      };
+      auto entry = [&](int t) {
+        return t < t_end && seen(t) ? raw_page(c, b, (w.k.base(t) + 16 * lane) >> c.page_log2) : INT_MIN;
+      };
+      int raw = entry(t_begin);
+      int k_sent = 0, r_sent = 0;  // tiles whose copies are on their way
+      for (int j = 0; ok && j < n; ++j) {
+        const int ks = j % kKStages, rs = j & 1;
+        const int page = raw == INT_MIN ? -1 : checked_page(c, raw, bad);
+        float kscale = 0.f, vscale = 1.f;
+        if (page >= 0) {
+          const size_t at = static_cast<size_t>(page) * c.hkv + hk;
+          kscale = __ldg(c.k_scale + at);
+          vscale = __ldg(c.v_scale + at);
+        }
+        raw = entry(t_begin + j + 1);
+        const bool copies = page >= 0 && (lane & (per - 1)) == 0;
+        const uint32_t total = __popc(__ballot_sync(0xffu, copies)) * bytes;
+        ok = j < kKStages || mbar_wait(bar(kKEmpty + ks), (j / kKStages - 1) & 1, c.err);
+        ok = __all_sync(0xffu, ok);
+        if (!ok) break;
+        // a ring of four: the softmax of tile j - 4 is done when the K stage of tile j is free
+        vscale = fmaxf(vscale, kMinBlockScale);
+        reinterpret_cast<float4*>(smem + L_::kConst)[(j & 3) * 8 + lane] =
+            make_float4(kscale, __log2f(vscale), __frcp_rn(vscale), 0.f);
+        if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + ks), total);
+        __syncwarp(0xffu);
+        if (copies)
+          tma_load_3d(base_u + L_::kK + ks * L_::kMat8 + 16 * lane * D, &k_map, 0, hk * c.page, page,
+                      bar(kKFull + ks));
+        mbar_arrive(bar(kKFull + ks));
+        k_sent = j + 1;
+        ok = j < 2 || mbar_wait(bar(kREmpty + rs), ((j >> 1) - 1) & 1, c.err);
+        ok = __all_sync(0xffu, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(bar(kRFull + rs), total);
+        __syncwarp(0xffu);
+        if (copies)
+          bulk_g2s(base_u + L_::kRaw + rs * L_::kMat8 + 16 * lane * D,
+                   c.v + (static_cast<size_t>(page) * c.hkv + hk) * bytes, bytes, bar(kRFull + rs));
+        r_sent = j + 1;
+      }
+      if (!ok) {  // the copies land before the CTA goes
+        for (int j = max(k_sent - kKStages, 0); j < k_sent; ++j)
+          mbar_wait(bar(kKFull + j % kKStages), (j / kKStages) & 1, c.err);
+        for (int j = max(r_sent - 2, 0); j < r_sent; ++j) mbar_wait(bar(kRFull + (j & 1)), (j >> 1) & 1, c.err);
+      }
+      if (bad) atomicOr(c.err, kErrBadBatch);
+    }
+  } else if (warp == 12) {
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t id_s = idesc_f16(kM, kTile);           // e4m3 is format 0 of its kind, too
       constexpr uint32_t id_o = idesc_f16(kM, D) | (1u << 16);  // V is MN-major
       auto issue_s = [&](int i, int stage) {
-        const uint32_t qa = base_u + L_::kQ + i * L_::kMat, kb = base_u + L_::kK + stage * L_::kMat;
+        const uint32_t qa = base_u + L_::kQ + i * 2 * L_::kMat8, kb = base_u + L_::kK + stage * L_::kMat8;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * L_::kHalf + (k & 3) * 32;
-          mma_ss(tmem + i * 128, sdesc_sw128(qa + off), sdesc_sw128(kb + off), id_s, k != 0);
-        }
+        for (int term = 0; term < 2; ++term)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            mma_ss_e4m3(tmem + i * 128, sdesc_k<D>(qa + term * L_::kMat8 + k * 32), sdesc_k<D>(kb + k * 32), id_s,
+                        (term | k) != 0);
         mma_commit(bar(kSFull + i));
       };
       bool ok = mbar_wait(bar(kQFull), 0, c.err) && mbar_wait(bar(kKFull), 0, c.err);
@@ -242,9 +307,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < n_mt; ++i) issue_s(i, 0);
         mma_commit(bar(kKEmpty));
       }
+      int ks = 0, kph = 0;  // K stage and parity of tile j
       for (int j = 0; ok && j < n; ++j) {
         const int st = j & 1;
         const uint32_t vb = base_u + L_::kV + st * L_::kMat;
+        if (++ks == kKStages) ks = 0, kph ^= 1;  // those of tile j + 1
         for (int i = 0; ok && i < n_mt; ++i) {
           ok = mbar_wait(bar(kPFull + i), j & 1, c.err) && (i > 0 || mbar_wait(bar(kVFull + st), (j >> 1) & 1, c.err));
           if (!ok) break;
@@ -257,12 +324,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j == n - 1) {
             mma_commit(bar(kOFull + i));
           } else {
-            const int s2 = (j + 1) & 1;
-            ok = i > 0 || mbar_wait(bar(kKFull + s2), ((j + 1) >> 1) & 1, c.err);
+            ok = i > 0 || mbar_wait(bar(kKFull + ks), kph, c.err);
             if (!ok) break;
             fence_after_sync();
-            issue_s(i, s2);
-            if (i == n_mt - 1) mma_commit(bar(kKEmpty + s2));
+            issue_s(i, ks);
+            if (i == n_mt - 1) mma_commit(bar(kKEmpty + ks));
           }
         }
       }
@@ -273,49 +339,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (wg == 2) {
+    // value codes to f16: thread t takes 16-byte chunk t % (D / 16) of keys
+    // t / (D / 16) + 0, kPer, ...; a chunk becomes two of the operand's
     const int tid = threadIdx.x - 256;
-    if (n > 0) {
-      Converter<D> cv;
-      uint4 kr[Converter<D>::kPasses], vr[Converter<D>::kPasses];
-      float4 cn = make_float4(0.f, 0.f, 1.f, 0.f);
-      auto consts = [&]() {  // of the tile whose pages are in cv
-        if (tid < 8) {
-          float ks = 0.f, vs = 1.f;
-          if (cv.gpid >= 0) {
-            const size_t at = static_cast<size_t>(cv.gpid) * c.hkv + w.hk;
-            ks = __ldg(c.k_scale + at);
-            vs = __ldg(c.v_scale + at);
-          }
-          vs = fmaxf(vs, kMinBlockScale);
-          cn = make_float4(ks, __log2f(vs), __frcp_rn(vs), 0.f);
+    constexpr int kChunks = D / 16, kPer = 128 / kChunks;
+    const int ch = tid % kChunks, row0 = tid / kChunks;
+    // the two halves' lanes store their two chunks in opposite order: no bank conflicts
+    const int c0 = 2 * (ch & 3) + (ch >> 2);
+    const uint32_t out = (ch >> 2) * L_::kHalf + row0 * 128;
+    const uint32_t o0 = out + ((c0 ^ (row0 & 7)) << 4), o1 = out + (((c0 ^ 1) ^ (row0 & 7)) << 4);
+    const bool swap = (ch >> 2) != 0;
+    for (int j = 0; j < n; ++j) {
+      const int st = j & 1, ph = (j >> 1) & 1;
+      if (!mbar_wait(bar(kRFull + st), ph, c.err)) break;
+      if (j >= 2 && !mbar_wait(bar(kVEmpty + st), ph ^ 1, c.err)) break;
+      const int base = w.k.base(t_begin + j);
+      const bool whole = base + kTile <= w.k.hi && (base >= w.k.lo || base + kTile <= a.sinks);
+      const char* src = smem + L_::kRaw + st * L_::kMat8 + tid * 16;
+      char* dst = smem + L_::kV + st * L_::kMat;
+#pragma unroll
+      for (int p = 0; p < kTile / kPer; ++p) {
+        uint4 raw = *reinterpret_cast<const uint4*>(src + p * 2048);
+        if (!whole) {
+          // what no row sees is zero: a NaN there would reach the rows through 0 * NaN
+          const int tok = base + p * kPer + row0;
+          if (!(tok < w.k.hi && (tok >= w.k.lo || tok < a.sinks))) raw = make_uint4(0, 0, 0, 0);
         }
-      };
-      cv.pages(c, a, w, t_begin, t_end, tid);
-      cv.load(c, w, c.k, t_begin, tid, kr);
-      cv.load(c, w, c.v, t_begin, tid, vr);
-      consts();
-      cv.pages(c, a, w, t_begin + 1, t_end, tid);
-      bool ok = true;
-      for (int j = 0; j < n; ++j) {
-        const int st = j & 1;
-        const uint32_t prev = ((j >> 1) & 1) ^ 1;  // parity of the stage's release two tiles ago
-        if (j >= 2 && !(ok = mbar_wait(bar(kKEmpty + st), prev, c.err))) break;
-        cv.store(smem + L_::kK + st * L_::kMat, tid, kr);
-        // a ring of four: the softmax of tile j - 3 is done when the K stage of tile j is free
-        if (tid < 8) reinterpret_cast<float4*>(smem + L_::kConst)[(j & 3) * 8 + tid] = cn;
-        fence_proxy_async_smem();
-        mbar_arrive(bar(kKFull + st));
-        if (j + 1 < n) cv.load(c, w, c.k, t_begin + j + 1, tid, kr);
-        if (j >= 2 && !(ok = mbar_wait(bar(kVEmpty + st), prev, c.err))) break;
-        cv.store(smem + L_::kV + st * L_::kMat, tid, vr);
-        fence_proxy_async_smem();
-        mbar_arrive(bar(kVFull + st));
-        if (j + 1 < n) {
-          cv.load(c, w, c.v, t_begin + j + 1, tid, vr);
-          consts();
-          cv.pages(c, a, w, t_begin + j + 2, t_end, tid);
-        }
+        uint4 lo, hi;
+        codes_to_half(raw.x, lo.x, lo.y);
+        codes_to_half(raw.y, lo.z, lo.w);
+        codes_to_half(raw.z, hi.x, hi.y);
+        codes_to_half(raw.w, hi.z, hi.w);
+        // (kPer is a multiple of 8: the swizzle of a later pass is the first's)
+        *reinterpret_cast<uint4*>(dst + o0 + p * kPer * 128) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(dst + o1 + p * kPer * 128) = swap ? lo : hi;
       }
+      fence_proxy_async_smem();
+      mbar_arrive(bar(kVFull + st));
+      mbar_arrive(bar(kREmpty + st));
     }
   } else if (wg < n_mt) {
     const int i = wg, row = threadIdx.x & 127;
@@ -329,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = -INFINITY, l = 0.f, lscale = 0.f;  // lscale >= 0: a negative scale turns the query's sign
     bool ok = true;
     if (n > 0) {
-      // the row's query to f16, brought to [2^14, 2^15) by a power of two
+      // the row's query, brought to [2^7, 2^8) by a power of two, as two e4m3 terms
       const uint4* src = reinterpret_cast<const uint4*>(
           a.q + (static_cast<int64_t>(w.q.q0) + tok) * a.q_stride + static_cast<int64_t>(head) * D);
       uint4 raw[D / 8];
@@ -340,20 +401,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t u[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xffff0000u))));
+          amax = max3(amax, fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xffff0000u)));
       }
-      const float f = copysignf(row_factor(amax), a.scale_log2);
+      const float f = copysignf(row_factor<7>(amax), a.scale_log2);
       lscale = a.scale_log2 / f;
-      char* dst = smem + L_::kQ + i * L_::kMat + row * 128;
+      const bool inf = !(amax < INFINITY);  // (codes saturate: such a row is NaN instead)
+      char* dst = smem + L_::kQ + i * 2 * L_::kMat8;
 #pragma unroll
-      for (int x = 0; x < D / 8; ++x) {
-        const uint32_t u[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
-        uint32_t h[4];
+      for (int x = 0; x < D / 16; ++x) {
+        const uint32_t u[8] = {raw[2 * x].x,     raw[2 * x].y,     raw[2 * x].z,     raw[2 * x].w,
+                               raw[2 * x + 1].x, raw[2 * x + 1].y, raw[2 * x + 1].z, raw[2 * x + 1].w};
+        uint32_t t0[4], t1[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          h[k] = half2_bits(__uint_as_float(u[k] << 16) * f, __uint_as_float(u[k] & 0xffff0000u) * f);
-        *reinterpret_cast<uint4*>(dst + (x >> 3) * L_::kHalf + (((x & 7) ^ (row & 7)) << 4)) =
-            make_uint4(h[0], h[1], h[2], h[3]);
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w0 = 0, w1 = 0;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 v = make_float2(__uint_as_float(u[2 * k + e] << 16) * f,
+                                         __uint_as_float(u[2 * k + e] & 0xffff0000u) * f);
+            const uint32_t q1 = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+            const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(q1), __NV_E4M3);
+            const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+            const uint32_t q2 =
+                __nv_cvt_float2_to_fp8x2(make_float2(v.x - back.x, v.y - back.y), __NV_SATFINITE, __NV_E4M3);
+            w0 |= q1 << (16 * e);
+            w1 |= q2 << (16 * e);
+          }
+          t0[k] = inf ? 0x7f7f7f7fu : w0;
+          t1[k] = w1;
+        }
+        const uint32_t off = k_off<D>(row, x);
+        *reinterpret_cast<uint4*>(dst + off) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
+        *reinterpret_cast<uint4*>(dst + L_::kMat8 + off) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(kQFull));
@@ -363,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = 0; j < n; ++j) {
       // K's barrier orders this thread after the scales in shared memory, S's
       // after the products (and after O += P V of the tile before)
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(kKFull + (j & 1)), (j >> 1) & 1, c.err) &&
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(kKFull + j % kKStages), (j / kKStages) & 1, c.err) &&
                                        mbar_wait(bar(kSFull + i), j & 1, c.err));
       if (!ok) break;
       fence_after_sync();
@@ -375,30 +454,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       // row's largest logit (within 16 keys of one scale the largest product
       // gives it), then for the weights
       float s[2][32];
-      auto hide = [&](int x) {
-        if (!whole) {
+      if (!whole) {
+        // what the row does not see goes to -inf first, where it lies
+#pragma unroll 1
+        for (int x = 0; x < 4; ++x) {
+          tmem_ld32(ts + 32 * x, s[0]);
+          tmem_wait_ld32(s[0]);
+          uint32_t u[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            s[x & 1][k] = sees(base + 32 * x + k) ? s[x & 1][k] : -INFINITY;
+          for (int k = 0; k < 32; ++k) u[k] = sees(base + 32 * x + k) ? __float_as_uint(s[0][k]) : 0xff800000u;
+          tmem_st32(ts + 32 * x, u);
         }
-      };
+        tmem_wait_st();
+      }
       float mt = -INFINITY;
       tmem_ld32(ts, s[0]);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         tmem_wait_ld32(s[x & 1]);
         tmem_ld32(ts + 32 * ((x + 1) & 3), s[(x + 1) & 1]);
-        hide(x);
 #pragma unroll
         for (int gg = 0; gg < 2; ++gg) {
           const float4 z = cn[2 * x + gg];
           const float* v = s[x & 1] + 16 * gg;
-          float t0 = fmaxf(fmaxf(v[0], v[1]), v[2]), t1 = fmaxf(fmaxf(v[3], v[4]), v[5]);
-#pragma unroll
-          for (int k = 6; k < 16; k += 2) {
-            float& t = (k & 2) ? t0 : t1;
-            t = fmaxf(fmaxf(t, v[k]), v[k + 1]);
-          }
+          float t0 = max3(v[0], v[1], v[2]), t1 = max3(v[3], v[4], v[5]);
+          t0 = max3(t0, v[6], v[7]), t1 = max3(t1, v[8], v[9]);
+          t0 = max3(t0, v[10], v[11]), t1 = max3(t1, v[12], v[13]);
+          t0 = max3(t0, v[14], v[15]);
           mt = fmaxf(mt, fmaf(fmaxf(t0, t1), fmaxf(lscale * z.x, kTiny), z.y));
         }
       }
@@ -424,7 +506,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < 4; ++x) {
         tmem_wait_ld32(s[x & 1]);
         if (x < 3) tmem_ld32(ts + 32 * (x + 1), s[(x + 1) & 1]);
-        hide(x);
         uint32_t u[16];
 #pragma unroll
         for (int gg = 0; gg < 2; ++gg) {
@@ -434,9 +515,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
-            const float w0 = ex2(fmaf(v[k], sc, off)), w1 = ex2(fmaf(v[k + 1], sc, off));
-            sum0 += w0;
-            sum1 += w1;
+            float w0, w1;
+            fma2(w0, w1, v[k], v[k + 1], sc, off);
+            w0 = ex2(w0), w1 = ex2(w1);
+            add2(sum0, sum1, w0, w1);
             u[8 * gg + k / 2] = half2_bits(w0, w1);
           }
           l = fmaf(sum0 + sum1, z.z, l);
@@ -503,7 +585,8 @@ __global__ void __launch_bounds__(kJoinThreads)
 }
 
 template <int D>
-cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, int n_sm, cudaStream_t s) {
+cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const CUtensorMap& k_map, int n_sm,
+                   cudaStream_t s) {
   static std::atomic<size_t> done[kMaxDevices];
   const void* fn = reinterpret_cast<const void*>(attn_tiles_kernel<D>);
   if (const cudaError_t e = opt_in_smem(fn, done, Lay<D>::kSmem); e != cudaSuccess) return e;
@@ -521,7 +604,7 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, int n_s
   pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
   const int64_t grid = base * pl.splits;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  attn_tiles_kernel<D><<<static_cast<unsigned>(grid), kThreads, Lay<D>::kSmem, s>>>(c, a, ws, pl);
+  attn_tiles_kernel<D><<<static_cast<unsigned>(grid), kThreads, Lay<D>::kSmem, s>>>(c, a, ws, pl, k_map);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || pl.splits == 1) return e;
   const int64_t items = base * kRows, per = kJoinThreads / (D / 4);
@@ -531,9 +614,9 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, int n_s
 
 }  // namespace
 
-cudaError_t attn_tiles_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, int n_sm,
-                              cudaStream_t s) {
-  return c.D == 128 ? launch<128>(c, a, ws, n_sm, s) : launch<64>(c, a, ws, n_sm, s);
+cudaError_t attn_tiles_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const KvMaps& maps,
+                              int n_sm, cudaStream_t s) {
+  return c.D == 128 ? launch<128>(c, a, ws, maps.k_tile, n_sm, s) : launch<64>(c, a, ws, maps.k_tile, n_sm, s);
 }
 
 }  // namespace moe
