@@ -58,7 +58,7 @@ struct Lay {
 
 enum Bar {
   kQFull = 0,
-  kKFull = 1,    // [3] bytes + the scales' writers
+  kKFull = 1,    // [3] key codes
   kKEmpty = 4,   // [3]
   kRFull = 7,    // [2] value codes
   kREmpty = 9,   // [2]
@@ -67,17 +67,53 @@ enum Bar {
   kSFull = 15,   // [2] by M tile
   kPFull = 17,
   kOFull = 19,
-  kBars = 21
+  kCFull = 21,   // [4] scales
+  kBars = 25
 };
 
-// D[tmem] (+)= A[smem] * B[smem], e4m3 operands, f32 accumulator.
-__device__ __forceinline__ void mma_ss_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// The one thread that issues products is on every step's path: the MMAs of a
+// product stand in one block, their descriptors a constant apart.
+//
+// S[tmem] = (Q1 + Q2) K^T: e4m3 operands, f32 accumulator; q and k step by 32
+// codes (32 bytes) along the head, the second term `TERM` bytes behind Q1.
+#define MOE_S_MMA(A, B, P) "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], " A ", " B ", %3, " P ";\n\t"
+template <int D>
+__device__ __forceinline__ void mma_s(uint32_t d_tmem, uint64_t q_desc, uint64_t k_desc, uint32_t idesc) {
+  constexpr uint64_t kTerm = (kTile * D) >> 4;
+  if constexpr (D == 128) {
+    asm volatile(
+        "{\n\t.reg .b64 q<8>, k<4>;\n\t"
+        "add.s64 k1, %2, 2;\n\tadd.s64 k2, %2, 4;\n\tadd.s64 k3, %2, 6;\n\t"
+        "add.s64 q1, %1, 2;\n\tadd.s64 q2, %1, 4;\n\tadd.s64 q3, %1, 6;\n\t"
+        "add.s64 q4, %1, %4;\n\tadd.s64 q5, q4, 2;\n\tadd.s64 q6, q4, 4;\n\tadd.s64 q7, q4, 6;\n\t"
+        MOE_S_MMA("%1", "%2", "0") MOE_S_MMA("q1", "k1", "1") MOE_S_MMA("q2", "k2", "1") MOE_S_MMA("q3", "k3", "1")
+        MOE_S_MMA("q4", "%2", "1") MOE_S_MMA("q5", "k1", "1") MOE_S_MMA("q6", "k2", "1") MOE_S_MMA("q7", "k3", "1")
+        "}" ::"r"(d_tmem), "l"(q_desc), "l"(k_desc), "r"(idesc), "n"(kTerm)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .b64 q<4>, k1;\n\t"
+        "add.s64 k1, %2, 2;\n\tadd.s64 q1, %1, 2;\n\tadd.s64 q2, %1, %4;\n\tadd.s64 q3, q2, 2;\n\t"
+        MOE_S_MMA("%1", "%2", "0") MOE_S_MMA("q1", "k1", "1") MOE_S_MMA("q2", "%2", "1") MOE_S_MMA("q3", "k1", "1")
+        "}" ::"r"(d_tmem), "l"(q_desc), "l"(k_desc), "r"(idesc), "n"(kTerm)
+        : "memory");
+  }
+}
+#undef MOE_S_MMA
+
+// O[tmem] (+)= P[tmem] V[smem] over 64 keys: P 8 columns, V 16 rows of 128
+// bytes a K step; the first MMA overwrites O when `first`.
+__device__ __forceinline__ void mma_o(uint32_t d_tmem, uint32_t p_tmem, uint64_t v_desc, uint32_t idesc,
+                                      uint32_t first) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 v<4>;\n\t"
+      "setp.eq.b32 p, %4, 0;\n\t"
+      "add.s64 v1, %2, 128;\n\tadd.s64 v2, %2, 256;\n\tadd.s64 v3, %2, 384;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1 + 8], v1, %3, 1;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1 + 16], v2, %3, 1;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1 + 24], v3, %3, 1;\n\t}" ::"r"(d_tmem),
+      "r"(p_tmem), "l"(v_desc), "r"(idesc), "r"(first)
       : "memory");
 }
 
@@ -133,6 +169,14 @@ __device__ __forceinline__ void tmem_wait_ld32(float* v) {
                  "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]),
                  "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]),
                  "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
                :
                : "memory");
 }
@@ -214,7 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   auto bar = [&](int i) { return base_u + L_::kBar + 8 * i; };
   if (threadIdx.x == 0) {
-    const int count[kBars] = {128 * n_mt, 9, 9, 9, 1, 1, 1, 1, 1, 128, 128, 128, 128, 1, 1, 1, 1, 128, 128, 1, 1};
+    const int count[kBars] = {128 * n_mt, 1, 1, 1, 1, 1, 1, 1, 1, 128, 128, 128, 128,
+                              1, 1, 1, 1, 128, 128, 1, 1, 8, 8, 8, 8};
 #pragma unroll
     for (int i = 0; i < kBars; ++i) mbar_init(bar(i), count[i]);
     fence_barrier_init();
@@ -259,16 +304,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = j < kKStages || mbar_wait(bar(kKEmpty + ks), (j / kKStages - 1) & 1, c.err);
         ok = __all_sync(0xffu, ok);
         if (!ok) break;
-        // a ring of four: the softmax of tile j - 4 is done when the K stage of tile j is free
+        // a ring of four: the softmax of tile j - 4 is done when the K stage of tile j is free,
+        // and has been through its slot's barrier (a parity tells neighbouring phases apart)
         vscale = fmaxf(vscale, kMinBlockScale);
         reinterpret_cast<float4*>(smem + L_::kConst)[(j & 3) * 8 + lane] =
             make_float4(kscale, __log2f(vscale), __frcp_rn(vscale), 0.f);
+        mbar_arrive(bar(kCFull + (j & 3)));
         if (lane == 0) mbar_arrive_expect_tx(bar(kKFull + ks), total);
         __syncwarp(0xffu);
         if (copies)
           tma_load_3d(base_u + L_::kK + ks * L_::kMat8 + 16 * lane * D, &k_map, 0, hk * c.page, page,
                       bar(kKFull + ks));
-        mbar_arrive(bar(kKFull + ks));
         k_sent = j + 1;
         ok = j < 2 || mbar_wait(bar(kREmpty + rs), ((j >> 1) - 1) & 1, c.err);
         ok = __all_sync(0xffu, ok);
@@ -291,14 +337,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && n > 0) {
       constexpr uint32_t id_s = idesc_f16(kM, kTile);           // e4m3 is format 0 of its kind, too
       constexpr uint32_t id_o = idesc_f16(kM, D) | (1u << 16);  // V is MN-major
+      const uint64_t q_desc = sdesc_k<D>(base_u + L_::kQ), k_desc = sdesc_k<D>(base_u + L_::kK);
+      const uint64_t v_desc = sdesc_sw128_mn(base_u + L_::kV, L_::kHalf);
       auto issue_s = [&](int i, int stage) {
-        const uint32_t qa = base_u + L_::kQ + i * 2 * L_::kMat8, kb = base_u + L_::kK + stage * L_::kMat8;
-#pragma unroll
-        for (int term = 0; term < 2; ++term)
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k)
-            mma_ss_e4m3(tmem + i * 128, sdesc_k<D>(qa + term * L_::kMat8 + k * 32), sdesc_k<D>(kb + k * 32), id_s,
-                        (term | k) != 0);
+        mma_s<D>(tmem + i * 128, q_desc + i * (2 * L_::kMat8 >> 4), k_desc + stage * (L_::kMat8 >> 4), id_s);
         mma_commit(bar(kSFull + i));
       };
       bool ok = mbar_wait(bar(kQFull), 0, c.err) && mbar_wait(bar(kKFull), 0, c.err);
@@ -310,16 +352,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       int ks = 0, kph = 0;  // K stage and parity of tile j
       for (int j = 0; ok && j < n; ++j) {
         const int st = j & 1;
-        const uint32_t vb = base_u + L_::kV + st * L_::kMat;
+        const uint64_t vd = v_desc + st * (L_::kMat >> 4);
         if (++ks == kKStages) ks = 0, kph ^= 1;  // those of tile j + 1
         for (int i = 0; ok && i < n_mt; ++i) {
           ok = mbar_wait(bar(kPFull + i), j & 1, c.err) && (i > 0 || mbar_wait(bar(kVFull + st), (j >> 1) & 1, c.err));
           if (!ok) break;
           fence_after_sync();
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_ts(tmem + 256 + i * 128, tmem + i * 128 + k * 8, sdesc_sw128_mn(vb + k * 2048, L_::kHalf), id_o,
-                   (j | k) != 0);
+          const uint32_t ot = tmem + 256 + i * 128, pt = tmem + i * 128;
+          mma_o(ot, pt, vd, id_o, j == 0);
+          mma_o(ot, pt + 32, vd + (64 * 128 >> 4), id_o, 0);
           if (i == n_mt - 1) mma_commit(bar(kVEmpty + st));
           if (j == n - 1) {
             mma_commit(bar(kOFull + i));
@@ -440,9 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the range that all rows of the CTA see whole
     const int p_lo = w.base_p + w.r0 / a.G, p_hi = w.base_p + (w.r1 - 1) / a.G;
     for (int j = 0; j < n; ++j) {
-      // K's barrier orders this thread after the scales in shared memory, S's
-      // after the products (and after O += P V of the tile before)
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(kKFull + j % kKStages), (j / kKStages) & 1, c.err) &&
+      // (S of this tile says that O += P V of the tile before is done, too)
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(kCFull + (j & 3)), (j >> 2) & 1, c.err) &&
                                        mbar_wait(bar(kSFull + i), j & 1, c.err));
       if (!ok) break;
       fence_after_sync();
@@ -494,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int x = 0; x < D / 16; ++x) {
             uint32_t u[16];
             tmem_ld16(to + 16 * x, u);
-            tmem_wait_ld();
+            tmem_wait_ld16(u);
 #pragma unroll
             for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * f);
             tmem_st16(to + 16 * x, u);
@@ -540,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float o[32];
         if (n > 0) {
           tmem_ld32(to + 32 * x, o);
-          tmem_wait_ld();
+          tmem_wait_ld32(o);
         } else {
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0.f;
