@@ -204,8 +204,7 @@ bool kv_create_maps(const moe_kv_config_t& cfg, const moe_kv_store_t& st, KvMaps
                   D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
-  const int small = cfg.page_size < 32 ? cfg.page_size : 32;
-  return make(&m->k_tile, st.k, cfg.page_size) && make(&m->k_rows, st.k, small) && make(&m->v_rows, st.v, small);
+  return make(&m->k_tile, st.k, cfg.page_size);
 }
 
 }  // namespace moe
@@ -503,7 +502,7 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
   const bool tiles = static_cast<int64_t>(c.max_q) * a.G >= 128;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return launched(h, tiles ? moe::attn_tiles_launch(c, a, h->ws, h->maps, h->n_sm, s)
-                           : moe::attn_rows_launch(c, a, h->ws, h->n_sm, s),
+                           : moe::attn_few_launch(c, a, h->ws, h->maps, h->n_sm, s),
                   "moe_kv_attend");
 }
 
