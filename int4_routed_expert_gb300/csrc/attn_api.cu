@@ -204,7 +204,7 @@ bool kv_create_maps(const moe_kv_config_t& cfg, const moe_kv_store_t& st, KvMaps
                   D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
   };
-  return make(&m->k_tile, st.k, cfg.page_size);
+  return make(&m->k_tile, st.k, cfg.page_size) && make(&m->v_tile, st.v, cfg.page_size);
 }
 
 }  // namespace moe

@@ -9,16 +9,23 @@
 // to the largest contribution, whatever the blocks' scales are.  m moves only
 // when it would grow by 2^5.
 //
-// A CTA takes N = 16 or 64 rows of a kv head and walks over tiles of 128 keys:
-//   S^T[128 keys x 2 N] = K [Q1; Q2]^T   e4m3; the bf16 query as two e4m3 terms
-//   P[128 keys x N]                      a thread a key, f16
-//   O^T[128 dims x N]  += V^T P          f16, V as it lies (M-major)
-// With the keys in M the tensor pipe reads K and V once whatever N is, a
-// thread's block scales are scalars, it writes its key's weights as they stand
-// in one operand row, and no thread shuffles: only when a reference moves, the
-// maxima over the keys are exchanged.  The keys are split over CTAs; the last
-// CTA of a row tile to arrive joins them.
-// Warps: 4 softmax for every 32 rows, 4 conversion of the value codes, MMA, load.
+// A CTA takes N = 16, 32 or 64 rows of a kv head and walks over tiles of 128
+// keys, multiplied as they are stored:
+//   S^T[128 keys x 2 N]   = K [Q1; Q2]^T         the bf16 query as two e4m3 terms
+//   P[128 keys x 4 N]                            a thread a key
+//   O^T[128 dims x 4 N]  += V^T [P1 P2 P3 P4]    V as it lies (M-major)
+// A weight is rounded to f16 (11 bits) and cut into e4m3 terms of 4 bits, term
+// i scaled by 16^(i - 1) into its own accumulator columns: exact for weights
+// above 2^-10 of the row's largest, and to 2^-30 of the largest below (the
+// lift of 7 and the reference within 2 of the largest see to that).  So no
+// value is converted, shared memory carries each code once in and once out,
+// and the extra columns are free: with the keys and dims in M the products are
+// bound by reading K and V, whatever N is.  A thread's block scales are
+// scalars, it writes its key's weights as they stand in one operand row, and
+// no thread shuffles: only when a reference moves, the maxima over the keys
+// are exchanged.  The keys are split over CTAs; the last CTA of a row tile to
+// arrive joins them.
+// Warps: 4 softmax for every 16 rows, MMA, load.
 // Bound by memory: 2 D bytes a key and kv head.
 #include "attn_tc.cuh"
 
@@ -26,41 +33,40 @@ namespace moe {
 namespace {
 
 
+constexpr float kFewLift = 7.f, kFewRescale = 1.f;  // weights below 2^8: an e4m3 ends at 448
+
 enum Bar {
   kQFull = 0,
-  kKFull = 1,    // [3] key codes
-  kKEmpty = 4,   // [3]
-  kRFull = 7,    // [3] value codes
-  kREmpty = 10,  // [3]
-  kVFull = 13,   // [2] values
-  kSFull = 15,   // [2] S^T
-  kPFull = 17,   // [2] P
-  kODone = 19,   // [2] O^T += V^T P, by the parity of the tile
-  kCFull = 21,   // [4] scales
-  kDrain = 25,
-  kBars = 26
+  kKFull = 1,    // [4] key codes
+  kKEmpty = 5,   // [4]
+  kVFull = 9,    // [4] value codes
+  kVEmpty = 13,  // [4]
+  kSFull = 17,   // [2] S^T
+  kPFull = 19,   // P
+  kODone = 20,   // O^T += V^T P
+  kCFull = 21,   // [8] scales
+  kDrain = 29,
+  kBars = 30
 };
 
-// N = 16 keeps to half an SM, so that two CTAs cover each other's bubbles.
+// Up to 32 rows keep to half an SM, so that two CTAs cover each other's bubbles.
 template <int D, int N>
 struct Lay {
-  static constexpr int kStages = N == 16 ? 2 : 3;   // of key codes and of value codes
-  static constexpr int kVStages = N == 16 ? 1 : 2;  // of f16 values
-  using Io = TileIo<D, kStages, kStages, kVStages>;
-  static constexpr int kGroups = N == 16 ? 1 : 2;   // softmax groups of 128 threads
-  static constexpr int kGroupRows = N / kGroups;
-  static constexpr int kThreads = 128 * kGroups + 192;
-  static constexpr int kQ = 0;                      // [2 N][D]
+  static constexpr int kStages = N == 16 ? 3 : N == 32 ? 2 : 4;  // of key codes and of value codes
+  static constexpr int kCtas = N == 64 ? 1 : 2;                  // a SM
+  using Io = TileIo<D, kStages, kStages, 0>;
+  static constexpr int kGroups = N / 16;  // softmax groups of 128 threads
+  static constexpr int kThreads = 128 * kGroups + 64;
+  static constexpr int kQ = 0;            // [2 N][D]
   static constexpr int kK = kQ + (2 * N * D + 1023) / 1024 * 1024;
   static constexpr int kV = kK + kStages * Io::kMat8;
-  static constexpr int kRaw = kV + kVStages * Io::kMat;
-  static constexpr int kP = kRaw + kStages * Io::kMat8;  // [2][128 keys][N] f16
-  static constexpr int kConst = kP + 2 * kKeys * N * 2;
+  static constexpr int kP = kV + kStages * Io::kMat8;  // [128 keys][4 N]
+  static constexpr int kConst = kP + kKeys * 4 * N;
   static constexpr int kRow = kConst + kConstRing * 8 * 16;  // [6][N]: see Rows
   static constexpr int kRed = kRow + 6 * N * 4;              // [4][N] floats
   static constexpr int kBar = kRed + 4 * N * 4;
   static constexpr int kSmem = kBar + kBars * 8 + 1024;
-  static constexpr int kTmem = N == 16 ? 128 : 512;          // S^T twice, then O^T
+  static constexpr int kTmem = 8 * N;                        // S^T twice, then O^T
 };
 
 // What the softmax threads share of the rows.
@@ -77,45 +83,61 @@ struct Rows {
         lo(reinterpret_cast<int*>(f + N)), hi(lo + N) {}
 };
 
-// P's operand layout: a key's N f16 in a row of 2 N bytes, rows swizzled in
-// 2 N-byte patterns; byte offset of its 16-byte chunk c.
+// P's operand layout: a key's terms in a row of 4 N bytes, term by term; rows
+// of 64 (N = 16) or 128 bytes, swizzled (N = 64: two blocks of 128-byte rows).
+// Byte offset of 16-byte chunk c of a key.
 template <int N>
 __device__ __forceinline__ uint32_t p_off(int key, int c) {
-  return N == 64 ? key * 128 + ((c ^ (key & 7)) << 4) : key * 32 + ((c ^ ((key >> 2) & 1)) << 4);
+  if constexpr (N == 16) return key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
+  return (c >> 3) * (kKeys * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4);
 }
-template <int N>
-__device__ __forceinline__ uint64_t sdesc_p(uint32_t smem_addr) {
+
+// MN-major operand of e4m3 codes: rows of `row` (64 or 128) bytes along M or N
+// a key, swizzled in rows; 8-key atoms of 8 rows; the next block of rows `lead`
+// bytes on.
+__device__ __forceinline__ uint64_t sdesc_mn8(uint32_t smem_addr, uint32_t row, uint32_t lead) {
   uint64_t d = 0;
   d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(1u) << 16;  // (one swizzle pattern wide: no next block along N)
-  d |= static_cast<uint64_t>((8 * 2 * N) >> 4) << 32;
+  d |= static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((8 * row) >> 4) << 32;
   d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(N == 64 ? 2u : 6u) << 61;
+  d |= static_cast<uint64_t>(row == 128 ? 2u : 4u) << 61;
   return d;
 }
 
-// O^T[tmem] (+)= V^T[smem] P[smem] over 128 keys, 16 a step: both operands
-// MN-major, V 2048 bytes a step, P 32 N.
-template <int N>
+// O^T[tmem] (+)= V^T[smem] P[smem] over 128 keys, 32 a step: both operands
+// MN-major, VSTEP and PSTEP bytes a step.
+template <int VSTEP, int PSTEP>
 __device__ __forceinline__ void mma_ot(uint32_t d_tmem, uint64_t v_desc, uint64_t p_desc, uint32_t idesc,
                                        uint32_t first) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 v<8>, b<8>;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 v<4>, b<4>;\n\t"
       "setp.eq.b32 p, %4, 0;\n\t"
-      "add.s64 v1, %1, 128;\n\tadd.s64 v2, v1, 128;\n\tadd.s64 v3, v2, 128;\n\tadd.s64 v4, v3, 128;\n\t"
-      "add.s64 v5, v4, 128;\n\tadd.s64 v6, v5, 128;\n\tadd.s64 v7, v6, 128;\n\t"
-      "add.s64 b1, %2, %5;\n\tadd.s64 b2, b1, %5;\n\tadd.s64 b3, b2, %5;\n\tadd.s64 b4, b3, %5;\n\t"
-      "add.s64 b5, b4, %5;\n\tadd.s64 b6, b5, %5;\n\tadd.s64 b7, b6, %5;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], v1, b1, %3, 1;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], v2, b2, %3, 1;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], v3, b3, %3, 1;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], v4, b4, %3, 1;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], v5, b5, %3, 1;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], v6, b6, %3, 1;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], v7, b7, %3, 1;\n\t}" ::"r"(d_tmem),
-      "l"(v_desc), "l"(p_desc), "r"(idesc), "r"(first), "n"(static_cast<uint64_t>(32 * N) >> 4)
+      "add.s64 v1, %1, %5;\n\tadd.s64 v2, v1, %5;\n\tadd.s64 v3, v2, %5;\n\t"
+      "add.s64 b1, %2, %6;\n\tadd.s64 b2, b1, %6;\n\tadd.s64 b3, b2, %6;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], v1, b1, %3, 1;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], v2, b2, %3, 1;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], v3, b3, %3, 1;\n\t}" ::"r"(d_tmem),
+      "l"(v_desc), "l"(p_desc), "r"(idesc), "r"(first), "n"(static_cast<uint64_t>(VSTEP) >> 4),
+      "n"(static_cast<uint64_t>(PSTEP) >> 4)
       : "memory");
+}
+
+// Two weights as four e4m3 pairs: h = t0 + t1 / 16 + t2 / 256 + t3 / 4096.
+__device__ __forceinline__ void split_weights(float w0, float w1, uint16_t (&t)[4]) {
+  asm("{\n\t.reg .b32 h, k, n, b;\n\t"
+      "cvt.rn.f16x2.f32 h, %5, %4;\n\t"
+      "mov.b32 k, 0x4c004c00;\n\tmov.b32 n, 0xcc00cc00;\n\t"  // 16, -16
+      "cvt.rn.satfinite.e4m3x2.f16x2 %0, h;\n\tcvt.rn.f16x2.e4m3x2 b, %0;\n\t"
+      "mul.rn.f16x2 h, h, k;\n\tfma.rn.f16x2 h, b, n, h;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 %1, h;\n\tcvt.rn.f16x2.e4m3x2 b, %1;\n\t"
+      "mul.rn.f16x2 h, h, k;\n\tfma.rn.f16x2 h, b, n, h;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 %2, h;\n\tcvt.rn.f16x2.e4m3x2 b, %2;\n\t"
+      "mul.rn.f16x2 h, h, k;\n\tfma.rn.f16x2 h, b, n, h;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 %3, h;\n\t}"
+      : "=&h"(t[0]), "=&h"(t[1]), "=&h"(t[2]), "=&h"(t[3])
+      : "f"(w0), "f"(w1));
 }
 
 // S^T[tmem] = K[smem] Q[smem]^T, e4m3, 32 codes a step.
@@ -155,6 +177,20 @@ __device__ __forceinline__ void tmem_wait_ld16f(float* v) {
                : "memory");
 }
 
+// Two waits whose first looks overlap.
+__device__ __forceinline__ bool mbar_wait2(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, int* err) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(b0), "r"(p0), "r"(b1), "r"(p1)
+      : "memory");
+  return ok != 0 || (mbar_wait(b0, p0, err) && mbar_wait(b1, p1, err));
+}
+
 // Whether any of a softmax group's 128 threads says yes (a barrier among them).
 __device__ __forceinline__ bool vote(int group, bool yes) {
   uint32_t r;
@@ -168,9 +204,9 @@ __device__ __forceinline__ bool vote(int group, bool yes) {
 }
 
 template <int D, int N>
-__global__ void __launch_bounds__(Lay<D, N>::kThreads, N == 16 ? 2 : 1)
+__global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
     attn_few_kernel(const KvView c, const AttnArgs a, const AttnWs ws, const Plan pl,
-                    const __grid_constant__ CUtensorMap k_map) {
+                    const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using L_ = Lay<D, N>;
   using Io = typename L_::Io;
   extern __shared__ char smem_raw[];
@@ -193,14 +229,14 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, N == 16 ? 2 : 1)
 
   auto bar = [&](int i) { return base_u + L_::kBar + 8 * i; };
   if (threadIdx.x == 0) {
-    constexpr int kS = 128 * L_::kGroups;
-    const int count[kBars] = {kS, 1, 1, 1, L_::kGroups, L_::kGroups, L_::kGroups, 1, 1, 1, 128, 128, 128, 128, 128,
-                              1, 1, kS, kS, 1, 1, 8, 8, 8, 8, 1};
+    constexpr int kS = 128 * L_::kGroups, kG = L_::kGroups;
+    const int count[kBars] = {kS, 1, 1, 1, 1, kG, kG, kG, kG, 1, 1, 1, 1, 1, 1, 1, 1,
+                              1,  1, kS, 1, 8, 8, 8, 8, 8, 8, 8, 8, 1};
 #pragma unroll
     for (int i = 0; i < kBars; ++i) mbar_init(bar(i), count[i]);
     fence_barrier_init();
   }
-  constexpr int kConv = 4 * L_::kGroups, kMma = kConv + 4;  // first conversion warp, MMA warp; then the load warp
+  constexpr int kMma = 4 * L_::kGroups;  // the MMA warp; then the load warp
   if (warp == kMma) {
     tmem_alloc(smem_u32(&s_tmem), L_::kTmem);
     tmem_relinquish();
@@ -210,20 +246,21 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, N == 16 ? 2 : 1)
   fence_after_sync();
   const uint32_t tmem = s_tmem;
   const uint32_t ot = tmem + 4 * N;  // S^T: columns 0 .. 4 N - 1
-  const Io io{base_u + L_::kK, base_u + L_::kRaw, base_u + L_::kV, smem, base_u, base_u + L_::kConst,
-              bar(kKFull), bar(kKEmpty), bar(kRFull), bar(kREmpty), bar(kVFull), bar(kCFull)};
+  const Io io{base_u + L_::kK, base_u + L_::kV, 0, smem, base_u, base_u + L_::kConst,
+              bar(kKFull), bar(kKEmpty), bar(kVFull), bar(kVEmpty), 0, bar(kCFull)};
   const Rows<N> rows(smem + L_::kRow);
 
   if (warp == kMma + 1) {
-    if (lane < 8 && n > 0) io.load(c, a, w.k, b, hk, t_begin, n, &k_map, lane);
+    if (lane < 8 && n > 0) io.load(c, a, w.k, b, hk, t_begin, n, &k_map, &v_map, lane);
   } else if (warp == kMma) {
     if (lane == 0 && n > 0) {
       constexpr uint32_t id_s = idesc_f16(kKeys, 2 * N);                      // e4m3 is format 0 of its kind, too
-      constexpr uint32_t id_o = idesc_f16(128, N) | (1u << 15) | (1u << 16);  // both MN-major
+      constexpr uint32_t id_o = idesc_f16(128, 4 * N) | (1u << 15) | (1u << 16);  // both MN-major
       const uint64_t q_desc = sdesc_k<D>(base_u + L_::kQ), k_desc = sdesc_k<D>(base_u + L_::kK);
-      // heads of 64: the accumulator's other 64 rows take what lies behind, and are not read
-      const uint64_t v_desc = sdesc_sw128_mn(base_u + L_::kV, D == 128 ? Io::kHalf : 1024);
-      const uint64_t p_desc = sdesc_p<N>(base_u + L_::kP);
+      // heads of 64: the accumulator's other 64 rows take the codes one atom on, and are not read
+      const uint64_t v_desc = sdesc_mn8(base_u + L_::kV, D, 8 * D);
+      const uint64_t p_desc = sdesc_mn8(base_u + L_::kP, N == 16 ? 64 : 128, kKeys * 128);
+      constexpr int kVStep = 32 * D, kPStep = 32 * (N == 16 ? 64 : 128);
       auto issue_s = [&](int j) {
         const int ks = j % L_::kStages;
         if (!mbar_wait(bar(kKFull + ks), (j / L_::kStages) & 1, c.err)) return false;
@@ -234,13 +271,12 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, N == 16 ? 2 : 1)
       };
       bool ok = mbar_wait(bar(kQFull), 0, c.err) && issue_s(0) && (n < 2 || issue_s(1));
       for (int j = 0; ok && j < n; ++j) {
-        const int vs = j % L_::kVStages;
-        ok = mbar_wait(bar(kPFull + (j & 1)), (j >> 1) & 1, c.err) &&
-             mbar_wait(bar(kVFull + vs), (j / L_::kVStages) & 1, c.err);
+        const int vs = j % L_::kStages;
+        ok = mbar_wait(bar(kPFull), j & 1, c.err) && mbar_wait(bar(kVFull + vs), (j / L_::kStages) & 1, c.err);
         if (!ok) break;
         fence_after_sync();
-        mma_ot<N>(ot, v_desc + vs * (Io::kMat >> 4), p_desc + (j & 1) * (kKeys * 2 * N >> 4), id_o, j == 0);
-        mma_commit(bar(kODone + (j & 1)));
+        mma_ot<kVStep, kPStep>(ot, v_desc + vs * (Io::kMat8 >> 4), p_desc, id_o, j == 0);
+        mma_commit(bar(kODone));
         ok = j + 2 >= n || issue_s(j + 2);
       }
       if (!ok) {
@@ -249,15 +285,9 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, N == 16 ? 2 : 1)
         mbar_wait(bar(kDrain), 0, c.err);
       }
     }
-  } else if (warp >= kConv) {
-    // the stage of tile j - VS is free when its product is done
-    io.convert(c, a, w.k, t_begin, n, threadIdx.x - 32 * kConv, [&](int j) {
-      const int i = j - L_::kVStages;
-      return mbar_wait(bar(kODone + (i & 1)), (i >> 1) & 1, c.err);
-    });
   } else {
     // ---- softmax: thread t is key t of a tile -----------------------------------
-    constexpr int NG = L_::kGroupRows;
+    constexpr int NG = 16;
     const int t = threadIdx.x & 127, grp = warp >> 2, g0 = grp * NG;  // rows g0 .. of the group
     float l[NG];
 #pragma unroll
@@ -313,61 +343,57 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, N == 16 ? 2 : 1)
       fence_proxy_async_smem();
       mbar_arrive(bar(kQFull));
     }
-    named_sync(3, 128 * L_::kGroups);
+    named_sync(8, 128 * L_::kGroups);
     const int p_lo = w.base_p + w.r0 / a.G, p_hi = w.base_p + (w.r1 - 1) / a.G;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 * (warp % 4)
     float* red = reinterpret_cast<float*>(smem + L_::kRed);
     bool ok = true, pending = true;  // a row has no reference yet
     for (int j = 0; j < n; ++j) {
-      const int bf = j & 1, ph = (j >> 1) & 1;
-      ok = mbar_wait(bar(kSFull + bf), ph, c.err) &&
-           mbar_wait(bar(kCFull + j % kConstRing), (j / kConstRing) & 1, c.err) &&
-           // P of tile j - 2 has been read
-           (j < 2 || mbar_wait(bar(kODone + bf), ph ^ 1, c.err));
-      ok = __all_sync(0xffffffffu, ok);
-      if (vote(grp, !ok)) {
-        ok = false;
-        break;
-      }
+      const int bf = j & 1;
+      // (a thread whose wait gave up waits no more; the vote below ends the loop)
+      ok = ok && mbar_wait2(bar(kSFull + bf), (j >> 1) & 1, bar(kCFull + j % kConstRing), (j / kConstRing) & 1, c.err);
+      __syncwarp();
       fence_after_sync();
-      if (t == 0) mbar_arrive(bar(kKEmpty + j % L_::kStages));
+      const uint32_t st = tmem + bf * 2 * N + lanes + g0;
+      float z[NG], s2[NG];
+      tmem_ld16f(st, z);
+      tmem_ld16f(st + N, s2);
       const float4 cn = io.scales(j)[t >> 4];
       const float ks = fmaxf(cn.x, kTiny);
       const int tok = w.k.base(t_begin + j) + t, key0 = tok - t;
       const bool whole = (a.causal ? key0 + kKeys <= p_lo + 1 : key0 + kKeys <= w.q.L) &&
                          (a.window == 0 || key0 > p_hi - a.window || key0 + kKeys <= a.sinks);
       // exponents relative to the rows' references
-      float z[NG];
       float top = -INFINITY;
-      const uint32_t st = tmem + bf * 2 * N + lanes + g0;
+      tmem_wait_ld16f(z);
+      tmem_wait_ld16f(s2);
 #pragma unroll
-      for (int x = 0; x < NG; x += 16) {
-        float s2[16];
-        tmem_ld16f(st + x, z + x);
-        tmem_ld16f(st + N + x, s2);
-        tmem_wait_ld16f(z + x);
-        tmem_wait_ld16f(s2);
-#pragma unroll
-        for (int r = 0; r < 16; r += 4) {
-          const float4 ls = *reinterpret_cast<const float4*>(rows.lscale + g0 + x + r);
-          const float4 nr = *reinterpret_cast<const float4*>(rows.nref + g0 + x + r);
-          float* y = z + x + r;
-          y[0] = fmaf((y[0] + s2[r]) * ks, ls.x, cn.y) + nr.x;
-          y[1] = fmaf((y[1] + s2[r + 1]) * ks, ls.y, cn.y) + nr.y;
-          y[2] = fmaf((y[2] + s2[r + 2]) * ks, ls.z, cn.y) + nr.z;
-          y[3] = fmaf((y[3] + s2[r + 3]) * ks, ls.w, cn.y) + nr.w;
-        }
-        if (!whole) {
-#pragma unroll
-          for (int r = x; r < x + 16; ++r) {
-            const bool sees = tok <= rows.hi[g0 + r] && (tok >= rows.lo[g0 + r] || tok < a.sinks);
-            z[r] = sees ? z[r] : -INFINITY;
-          }
-        }
-#pragma unroll
-        for (int r = x; r < x + 16; r += 2) top = max3(top, z[r], z[r + 1]);
+      for (int r = 0; r < NG; r += 4) {
+        const float4 ls = *reinterpret_cast<const float4*>(rows.lscale + g0 + r);
+        const float4 nr = *reinterpret_cast<const float4*>(rows.nref + g0 + r);
+        float* y = z + r;
+        add2(y[0], y[1], s2[r], s2[r + 1]);
+        add2(y[2], y[3], s2[r + 2], s2[r + 3]);
+        float m0, m1, m2, m3, b0 = nr.x, b1 = nr.y, b2 = nr.z, b3 = nr.w;
+        mul2(m0, m1, ls.x, ls.y, ks);
+        mul2(m2, m3, ls.z, ls.w, ks);
+        add2(b0, b1, cn.y, cn.y);
+        add2(b2, b3, cn.y, cn.y);
+        fma2(y[0], y[1], y[0], y[1], m0, m1, b0, b1);
+        fma2(y[2], y[3], y[2], y[3], m2, m3, b2, b3);
       }
-      if (vote(grp, pending || top > kLift + kRescale)) {
+      if (!whole) {
+#pragma unroll
+        for (int r = 0; r < NG; ++r) {
+          const bool sees = tok <= rows.hi[g0 + r] && (tok >= rows.lo[g0 + r] || tok < a.sinks);
+          z[r] = sees ? z[r] : -INFINITY;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < NG; r += 2) top = max3(top, z[r], z[r + 1]);
+      if (vote(grp, pending || top > kFewLift + kFewRescale || !ok)) {
+        ok = !vote(grp, !ok);
+        if (!ok) break;
         // some reference moves: the rows' maxima over the tile, warp by warp
 #pragma unroll
         for (int r = 0; r < NG; ++r) {
@@ -380,12 +406,12 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, N == 16 ? 2 : 1)
           const int q = g0 + t;
           const float mx = fmaxf(fmaxf(red[q], red[N + q]), fmaxf(red[2 * N + q], red[3 * N + q])) - rows.nref[q];
           const float m = rows.m[q];
-          const bool move = mx > m + kRescale;
+          const bool move = mx > m + kFewRescale;
           const float nm = move ? mx : m;
           rows.f[q] = move ? ex2(m - nm) : 1.f;
-          red[q] = move ? (kLift - nm) - rows.nref[q] : 0.f;  // what the exponents change by
+          red[q] = move ? (kFewLift - nm) - rows.nref[q] : 0.f;  // what the exponents change by
           rows.m[q] = nm;
-          if (move) rows.nref[q] = kLift - nm;
+          if (move) rows.nref[q] = kFewLift - nm;
         }
         named_sync(1 + grp, 128);
 #pragma unroll
@@ -394,38 +420,58 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, N == 16 ? 2 : 1)
           l[r] *= rows.f[g0 + r];
         }
         if (j > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(kODone + (bf ^ 1)), ((j - 1) >> 1) & 1, c.err));
+          ok = mbar_wait(bar(kODone), (j - 1) & 1, c.err);
+          __syncwarp();
           fence_after_sync();
 #pragma unroll
-          for (int x = 0; x < NG; x += 16) {
+          for (int x = 0; x < 4; ++x) {
             uint32_t u[16];
-            tmem_ld16(ot + lanes + g0 + x, u);
+            tmem_ld16(ot + lanes + x * N + g0, u);
             tmem_wait_ld16(u);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) u[r] = __float_as_uint(__uint_as_float(u[r]) * rows.f[g0 + x + r]);
-            tmem_st16(ot + lanes + g0 + x, u);
+            for (int r = 0; r < 16; ++r) u[r] = __float_as_uint(__uint_as_float(u[r]) * rows.f[g0 + r]);
+            tmem_st16(ot + lanes + x * N + g0, u);
           }
           tmem_wait_st();
         }
         // (a barrier, too: red and f are free again)
         pending = vote(grp, t < NG && rows.m[g0 + t % NG] == -INFINITY && rows.hi[g0 + t % NG] >= 0);
       }
-      char* p = smem + L_::kP + bf * (kKeys * 2 * N);
+      // the weights, and their terms: row pairs of term i in u[i]
+      uint32_t u[4][4];
 #pragma unroll
-      for (int x = 0; x < NG; x += 8) {
-        uint32_t u[4];
+      for (int r = 0; r < NG; r += 4) {
+        uint16_t t0[4], t1[4];
+        const float w0 = ex2(z[r]), w1 = ex2(z[r + 1]), w2 = ex2(z[r + 2]), w3 = ex2(z[r + 3]);
+        fma2(l[r], l[r + 1], w0, w1, cn.z, cn.z, l[r], l[r + 1]);
+        fma2(l[r + 2], l[r + 3], w2, w3, cn.z, cn.z, l[r + 2], l[r + 3]);
+        split_weights(w0, w1, t0);
+        split_weights(w2, w3, t1);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float w0 = ex2(z[x + 2 * r]), w1 = ex2(z[x + 2 * r + 1]);
-          l[x + 2 * r] = fmaf(w0, cn.z, l[x + 2 * r]);
-          l[x + 2 * r + 1] = fmaf(w1, cn.z, l[x + 2 * r + 1]);
-          u[r] = half2_bits(w0, w1);
-        }
-        *reinterpret_cast<uint4*>(p + p_off<N>(t, (g0 + x) >> 3)) = make_uint4(u[0], u[1], u[2], u[3]);
+        for (int i = 0; i < 4; ++i) u[i][r >> 2] = t0[i] | (static_cast<uint32_t>(t1[i]) << 16);
       }
+      if (grp == 0 && !whole) {
+        // the values that no row sees are zero: a NaN code there would reach the rows through 0 * NaN
+        ok = ok && mbar_wait(bar(kVFull + j % L_::kStages), (j / L_::kStages) & 1, c.err);
+        if (!(tok < w.k.hi && (tok >= w.k.lo || tok < a.sinks))) {
+          uint4* v = reinterpret_cast<uint4*>(smem + L_::kV + (j % L_::kStages) * Io::kMat8 + t * D);
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) v[x] = make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+      }
+      if (j > 0) ok = ok && mbar_wait(bar(kODone), (j - 1) & 1, c.err);  // P of the tile before has been read
+      if (t == 0) {  // through with K of this tile and, once for all groups, with V of the one before
+        mbar_arrive(bar(kKEmpty + j % L_::kStages));
+        if (grp == 0 && j > 0) mbar_arrive(bar(kVEmpty + (j - 1) % L_::kStages));
+      }
+      char* p = smem + L_::kP;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(p + p_off<N>(t, (i * N + g0) >> 4)) = make_uint4(u[i][0], u[i][1], u[i][2], u[i][3]);
       fence_proxy_async_smem();
       fence_before_sync();
-      mbar_arrive(bar(kPFull + bf));
+      mbar_arrive(bar(kPFull));
     }
     // the weights' sums over the keys
 #pragma unroll
@@ -435,42 +481,44 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, N == 16 ? 2 : 1)
       if (lane == 0) red[(warp & 3) * N + g0 + r] = l[r];
     }
     if (ok && n > 0)
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(kODone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, c.err));
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(kODone), (n - 1) & 1, c.err));
     named_sync(1 + grp, 128);
     fence_after_sync();
     // thread t has dim t of every row
     const size_t tile_id = (static_cast<size_t>(b) * c.hkv + hk) * pl.row_tiles + rt;
     const size_t prow = (tile_id * pl.splits + split) * N;
     const int live = w.r1 - w.r0;
+    float o[NG];
 #pragma unroll
-    for (int x = 0; x < NG; x += 16) {
-      float o[16];
-      if (n > 0 && ok) {
-        tmem_ld16f(ot + lanes + g0 + x, o);
-        tmem_wait_ld16f(o);
-      } else {
+    for (int r = 0; r < NG; ++r) o[r] = 0.f;
+    if (n > 0 && ok) {
+      // the terms' columns, the smallest first
 #pragma unroll
-        for (int r = 0; r < 16; ++r) o[r] = 0.f;
+      for (int i = 3; i >= 0; --i) {
+        float y[NG];
+        tmem_ld16f(ot + lanes + i * N + g0, y);
+        tmem_wait_ld16f(y);
+#pragma unroll
+        for (int r = 0; r < NG; ++r) o[r] = fmaf(o[r], 0.0625f, y[r]);
       }
+    }
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int row = g0 + x + r;
-        if (row < live && t < D) {
-          const float ll = (red[row] + red[N + row]) + (red[2 * N + row] + red[3 * N + row]);
-          if (w.n_split == 1) {
-            const int gr = w.r0 + row, tk = gr / a.G;
-            const size_t orow = (static_cast<size_t>(w.q.q0) + tk) * a.hq + hk * a.G + gr - tk * a.G;
-            const bool any = ll > 0.f || ll != ll;
-            a.out[orow * D + t] = __float2bfloat16_rn(any ? o[r] / ll : 0.f);
-            if (a.lse && t == 0)
-              a.lse[orow] = any ? (rows.m[row] - kLift + log2f(ll)) * 0.693147180559945f : -INFINITY;
-          } else {
-            ws.o[(prow + row) * D + t] = o[r];
-            if (t == 0) ws.ml[prow + row] = make_float2(rows.m[row], ll);
-          }
+    for (int r = 0; r < NG; ++r) {
+      const int row = g0 + r;
+      if (row < live && t < D) {
+        const float ll = (red[row] + red[N + row]) + (red[2 * N + row] + red[3 * N + row]);
+        const float mm = rows.m[row] + (kLift - kFewLift);  // as the other kernels count
+        if (w.n_split == 1) {
+          const int gr = w.r0 + row, tk = gr / a.G;
+          const size_t orow = (static_cast<size_t>(w.q.q0) + tk) * a.hq + hk * a.G + gr - tk * a.G;
+          const bool any = ll > 0.f || ll != ll;
+          a.out[orow * D + t] = __float2bfloat16_rn(any ? o[r] / ll : 0.f);
+          if (a.lse && t == 0) a.lse[orow] = any ? (mm - kLift + log2f(ll)) * 0.693147180559945f : -INFINITY;
+        } else {
+          ws.o[(prow + row) * D + t] = o[r];
+          if (t == 0) ws.ml[prow + row] = make_float2(mm, ll);
         }
       }
-      __syncwarp();
     }
     if (w.n_split > 1) __threadfence();
   }
@@ -497,8 +545,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, N == 16 ? 2 : 1)
 }
 
 template <int D, int N>
-cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const CUtensorMap& k_map, int n_sm,
-                   cudaStream_t s) {
+cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const KvMaps& maps, int n_sm, cudaStream_t s) {
   static std::atomic<size_t> done[kMaxDevices];
   const void* fn = reinterpret_cast<const void*>(attn_few_kernel<D, N>);
   if (const cudaError_t e = opt_in_smem(fn, done, Lay<D, N>::kSmem); e != cudaSuccess) return e;
@@ -507,13 +554,15 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const C
   pl.row_tiles = static_cast<int>((rows + N - 1) / N);
   const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
   const int64_t tiles = max_key_tiles(c, a, N, kKeys);
-  const int64_t resident = static_cast<int64_t>(n_sm) * (N == 16 ? 2 : 1);
-  const int64_t splits = best_splits(base, resident, tiles, static_cast<int64_t>(ws.cap_rows) / (base * N));
+  const int64_t resident = static_cast<int64_t>(n_sm) * Lay<D, N>::kCtas;
+  const int64_t splits = best_splits(base, resident, tiles, static_cast<int64_t>(ws.cap_rows) / (base * N),
+                                     false);
   pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
   pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
   const int64_t grid = base * pl.splits;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  attn_few_kernel<D, N><<<static_cast<unsigned>(grid), Lay<D, N>::kThreads, Lay<D, N>::kSmem, s>>>(c, a, ws, pl, k_map);
+  attn_few_kernel<D, N><<<static_cast<unsigned>(grid), Lay<D, N>::kThreads, Lay<D, N>::kSmem, s>>>(c, a, ws, pl,
+                                                                                                     maps.k_tile, maps.v_tile);
   return cudaGetLastError();
 }
 
@@ -521,10 +570,10 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const C
 
 cudaError_t attn_few_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const KvMaps& maps,
                             int n_sm, cudaStream_t s) {
-  const bool small = static_cast<int64_t>(c.max_q) * a.G <= 16;
+  const int64_t rows = static_cast<int64_t>(c.max_q) * a.G;
   if (c.D == 128)
-    return small ? launch<128, 16>(c, a, ws, maps.k_tile, n_sm, s) : launch<128, 64>(c, a, ws, maps.k_tile, n_sm, s);
-  return small ? launch<64, 16>(c, a, ws, maps.k_tile, n_sm, s) : launch<64, 64>(c, a, ws, maps.k_tile, n_sm, s);
+    return (rows <= 16 ? launch<128, 16> : rows <= 32 ? launch<128, 32> : launch<128, 64>)(c, a, ws, maps, n_sm, s);
+  return (rows <= 16 ? launch<64, 16> : rows <= 32 ? launch<64, 32> : launch<64, 64>)(c, a, ws, maps, n_sm, s);
 }
 
 }  // namespace moe

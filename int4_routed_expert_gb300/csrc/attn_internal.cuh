@@ -99,10 +99,10 @@ cudaError_t kv_read_launch(const KvView& c, void* k, void* v, moe_dtype_t dt, cu
 cudaError_t attn_rows_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, int n_sm,
                              cudaStream_t s);
 
-// TMA map of the key codes as [n_pages][n_kv_heads * page_size][D] bytes, boxes
+// TMA maps of the code arrays as [n_pages][n_kv_heads * page_size][D] bytes, boxes
 // of one page of one head, swizzled in D-byte rows.
 struct KvMaps {
-  CUtensorMap k_tile;
+  CUtensorMap k_tile, v_tile;
 };
 bool kv_create_maps(const moe_kv_config_t& cfg, const moe_kv_store_t& st, KvMaps* m);
 cudaError_t attn_few_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const KvMaps& maps,

@@ -14,7 +14,7 @@ namespace moe {
 using namespace tc;
 
 constexpr int kKeys = 128;       // keys of a tile
-constexpr int kConstRing = 4;    // tiles whose blocks' scales are kept
+constexpr int kConstRing = 8;    // tiles whose blocks' scales are kept
 constexpr float kTiny = 1e-37f;  // keeps what is hidden at -inf where a block's scale is 0
 
 // The one thread that issues products is on every step's path: the MMAs of a
@@ -142,6 +142,22 @@ __device__ __forceinline__ void add2(float& x, float& y, float a0, float a1) {
       : "+f"(x), "+f"(y)
       : "f"(a0), "f"(a1));
 }
+// (x, y) = (a0, a1) * (b0, b1) + (c0, c1)
+__device__ __forceinline__ void fma2(float& x, float& y, float a0, float a1, float b0, float b1, float c0,
+                                     float c1) {
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mul2(float& x, float& y, float a0, float a1, float b) {
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %4};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "f"(a0), "f"(a1), "f"(b));
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -151,9 +167,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // ---- tiles of keys into shared memory ---------------------------------------------
 //
 // KS stages of key codes in the swizzled operand layout, RS stages of value
-// codes as they lie, VS stages of values in f16 in the swizzled layout
-// [D / 64][128 keys][128 bytes], and a ring of the blocks' scales by groups of
-// 16 keys: {key scale, log2 value scale, 1 / value scale, 0}.
+// codes (VS = 0: in the same layout; else as they lie, and VS stages of values
+// in f16 in the swizzled layout [D / 64][128 keys][128 bytes]), and a ring of
+// the blocks' scales by groups of 16 keys: {key scale, log2 value scale,
+// 1 / value scale, 0}.
 template <int D, int KS, int RS, int VS>
 struct TileIo {
   static constexpr int kMat8 = kKeys * D;
@@ -175,7 +192,8 @@ struct TileIo {
   // the softmax, which then also is through with the scales of the tile
   // kConstRing - KS before.
   __device__ __forceinline__ void load(const KvView& c, const AttnArgs& a, const KeyTiles& kt, int b, int hk,
-                                       int t_begin, int n, const CUtensorMap* k_map, int lane) const {
+                                       int t_begin, int n, const CUtensorMap* k_map, const CUtensorMap* v_map,
+                                       int lane) const {
     static_assert(kConstRing > KS, "the ring outlives the key stages");
     const int t_end = t_begin + n;
     bool ok = true, bad = false;
@@ -223,7 +241,9 @@ struct TileIo {
       if (!ok) break;
       if (lane == 0) mbar_arrive_expect_tx(r_full + 8 * rs, total);
       __syncwarp(0xffu);
-      if (copies)
+      if (copies && VS == 0)
+        tma_load_3d(raw + rs * kMat8 + 16 * lane * D, v_map, 0, hk * c.page, page, r_full + 8 * rs);
+      if (copies && VS != 0)
         bulk_g2s(raw + rs * kMat8 + 16 * lane * D, c.v + (static_cast<size_t>(page) * c.hkv + hk) * bytes, bytes,
                  r_full + 8 * rs);
       r_sent = j + 1;
@@ -255,23 +275,26 @@ struct TileIo {
       const int base_key = kt.base(t_begin + j);
       const bool whole = base_key + kKeys <= kt.hi && (base_key >= kt.lo || base_key + kKeys <= a.sinks);
       const char* src = smem + (raw - base) + rs * kMat8 + tid * 16;
+      const char* src0 = src + (swap ? 8 : 0);
+      const char* src1 = src + (swap ? 0 : 8);
       char* dst = smem + (v - base) + vs * kMat;
 #pragma unroll
       for (int p = 0; p < kKeys / kPer; ++p) {
-        uint4 u = *reinterpret_cast<const uint4*>(src + p * 2048);
+        uint2 u0 = *reinterpret_cast<const uint2*>(src0 + p * 2048);
+        uint2 u1 = *reinterpret_cast<const uint2*>(src1 + p * 2048);
         if (!whole) {
           // what no row sees is zero: a NaN there would reach the rows through 0 * NaN
           const int tok = base_key + p * kPer + row0;
-          if (!(tok < kt.hi && (tok >= kt.lo || tok < a.sinks))) u = make_uint4(0, 0, 0, 0);
+          if (!(tok < kt.hi && (tok >= kt.lo || tok < a.sinks))) u0 = u1 = make_uint2(0, 0);
         }
-        uint4 lo, hi;
-        codes_to_half(u.x, lo.x, lo.y);
-        codes_to_half(u.y, lo.z, lo.w);
-        codes_to_half(u.z, hi.x, hi.y);
-        codes_to_half(u.w, hi.z, hi.w);
+        uint4 h0, h1;
+        codes_to_half(u0.x, h0.x, h0.y);
+        codes_to_half(u0.y, h0.z, h0.w);
+        codes_to_half(u1.x, h1.x, h1.y);
+        codes_to_half(u1.y, h1.z, h1.w);
         // (kPer is a multiple of 8: the swizzle of a later pass is the first's)
-        *reinterpret_cast<uint4*>(dst + o0 + p * kPer * 128) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(dst + o1 + p * kPer * 128) = swap ? lo : hi;
+        *reinterpret_cast<uint4*>(dst + o0 + p * kPer * 128) = h0;
+        *reinterpret_cast<uint4*>(dst + o1 + p * kPer * 128) = h1;
       }
       fence_proxy_async_smem();
       mbar_arrive(v_full + 8 * vs);
@@ -297,14 +320,21 @@ struct Plan {
 
 // Splits of `tiles` tiles for `base` row tiles on `resident` CTA slots, at most
 // `most`: the fewest tile times, a CTA costing kCtaTiles beside its own (start,
-// first loads, results).
-inline int64_t best_splits(int64_t base, int64_t resident, int64_t tiles, int64_t most) {
+// first loads, results).  Several sequences may be shorter than the bound that
+// `tiles` comes from: the finest cut within a sixteenth of the best one then.
+inline int64_t best_splits(int64_t base, int64_t resident, int64_t tiles, int64_t most, bool ragged) {
   constexpr int64_t kCtaTiles = 3;
-  int64_t best = 1, cost = INT64_MAX;
-  for (int64_t s = 1; s <= std::min<int64_t>({tiles, most, 256}) || s == 1; ++s) {
-    const int64_t c = (base * s + resident - 1) / resident * ((tiles + s - 1) / s + kCtaTiles);
-    if (c < cost) cost = c, best = s;
-  }
+  const int64_t end = std::max<int64_t>(std::min<int64_t>({tiles, most, 256}), 1);
+  auto cost = [&](int64_t s) {
+    return (base * s + resident - 1) / resident * ((tiles + s - 1) / s + kCtaTiles);
+  };
+  int64_t least = INT64_MAX, best = 1;
+  for (int64_t s = 1; s <= end; ++s) least = std::min(least, cost(s));
+  for (int64_t s = 1; s <= end; ++s)
+    if (cost(s) * 16 <= least * (ragged ? 17 : 16)) {
+      best = s;
+      if (!ragged) break;
+    }
   return best;
 }
 

@@ -59,9 +59,9 @@ enum Bar {
   kSFull = 15,   // [2] by M tile
   kPFull = 17,
   kOFull = 19,   // [2]
-  kCFull = 21,   // [4] scales
-  kDrain = 25,
-  kBars = 26
+  kCFull = 21,   // [8] scales
+  kDrain = 29,
+  kBars = 30
 };
 
 template <int D>
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return base_u + L_::kBar + 8 * i; };
   if (threadIdx.x == 0) {
     const int count[kBars] = {128 * n_mt, 1, 1, 1, 1, 1, 1, 1, 1, 128, 128, 128, 128,
-                              1, 1, 1, 1, 128, 128, 1, 1, 8, 8, 8, 8, 1};
+                              1, 1, 1, 1, 128, 128, 1, 1, 8, 8, 8, 8, 8, 8, 8, 8, 1};
 #pragma unroll
     for (int i = 0; i < kBars; ++i) mbar_init(bar(i), count[i]);
     fence_barrier_init();
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Io<D> io{base_u + L_::kK, base_u + L_::kRaw, base_u + L_::kV, smem, base_u, base_u + L_::kConst,
                  bar(kKFull), bar(kKEmpty), bar(kRFull), bar(kREmpty), bar(kVFull), bar(kCFull)};
   if (warp == 13) {
-    if (lane < 8 && n > 0) io.load(c, a, w.k, b, hk, t_begin, n, &k_map, lane);
+    if (lane < 8 && n > 0) io.load(c, a, w.k, b, hk, t_begin, n, &k_map, nullptr, lane);
   } else if (warp == 12) {
     if (lane == 0 && n > 0) {
       constexpr uint32_t id_s = idesc_f16(kM, kKeys);           // e4m3 is format 0 of its kind, too
@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int p_lo = w.base_p + w.r0 / a.G, p_hi = w.base_p + (w.r1 - 1) / a.G;
     for (int j = 0; j < n; ++j) {
       // (S of this tile says that O += P V of the tile before is done, too)
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(kCFull + (j & 3)), (j >> 2) & 1, c.err) &&
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(kCFull + j % kConstRing), (j / kConstRing) & 1, c.err) &&
                                        mbar_wait(bar(kSFull + i), j & 1, c.err));
       if (!ok) break;
       fence_after_sync();
