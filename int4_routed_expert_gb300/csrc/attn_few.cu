@@ -15,9 +15,9 @@
 //   P[128 keys x 4 N]                            a thread a key
 //   O^T[128 dims x 4 N]  += V^T [P1 P2 P3 P4]    V as it lies (M-major)
 // A weight is rounded to f16 (11 bits) and cut into e4m3 terms of 4 bits, term
-// i scaled by 16^(i - 1) into its own accumulator columns: exact for weights
-// above 2^-10 of the row's largest, and to 2^-30 of the largest below (the
-// lift of 7 and the reference within 2 of the largest see to that).  So no
+// i scaled by 32^(i - 1) into its own accumulator columns: exact for weights
+// above 2^-15 of the row's largest, and to 2^-29 of the largest below (the
+// lift of 5 and the reference within 2^3 of the largest see to that).  So no
 // value is converted, shared memory carries each code once in and once out,
 // and the extra columns are free: with the keys and dims in M the products are
 // bound by reading K and V, whatever N is.  A thread's block scales are
@@ -33,7 +33,7 @@ namespace moe {
 namespace {
 
 
-constexpr float kFewLift = 7.f, kFewRescale = 1.f;  // weights below 2^8: an e4m3 ends at 448
+constexpr float kFewLift = 5.f, kFewRescale = 3.f;  // weights below 2^8: an e4m3 ends at 448
 
 enum Bar {
   kQFull = 0,
@@ -42,18 +42,18 @@ enum Bar {
   kVFull = 9,    // [4] value codes
   kVEmpty = 13,  // [4]
   kSFull = 17,   // [2] S^T
-  kPFull = 19,   // P
-  kODone = 20,   // O^T += V^T P
-  kCFull = 21,   // [8] scales
-  kDrain = 29,
-  kBars = 30
+  kPFull = 19,   // [2] P
+  kODone = 21,   // [2] O^T += V^T P, by buffer of P
+  kCFull = 23,   // [8] scales
+  kDrain = 31,
+  kBars = 32
 };
 
 // Up to 32 rows keep to half an SM, so that two CTAs cover each other's bubbles.
 template <int D, int N>
 struct Lay {
   static constexpr int kStages = N == 16 ? 3 : N == 32 ? 2 : 4;  // of key codes and of value codes
-  static constexpr int kCtas = N == 64 ? 1 : 2;                  // a SM
+  static constexpr int kCtas = N == 64 ? 1 : 2;  // a SM
   using Io = TileIo<D, kStages, kStages, 0>;
   static constexpr int kGroups = N / 16;  // softmax groups of 128 threads
   static constexpr int kThreads = 128 * kGroups + 64;
@@ -61,7 +61,8 @@ struct Lay {
   static constexpr int kK = kQ + (2 * N * D + 1023) / 1024 * 1024;
   static constexpr int kV = kK + kStages * Io::kMat8;
   static constexpr int kP = kV + kStages * Io::kMat8;  // [128 keys][4 N]
-  static constexpr int kConst = kP + kKeys * 4 * N;
+  static constexpr int kPs = N == 64 ? 2 : 1;  // buffers of P
+  static constexpr int kConst = kP + kPs * kKeys * 4 * N;
   static constexpr int kRow = kConst + kConstRing * 8 * 16;  // [6][N]: see Rows
   static constexpr int kRed = kRow + 6 * N * 4;              // [4][N] floats
   static constexpr int kBar = kRed + 4 * N * 4;
@@ -124,11 +125,12 @@ __device__ __forceinline__ void mma_ot(uint32_t d_tmem, uint64_t v_desc, uint64_
       : "memory");
 }
 
-// Two weights as four e4m3 pairs: h = t0 + t1 / 16 + t2 / 256 + t3 / 4096.
+// Two weights below 2^8 as four e4m3 pairs: h = t0 + t1 / 32 + t2 / 32^2 + t3 / 32^3
+// (a term is off by at most 2^-5 of its binade, 8 at 2^8, and 8 * 32 is below 448).
 __device__ __forceinline__ void split_weights(float w0, float w1, uint16_t (&t)[4]) {
   asm("{\n\t.reg .b32 h, k, n, b;\n\t"
       "cvt.rn.f16x2.f32 h, %5, %4;\n\t"
-      "mov.b32 k, 0x4c004c00;\n\tmov.b32 n, 0xcc00cc00;\n\t"  // 16, -16
+      "mov.b32 k, 0x50005000;\n\tmov.b32 n, 0xd000d000;\n\t"  // 32, -32
       "cvt.rn.satfinite.e4m3x2.f16x2 %0, h;\n\tcvt.rn.f16x2.e4m3x2 b, %0;\n\t"
       "mul.rn.f16x2 h, h, k;\n\tfma.rn.f16x2 h, b, n, h;\n\t"
       "cvt.rn.satfinite.e4m3x2.f16x2 %1, h;\n\tcvt.rn.f16x2.e4m3x2 b, %1;\n\t"
@@ -231,7 +233,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
   if (threadIdx.x == 0) {
     constexpr int kS = 128 * L_::kGroups, kG = L_::kGroups;
     const int count[kBars] = {kS, 1, 1, 1, 1, kG, kG, kG, kG, 1, 1, 1, 1, 1, 1, 1, 1,
-                              1,  1, kS, 1, 8, 8, 8, 8, 8, 8, 8, 8, 1};
+                              1,  1, kS, kS, 1, 1, 8, 8, 8, 8, 8, 8, 8, 8, 1};
 #pragma unroll
     for (int i = 0; i < kBars; ++i) mbar_init(bar(i), count[i]);
     fence_barrier_init();
@@ -272,11 +274,12 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
       bool ok = mbar_wait(bar(kQFull), 0, c.err) && issue_s(0) && (n < 2 || issue_s(1));
       for (int j = 0; ok && j < n; ++j) {
         const int vs = j % L_::kStages;
-        ok = mbar_wait(bar(kPFull), j & 1, c.err) && mbar_wait(bar(kVFull + vs), (j / L_::kStages) & 1, c.err);
+        ok = mbar_wait(bar(kPFull + j % L_::kPs), (j / L_::kPs) & 1, c.err) && mbar_wait(bar(kVFull + vs), (j / L_::kStages) & 1, c.err);
         if (!ok) break;
         fence_after_sync();
-        mma_ot<kVStep, kPStep>(ot, v_desc + vs * (Io::kMat8 >> 4), p_desc, id_o, j == 0);
-        mma_commit(bar(kODone));
+        mma_ot<kVStep, kPStep>(ot, v_desc + vs * (Io::kMat8 >> 4),
+                             p_desc + j % L_::kPs * (kKeys * 4 * N >> 4), id_o, j == 0);
+        mma_commit(bar(kODone + j % L_::kPs));
         ok = j + 2 >= n || issue_s(j + 2);
       }
       if (!ok) {
@@ -420,7 +423,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
           l[r] *= rows.f[g0 + r];
         }
         if (j > 0) {
-          ok = mbar_wait(bar(kODone), (j - 1) & 1, c.err);
+          ok = mbar_wait(bar(kODone + (j - 1) % L_::kPs), ((j - 1) / L_::kPs) & 1, c.err);
           __syncwarp();
           fence_after_sync();
 #pragma unroll
@@ -460,18 +463,20 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
         }
         __syncwarp();
       }
-      if (j > 0) ok = ok && mbar_wait(bar(kODone), (j - 1) & 1, c.err);  // P of the tile before has been read
-      if (t == 0) {  // through with K of this tile and, once for all groups, with V of the one before
+      // the buffer of P has been read; through with V of that tile (once for all groups), K of this one
+      constexpr int kBack = L_::kPs;
+      if (j >= kBack) ok = ok && mbar_wait(bar(kODone + (j - kBack) % kBack), ((j - kBack) / kBack) & 1, c.err);
+      if (t == 0) {
         mbar_arrive(bar(kKEmpty + j % L_::kStages));
-        if (grp == 0 && j > 0) mbar_arrive(bar(kVEmpty + (j - 1) % L_::kStages));
+        if (grp == 0 && j >= kBack) mbar_arrive(bar(kVEmpty + (j - kBack) % L_::kStages));
       }
-      char* p = smem + L_::kP;
+      char* p = smem + L_::kP + j % kBack * (kKeys * 4 * N);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<uint4*>(p + p_off<N>(t, (i * N + g0) >> 4)) = make_uint4(u[i][0], u[i][1], u[i][2], u[i][3]);
       fence_proxy_async_smem();
       fence_before_sync();
-      mbar_arrive(bar(kPFull));
+      mbar_arrive(bar(kPFull + j % kBack));
     }
     // the weights' sums over the keys
 #pragma unroll
@@ -481,7 +486,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
       if (lane == 0) red[(warp & 3) * N + g0 + r] = l[r];
     }
     if (ok && n > 0)
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(kODone), (n - 1) & 1, c.err));
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(kODone + (n - 1) % L_::kPs), ((n - 1) / L_::kPs) & 1, c.err));
     named_sync(1 + grp, 128);
     fence_after_sync();
     // thread t has dim t of every row
@@ -499,7 +504,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
         tmem_ld16f(ot + lanes + i * N + g0, y);
         tmem_wait_ld16f(y);
 #pragma unroll
-        for (int r = 0; r < NG; ++r) o[r] = fmaf(o[r], 0.0625f, y[r]);
+        for (int r = 0; r < NG; ++r) o[r] = fmaf(o[r], 0.03125f, y[r]);
       }
     }
 #pragma unroll
