@@ -100,24 +100,39 @@ __device__ __forceinline__ void finish_row(const AttnArgs& a, size_t row, int d4
   if (a.lse && d4 == 0) a.lse[row] = any ? (mm - kLift + log2f(ll)) * 0.693147180559945f : -INFINITY;
 }
 
-// Joins a row's `n` partial results, `stride` rows apart, in their order.
+// Joins a row's `n` partial results, `stride` rows apart, in their order: eight
+// at a time, their loads under way together.
 template <int D>
 __device__ __forceinline__ void join_row(const AttnArgs& a, const AttnWs& ws, size_t first, int stride,
                                          int n, size_t row, int d4) {
-  float mm = -INFINITY;
-  for (int s = 0; s < n; ++s)
-    mm = fmaxf(mm, __ldcg(&ws.ml[first + static_cast<size_t>(s) * stride]).x);
-  const float ref = mm == -INFINITY ? 0.f : mm;
-  float ll = 0.f;
+  constexpr int kBatch = 8;
+  float mm = -INFINITY, ll = 0.f;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < n; ++s) {
-    const size_t at = first + static_cast<size_t>(s) * stride;
-    const float2 x = __ldcg(&ws.ml[at]);
-    const float f = ex2(x.x - ref);
-    const float4 y = __ldcg(reinterpret_cast<const float4*>(ws.o + at * D + 4 * d4));
-    ll = fmaf(x.y, f, ll);
-    v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y);
-    v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
+  for (int s0 = 0; s0 < n; s0 += kBatch) {
+    float2 x[kBatch];
+    float4 y[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const size_t at = first + static_cast<size_t>(min(s0 + i, n - 1)) * stride;
+      x[i] = __ldcg(&ws.ml[at]);
+      y[i] = __ldcg(reinterpret_cast<const float4*>(ws.o + at * D + 4 * d4));
+    }
+    float top = mm;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) top = fmaxf(top, x[i].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float back = ex2(mm - ref);
+    mm = top;
+    ll *= back;
+    v.x *= back, v.y *= back, v.z *= back, v.w *= back;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (s0 + i >= n) break;
+      const float f = ex2(x[i].x - ref);
+      ll = fmaf(x[i].y, f, ll);
+      v.x = fmaf(y[i].x, f, v.x), v.y = fmaf(y[i].y, f, v.y);
+      v.z = fmaf(y[i].z, f, v.z), v.w = fmaf(y[i].w, f, v.w);
+    }
   }
   finish_row<D>(a, row, d4, v, mm, ll);
 }

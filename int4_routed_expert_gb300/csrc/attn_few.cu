@@ -46,7 +46,8 @@ enum Bar {
   kODone = 21,   // [2] O^T += V^T P, by buffer of P
   kCFull = 23,   // [8] scales
   kDrain = 31,
-  kBars = 32
+  kJoin = 32,    // partial results
+  kBars = 33
 };
 
 // Up to 32 rows keep to half an SM, so that two CTAs cover each other's bubbles.
@@ -63,8 +64,8 @@ struct Lay {
   static constexpr int kP = kV + kStages * Io::kMat8;  // [128 keys][4 N]
   static constexpr int kPs = N == 64 ? 2 : 1;  // buffers of P
   static constexpr int kConst = kP + kPs * kKeys * 4 * N;
-  static constexpr int kRow = kConst + kConstRing * 8 * 16;  // [6][N]: see Rows
-  static constexpr int kRed = kRow + 6 * N * 4;              // [4][N] floats
+  static constexpr int kRow = kConst + kConstRing * 8 * 16;  // [7][N]: see Rows
+  static constexpr int kRed = kRow + 7 * N * 4;              // [4][N] floats
   static constexpr int kBar = kRed + 4 * N * 4;
   static constexpr int kSmem = kBar + kBars * 8 + 1024;
   static constexpr int kTmem = 8 * N;                        // S^T twice, then O^T
@@ -79,9 +80,10 @@ struct Rows {
   float* f;       // factor of a move
   int* lo;
   int* hi;
+  int* out;       // row of the output
   __device__ __forceinline__ explicit Rows(char* p)
       : lscale(reinterpret_cast<float*>(p)), nref(lscale + N), m(nref + N), f(m + N),
-        lo(reinterpret_cast<int*>(f + N)), hi(lo + N) {}
+        lo(reinterpret_cast<int*>(f + N)), hi(lo + N), out(hi + N) {}
 };
 
 // P's operand layout: a key's terms in a row of 4 N bytes, term by term; rows
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
   if (threadIdx.x == 0) {
     constexpr int kS = 128 * L_::kGroups, kG = L_::kGroups;
     const int count[kBars] = {kS, 1, 1, 1, 1, kG, kG, kG, kG, 1, 1, 1, 1, 1, 1, 1, 1,
-                              1,  1, kS, kS, 1, 1, 8, 8, 8, 8, 8, 8, 8, 8, 1};
+                              1,  1, kS, kS, 1, 1, 8, 8, 8, 8, 8, 8, 8, 8, 1, 1};
 #pragma unroll
     for (int i = 0; i < kBars; ++i) mbar_init(bar(i), count[i]);
     fence_barrier_init();
@@ -342,6 +344,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
         rows.m[r] = -INFINITY;
         rows.lo[r] = s.lo;
         rows.hi[r] = s.hi;
+        rows.out[r] = (w.q.q0 + tok) * a.hq + hk * a.G + (live ? gr - tok * a.G : 0);
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(kQFull));
@@ -478,26 +481,27 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
       fence_before_sync();
       mbar_arrive(bar(kPFull + j % kBack));
     }
-    // the weights' sums over the keys
+    // the weights' sums over the warp's keys: half the rows go each way at a step,
+    // so that lanes r and r + 16 end with row r's halves
 #pragma unroll
-    for (int r = 0; r < NG; ++r) {
+    for (int o = 8; o > 0; o >>= 1) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-      if (lane == 0) red[(warp & 3) * N + g0 + r] = l[r];
+      for (int r = 0; r < o; ++r) {
+        const bool up = (lane & o) != 0;
+        const float give = up ? l[r] : l[r + o], keep = up ? l[r + o] : l[r];
+        l[r] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
     }
+    l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
+    if (lane < NG) red[(warp & 3) * N + g0 + lane] = l[0];
     if (ok && n > 0)
       ok = __all_sync(0xffffffffu, mbar_wait(bar(kODone + (n - 1) % L_::kPs), ((n - 1) / L_::kPs) & 1, c.err));
-    named_sync(1 + grp, 128);
     fence_after_sync();
-    // thread t has dim t of every row
-    const size_t tile_id = (static_cast<size_t>(b) * c.hkv + hk) * pl.row_tiles + rt;
-    const size_t prow = (tile_id * pl.splits + split) * N;
-    const int live = w.r1 - w.r0;
+    // thread t has dim t of every row: the terms' columns, the smallest first
     float o[NG];
 #pragma unroll
     for (int r = 0; r < NG; ++r) o[r] = 0.f;
     if (n > 0 && ok) {
-      // the terms' columns, the smallest first
 #pragma unroll
       for (int i = 3; i >= 0; --i) {
         float y[NG];
@@ -507,22 +511,29 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
         for (int r = 0; r < NG; ++r) o[r] = fmaf(o[r], 0.03125f, y[r]);
       }
     }
+    named_sync(1 + grp, 128);
+    const int live = w.r1 - w.r0;
+    const size_t prow = (((static_cast<size_t>(b) * c.hkv + hk) * pl.row_tiles + rt) * pl.splits + split) * N;
+    if (t < NG && g0 + t < live) {
+      const int row = g0 + t;
+      const float ll = (red[row] + red[N + row]) + (red[2 * N + row] + red[3 * N + row]);
+      const float mm = rows.m[row] + (kLift - kFewLift);  // as the other kernel counts
+      const bool any = ll > 0.f || ll != ll;
+      rows.f[row] = any ? 1.f / ll : 0.f;
+      if (w.n_split > 1)
+        ws.ml[prow + row] = make_float2(mm, ll);
+      else if (a.lse)
+        a.lse[rows.out[row]] = any ? (mm - kLift + log2f(ll)) * 0.693147180559945f : -INFINITY;
+    }
+    named_sync(1 + grp, 128);
 #pragma unroll
     for (int r = 0; r < NG; ++r) {
       const int row = g0 + r;
       if (row < live && t < D) {
-        const float ll = (red[row] + red[N + row]) + (red[2 * N + row] + red[3 * N + row]);
-        const float mm = rows.m[row] + (kLift - kFewLift);  // as the other kernels count
-        if (w.n_split == 1) {
-          const int gr = w.r0 + row, tk = gr / a.G;
-          const size_t orow = (static_cast<size_t>(w.q.q0) + tk) * a.hq + hk * a.G + gr - tk * a.G;
-          const bool any = ll > 0.f || ll != ll;
-          a.out[orow * D + t] = __float2bfloat16_rn(any ? o[r] / ll : 0.f);
-          if (a.lse && t == 0) a.lse[orow] = any ? (mm - kLift + log2f(ll)) * 0.693147180559945f : -INFINITY;
-        } else {
+        if (w.n_split == 1)
+          a.out[static_cast<size_t>(rows.out[row]) * D + t] = __float2bfloat16_rn(o[r] * rows.f[row]);
+        else
           ws.o[(prow + row) * D + t] = o[r];
-          if (t == 0) ws.ml[prow + row] = make_float2(mm, ll);
-        }
       }
     }
     if (w.n_split > 1) __threadfence();
@@ -542,10 +553,67 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  for (int e = threadIdx.x; e < (w.r1 - w.r0) * (D / 4); e += L_::kThreads) {
-    const int row = e / (D / 4), gr = w.r0 + row, tk = gr / a.G;
-    join_row<D>(a, ws, tile_id * pl.splits * N + row, N, w.n_split,
-                (static_cast<size_t>(w.q.q0) + tk) * a.hq + hk * a.G + gr - tk * a.G, e % (D / 4));
+  // Partial results come from SMs far away: as many splits as fit are copied
+  // over the key and value stages at once, a lane a split, so that their
+  // latencies overlap.
+  constexpr int kEach = (N * (D / 4) + L_::kThreads - 1) / L_::kThreads;
+  constexpr int kRoom = 2 * L_::kStages * Io::kMat8;
+  const int live = w.r1 - w.r0;
+  const uint32_t o_bytes = live * D * 4, ml_bytes = N * 8;
+  const int chunk = kRoom / (o_bytes + ml_bytes);
+  const size_t first = tile_id * pl.splits * N;
+  float mm[kEach], ll[kEach];
+  float4 v[kEach];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) mm[k] = -INFINITY, ll[k] = 0.f, v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4* so = reinterpret_cast<const float4*>(smem + L_::kK);
+  bool landed = true;
+  for (int s0 = 0, ph = 0; s0 < w.n_split && landed; s0 += chunk, ph ^= 1) {
+    const int m = min(chunk, w.n_split - s0);
+    const float2* sml = reinterpret_cast<const float2*>(smem + L_::kK + m * o_bytes);
+    if (warp == 0) {
+      // (the results were written by other threads' plain stores, and so were
+      // this buffer's last reads)
+      asm volatile("fence.proxy.async;" ::: "memory");
+      if (lane == 0) mbar_arrive_expect_tx(bar(kJoin), m * (o_bytes + ml_bytes));
+      __syncwarp();
+      for (int s = lane; s < m; s += 32) {
+        const size_t from = first + static_cast<size_t>(s0 + s) * N;
+        bulk_g2s(smem_u32(so) + s * o_bytes, ws.o + from * D, o_bytes, bar(kJoin));
+        bulk_g2s(smem_u32(sml) + s * ml_bytes, ws.ml + from, ml_bytes, bar(kJoin));
+      }
+    }
+    landed = mbar_wait(bar(kJoin), ph, c.err);
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+      const int e = threadIdx.x + k * L_::kThreads;
+      if (e < live * (D / 4)) {
+        const int row = e / (D / 4);
+        float top = mm[k];
+#pragma unroll 4
+        for (int s = 0; s < m; ++s) top = fmaxf(top, sml[s * N + row].x);
+        const float ref = top == -INFINITY ? 0.f : top, back = ex2(mm[k] - ref);
+        mm[k] = top;
+        ll[k] *= back;
+        v[k].x *= back, v[k].y *= back, v[k].z *= back, v[k].w *= back;
+        const float4* y = so + e;
+#pragma unroll 4
+        for (int s = 0; s < m; ++s, y += live * (D / 4)) {
+          const float2 x = sml[s * N + row];
+          const float4 z = *y;
+          const float f = ex2(x.x - ref);
+          ll[k] = fmaf(x.y, f, ll[k]);
+          v[k].x = fmaf(z.x, f, v[k].x), v[k].y = fmaf(z.y, f, v[k].y);
+          v[k].z = fmaf(z.z, f, v[k].z), v[k].w = fmaf(z.w, f, v[k].w);
+        }
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int e = threadIdx.x + k * L_::kThreads;
+    if (e < live * (D / 4)) finish_row<D>(a, rows.out[e / (D / 4)], e % (D / 4), v[k], mm[k], ll[k]);
   }
 }
 
@@ -560,8 +628,7 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const K
   const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
   const int64_t tiles = max_key_tiles(c, a, N, kKeys);
   const int64_t resident = static_cast<int64_t>(n_sm) * Lay<D, N>::kCtas;
-  const int64_t splits = best_splits(base, resident, tiles, static_cast<int64_t>(ws.cap_rows) / (base * N),
-                                     false);
+  const int64_t splits = best_splits(base, resident, tiles, static_cast<int64_t>(ws.cap_rows) / (base * N));
   pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
   pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
   const int64_t grid = base * pl.splits;

@@ -76,7 +76,7 @@ __device__ __forceinline__ int checked_page(const KvView& c, int p, bool& bad) {
 struct AttnWs {
   float* o;        // [cap_rows][D] unnormalised sums
   float2* ml;      // [cap_rows] running reference and weight sum
-  unsigned* count; // [cap_rows / kRowTile + 1]
+  unsigned* count; // [cap_rows / 16]
   size_t cap_rows;
 };
 
@@ -96,9 +96,6 @@ cudaError_t rope_launch(const uint64_t* inc, int rot_dim, float amplitude, bool 
 cudaError_t kv_write_launch(const KvView& c, const void* k, int64_t ks, const void* v, int64_t vs,
                             moe_dtype_t dt, cudaStream_t s);
 cudaError_t kv_read_launch(const KvView& c, void* k, void* v, moe_dtype_t dt, cudaStream_t s);
-cudaError_t attn_rows_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, int n_sm,
-                             cudaStream_t s);
-
 // TMA maps of the code arrays as [n_pages][n_kv_heads * page_size][D] bytes, boxes
 // of one page of one head, swizzled in D-byte rows.
 struct KvMaps {

@@ -319,22 +319,16 @@ struct Plan {
 };
 
 // Splits of `tiles` tiles for `base` row tiles on `resident` CTA slots, at most
-// `most`: the fewest tile times, a CTA costing kCtaTiles beside its own (start,
-// first loads, results).  Several sequences may be shorter than the bound that
-// `tiles` comes from: the finest cut within a sixteenth of the best one then.
-inline int64_t best_splits(int64_t base, int64_t resident, int64_t tiles, int64_t most, bool ragged) {
-  constexpr int64_t kCtaTiles = 3;
+// `most`: the least time in sixteenths of a tile, a CTA costing three tiles
+// beside its own (start, first loads, results) and the join half a sixteenth a
+// split.
+inline int64_t best_splits(int64_t base, int64_t resident, int64_t tiles, int64_t most) {
   const int64_t end = std::max<int64_t>(std::min<int64_t>({tiles, most, 256}), 1);
-  auto cost = [&](int64_t s) {
-    return (base * s + resident - 1) / resident * ((tiles + s - 1) / s + kCtaTiles);
-  };
   int64_t least = INT64_MAX, best = 1;
-  for (int64_t s = 1; s <= end; ++s) least = std::min(least, cost(s));
-  for (int64_t s = 1; s <= end; ++s)
-    if (cost(s) * 16 <= least * (ragged ? 17 : 16)) {
-      best = s;
-      if (!ragged) break;
-    }
+  for (int64_t s = 1; s <= end; ++s) {
+    const int64_t cost = (base * s + resident - 1) / resident * ((tiles + s - 1) / s + 3) * 16 + s / 2;
+    if (cost < least) least = cost, best = s;
+  }
   return best;
 }
 

@@ -1,8 +1,9 @@
 // Rotary positions (moe_rope_apply).
 //
-// One CTA a token: the angles' sines and cosines go to shared memory once for
-// all heads, then the threads stream the token's heads, 16 elements (8 pairs,
-// or 16 copied elements) an item.  The angle of pair i at position p is p *
+// The angles' sines and cosines of a CTA's tokens go to shared memory once for
+// all heads; then a thread holds its 8 pairs' ones in registers and streams
+// its place of the token's heads (8 pairs, or 16 copied elements).  The angle
+// of pair i at position p is p *
 // inc[i] mod 2^64, a 64-bit fraction of a turn: an integer product wraps
 // exactly, so far positions lose nothing.  Bound by memory: x is read once and
 // y written once.
@@ -12,110 +13,131 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kItems = 2;   // heads of a thread under way
+constexpr int kTokens = 4;  // most tokens of a CTA
 
 struct RopeParams {
   uint64_t inc[128];  // fraction of a turn per position, 64-bit fixed point
   const void* x[2];
-  void* y[2];
+  const void* y[2];
   int64_t xs[2], ys[2];
   const int32_t* pos;
   float amplitude;
   int heads[2];
-  int rot, head_dim;
+  int rot, head_dim, T, tokens;
 };
 
-struct V8 {
-  float f[8];
-};
-
+// 8 elements as they lie, and as fp32
 template <typename T>
-__device__ __forceinline__ V8 load8(const T* p);
-template <>
-__device__ __forceinline__ V8 load8<float>(const float* p) {
-  V8 v;
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v.f[0] = a.x, v.f[1] = a.y, v.f[2] = a.z, v.f[3] = a.w;
-  v.f[4] = b.x, v.f[5] = b.y, v.f[6] = b.z, v.f[7] = b.w;
-  return v;
-}
-template <>
-__device__ __forceinline__ V8 load8<__nv_bfloat16>(const __nv_bfloat16* p) {
-  V8 v;
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Raw {
+  static constexpr int kVec = sizeof(T) / 2;
+  uint4 v[kVec];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v.f[2 * i] = __uint_as_float(w[i] << 16);
-    v.f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < kVec; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
   }
-  return v;
-}
-__device__ __forceinline__ void store8(float* p, const V8& v) {
-  *reinterpret_cast<float4*>(p) = make_float4(v.f[0], v.f[1], v.f[2], v.f[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v.f[4], v.f[5], v.f[6], v.f[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const V8& v) {
-  uint4 a;
-  uint32_t* w = &a.x;
+  __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v.f[2 * i], v.f[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    for (int i = 0; i < kVec; ++i) reinterpret_cast<uint4*>(p)[i] = v[i];
   }
-  *reinterpret_cast<uint4*>(p) = a;
-}
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    if constexpr (kVec == 1) {
+      const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f[4 * i] = __uint_as_float(v[i].x), f[4 * i + 1] = __uint_as_float(v[i].y);
+        f[4 * i + 2] = __uint_as_float(v[i].z), f[4 * i + 3] = __uint_as_float(v[i].w);
+      }
+    }
+  }
+  __device__ __forceinline__ void put(const float (&f)[8]) {
+    if constexpr (kVec == 1) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        v[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
+                          __float_as_uint(f[4 * i + 3]));
+    }
+  }
+};
 
 template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams P) {
-  __shared__ float2 cs[128];  // cosine, sine
-  const int t = blockIdx.x;
+  __shared__ float2 cs[kTokens][128];  // cosine, sine
   const int half = P.rot >> 1;
-  for (int i = threadIdx.x; i < half; i += kThreads) {
-    const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(P.pos[t])) * P.inc[i];
+  const int t0 = blockIdx.x * P.tokens, tn = min(P.tokens, P.T - t0);
+  for (int i = threadIdx.x; i < tn * half; i += blockDim.x) {
+    const int tk = i / half, pair = i - tk * half;
+    const uint64_t phase =
+        static_cast<uint64_t>(static_cast<int64_t>(__ldg(P.pos + t0 + tk))) * P.inc[pair];
     // the top 32 bits as a signed number of half turns in [-1, 1)
     float s, c;
     sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.6566128730773926e-10f, &s, &c);
-    cs[i] = make_float2(c * P.amplitude, s * P.amplitude);
+    cs[tk][pair] = make_float2(c * P.amplitude, s * P.amplitude);
   }
-  __syncthreads();
+  // a thread's place c in a head is fixed: elements ia .. ia + 7 and ib .. ib + 7
   const int per_head = P.head_dim >> 4;
-  const int turned = P.rot >> 4;
+  const int h0 = threadIdx.x / per_head, c = threadIdx.x - h0 * per_head;
+  const int hstep = blockDim.x / per_head, heads = P.heads[0] + P.heads[1];
+  const bool turned = c < (P.rot >> 4);
+  int ia = 16 * c, ib = 16 * c + 8;
+  if (!INTERLEAVED && turned) ia = 8 * c, ib = 8 * c + half;
+  auto at = [&](const void* const (&base)[2], const int64_t (&stride)[2], int t, int h) {
+    const int w = h >= P.heads[0];
+    return static_cast<const T*>(base[w]) + (t0 + t) * stride[w] + (h - (w ? P.heads[0] : 0)) * P.head_dim;
+  };
+  __syncthreads();
+  for (int t = 0; t < tn; ++t) {
+    float2 r[8];
+    if (turned) {
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const T* x = static_cast<const T*>(P.x[w]) + t * P.xs[w];
-    T* y = static_cast<T*>(P.y[w]) + t * P.ys[w];
-    const int items = P.heads[w] * per_head;
-    for (int it = threadIdx.x; it < items; it += kThreads) {
-      const int h = it / per_head, c = it - h * per_head;
-      const size_t base = static_cast<size_t>(h) * P.head_dim;
-      size_t ia = base + 16 * c, ib = ia + 8;
-      if (!INTERLEAVED && c < turned) ia = base + 8 * c, ib = ia + half;
-      V8 a = load8<T>(x + ia), b = load8<T>(x + ib);
-      if (c < turned) {
-        const float2* q = cs + 8 * c;
-        if (INTERLEAVED) {
+      for (int i = 0; i < 8; ++i) r[i] = cs[t][8 * c + i];
+    }
+    for (int h = h0; h < heads; h += kItems * hstep) {
+      Raw<T> a[kItems], b[kItems];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 r = q[i], z = q[i + 4];
-            const float a0 = a.f[2 * i], a1 = a.f[2 * i + 1];
-            a.f[2 * i] = a0 * r.x - a1 * r.y;
-            a.f[2 * i + 1] = a0 * r.y + a1 * r.x;
-            const float b0 = b.f[2 * i], b1 = b.f[2 * i + 1];
-            b.f[2 * i] = b0 * z.x - b1 * z.y;
-            b.f[2 * i + 1] = b0 * z.y + b1 * z.x;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 r = q[i];
-            const float a0 = a.f[i], b0 = b.f[i];
-            a.f[i] = a0 * r.x - b0 * r.y;
-            b.f[i] = a0 * r.y + b0 * r.x;
-          }
+      for (int n = 0; n < kItems; ++n) {
+        if (h + n * hstep < heads) {
+          const T* x = at(P.x, P.xs, t, h + n * hstep);
+          a[n].load(x + ia);
+          b[n].load(x + ib);
         }
       }
-      store8(y + ia, a);
-      store8(y + ib, b);
+#pragma unroll
+      for (int n = 0; n < kItems; ++n) {
+        if (h + n * hstep >= heads) break;
+        if (turned) {
+          float f[8], g[8];
+          a[n].get(f);
+          b[n].get(g);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float& u = !INTERLEAVED ? f[i] : i < 4 ? f[2 * i] : g[2 * i - 8];
+            float& v = !INTERLEAVED ? g[i] : i < 4 ? f[2 * i + 1] : g[2 * i - 7];
+            const float u0 = u, v0 = v;
+            u = u0 * r[i].x - v0 * r[i].y;
+            v = u0 * r[i].y + v0 * r[i].x;
+          }
+          a[n].put(f);
+          b[n].put(g);
+        }
+        T* y = const_cast<T*>(at(P.y, P.ys, t, h + n * hstep));
+        a[n].store(y + ia);
+        b[n].store(y + ib);
+      }
     }
   }
 }
@@ -139,16 +161,21 @@ cudaError_t rope_launch(const uint64_t* inc, int rot_dim, float amplitude, bool 
   P.amplitude = amplitude;
   P.rot = rot_dim;
   P.head_dim = head_dim;
+  P.T = T;
+  // one token a CTA while that fills the device once; four share the angles' phase then
+  P.tokens = T >= 2048 ? kTokens : 1;
+  const int per_head = head_dim / 16, threads = kThreads / per_head * per_head;
+  const int grid = (T + P.tokens - 1) / P.tokens;
   if (dt == MOE_BF16) {
     if (interleaved)
-      rope_kernel<__nv_bfloat16, true><<<T, kThreads, 0, s>>>(P);
+      rope_kernel<__nv_bfloat16, true><<<grid, threads, 0, s>>>(P);
     else
-      rope_kernel<__nv_bfloat16, false><<<T, kThreads, 0, s>>>(P);
+      rope_kernel<__nv_bfloat16, false><<<grid, threads, 0, s>>>(P);
   } else {
     if (interleaved)
-      rope_kernel<float, true><<<T, kThreads, 0, s>>>(P);
+      rope_kernel<float, true><<<grid, threads, 0, s>>>(P);
     else
-      rope_kernel<float, false><<<T, kThreads, 0, s>>>(P);
+      rope_kernel<float, false><<<grid, threads, 0, s>>>(P);
   }
   return cudaGetLastError();
 }
