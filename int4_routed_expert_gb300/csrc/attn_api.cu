@@ -85,10 +85,9 @@ const char* check_kv_config(const moe_kv_config_t* c) {
   return nullptr;
 }
 
-// Rows of partial results: 2^17 hold two CTAs of 256 rows a SM and more than
-// eight rounds of two CTAs of 16 rows; the splits of a call are limited to
-// what fits.
-constexpr size_t kPartRows = 1u << 17;
+// Rows of partial results: 2^18 hold six CTAs of 256 rows a SM; the splits of
+// a call are limited to what fits.
+constexpr size_t kPartRows = 1u << 18;
 
 struct KvLayout {
   size_t o, ml, count, err, total;

@@ -12,8 +12,8 @@
 //   4 warps   value codes -> f16 (exact) in the swizzled operand layout
 //   1 thread  tcgen05.mma: S = Q K^T in e4m3, then O += P V in f16 (P from
 //             tensor memory, V as it lies, MN-major)
-//   2 x 4     softmax warps, one group a M tile, a thread a row: S from tensor
-//             memory, weights back as f16 over S
+//   2 x 8     softmax warps, two groups a M tile, two threads a row, 64 keys
+//             each: S from tensor memory, weights back as f16 over S
 // Keys are multiplied as they are stored: a bf16 query (8 bits) is the sum of
 // two e4m3 numbers of 4 bits each, exact down to 2^-18 of the row's largest,
 // and e4m3 products run at twice the rate of f16 ones, so the two terms cost
@@ -29,7 +29,9 @@ namespace {
 
 constexpr int kM = 128;        // rows of an M tile
 constexpr int kRows = 2 * kM;  // rows of a CTA
-constexpr int kThreads = 448;  // 4 + 4 softmax warps, 4 conversion warps, MMA warp, load warp
+constexpr int kSoftmax = 512;              // threads: 2 M tiles x 2 halves of the keys x 128 rows
+constexpr int kThreads = kSoftmax + 192;   // 4 conversion warps, MMA warp, load warp
+constexpr int kMmaWarp = kSoftmax / 32 + 4;
 constexpr int kKStages = 3;
 
 template <int D>
@@ -43,7 +45,8 @@ struct Lay {
   static constexpr int kV = kK + kKStages * kMat8;
   static constexpr int kRaw = kV + 2 * kMat;
   static constexpr int kConst = kRaw + 2 * kMat8;
-  static constexpr int kBar = kConst + kConstRing * 8 * 16;
+  static constexpr int kPair = kConst + kConstRing * 8 * 16;  // [2][2][2][128] floats between a row's threads
+  static constexpr int kBar = kPair + 2 * 2 * 2 * 128 * 4;
   static constexpr int kEnd = kBar + 32 * 8;
   static constexpr int kSmem = kEnd + 1024;        // the base is rounded up to 1024
 };
@@ -92,13 +95,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   auto bar = [&](int i) { return base_u + L_::kBar + 8 * i; };
   if (threadIdx.x == 0) {
-    const int count[kBars] = {128 * n_mt, 1, 1, 1, 1, 1, 1, 1, 1, 128, 128, 128, 128,
-                              1, 1, 1, 1, 128, 128, 1, 1, 8, 8, 8, 8, 8, 8, 8, 8, 1};
+    const int count[kBars] = {256 * n_mt, 1, 1, 1, 1, 1, 1, 1, 1, 128, 128, 128, 128,
+                              1, 1, 1, 1, 256, 256, 1, 1, 8, 8, 8, 8, 8, 8, 8, 8, 1};
 #pragma unroll
     for (int i = 0; i < kBars; ++i) mbar_init(bar(i), count[i]);
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&s_tmem), 512);
     tmem_relinquish();
   }
@@ -109,9 +112,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const Io<D> io{base_u + L_::kK, base_u + L_::kRaw, base_u + L_::kV, smem, base_u, base_u + L_::kConst,
                  bar(kKFull), bar(kKEmpty), bar(kRFull), bar(kREmpty), bar(kVFull), bar(kCFull)};
-  if (warp == 13) {
+  if (warp == kMmaWarp + 1) {
     if (lane < 8 && n > 0) io.load(c, a, w.k, b, hk, t_begin, n, &k_map, nullptr, lane);
-  } else if (warp == 12) {
+  } else if (warp == kMmaWarp) {
     if (lane == 0 && n > 0) {
       constexpr uint32_t id_s = idesc_f16(kM, kKeys);           // e4m3 is format 0 of its kind, too
       constexpr uint32_t id_o = idesc_f16(kM, D) | (1u << 16);  // V is MN-major
@@ -138,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_after_sync();
           const uint32_t ot = tmem + 256 + i * 128, pt = tmem + i * 128;
           mma_o(ot, pt, vd, id_o, j == 0);
-          mma_o(ot, pt + 32, vd + (64 * 128 >> 4), id_o, 0);
+          mma_o(ot, pt + 64, vd + (64 * 128 >> 4), id_o, 0);  // P's halves start where S's do
           if (i == n_mt - 1) mma_commit(bar(kVEmpty + st));
           if (j == n - 1) {
             mma_commit(bar(kOFull + i));
@@ -157,40 +160,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(bar(kDrain), 0, c.err);
       }
     }
-  } else if (wg == 2) {
-    io.convert(c, a, w.k, t_begin, n, threadIdx.x - 256,
+  } else if (wg == 4) {
+    io.convert(c, a, w.k, t_begin, n, threadIdx.x - kSoftmax,
                [&](int j) { return mbar_wait(bar(kVEmpty + (j & 1)), ((j >> 1) & 1) ^ 1, c.err); });
-  } else if (wg < n_mt) {
-    const int i = wg, row = threadIdx.x & 127;
+  } else if ((wg >> 1) < n_mt) {
+    const int i = wg >> 1, half = wg & 1, row = threadIdx.x & 127;  // M tile, half of the keys
     const int r = w.r0 + i * kM + row;
     const bool live = r < w.r1;
     const int tok = live ? r / a.G : 0;
     const int head = w.hk * a.G + (live ? r - tok * a.G : 0);
     const RowSees sees = row_sees(a, w.q.L, w.base_p + tok, live);
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 * (warp % 4)
-    const uint32_t ts = tmem + i * 128 + lanes, to = tmem + 256 + i * 128 + lanes;
+    const uint32_t ts = tmem + i * 128 + lanes + half * 64, to = tmem + 256 + i * 128 + lanes + half * (D / 2);
+    // what the row's two threads tell each other, two buffers in turn
+    float* pair = reinterpret_cast<float*>(smem + L_::kPair) + i * 512;
+    auto other = [&](int buf, float mine) {
+      pair[buf * 256 + half * 128 + row] = mine;
+      named_sync(1 + i, 256);
+      return pair[buf * 256 + (half ^ 1) * 128 + row];
+    };
     float m = -INFINITY, l = 0.f, lscale = 0.f;  // lscale >= 0: a negative scale turns the query's sign
     bool ok = true;
     if (n > 0) {
       // the row's query, brought to [2^7, 2^8) by a power of two, as two e4m3 terms
       const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + (static_cast<int64_t>(w.q.q0) + tok) * a.q_stride + static_cast<int64_t>(head) * D);
-      uint4 raw[D / 8];
+          a.q + (static_cast<int64_t>(w.q.q0) + tok) * a.q_stride + static_cast<int64_t>(head) * D + half * (D / 2));
+      uint4 raw[D / 16];
       float amax = 0.f;
 #pragma unroll
-      for (int x = 0; x < D / 8; ++x) {
+      for (int x = 0; x < D / 16; ++x) {
         raw[x] = live ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
         const uint32_t u[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           amax = max3(amax, fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xffff0000u)));
       }
+      amax = fmaxf(amax, other(1, amax));
       const float f = copysignf(row_factor<7>(amax), a.scale_log2);
       lscale = a.scale_log2 / f;
       const bool inf = !(amax < INFINITY);  // (codes saturate: such a row is NaN instead)
       char* dst = smem + L_::kQ + i * 2 * L_::kMat8;
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
+      for (int x = 0; x < D / 32; ++x) {
         const uint32_t u[8] = {raw[2 * x].x,     raw[2 * x].y,     raw[2 * x].z,     raw[2 * x].w,
                                raw[2 * x + 1].x, raw[2 * x + 1].y, raw[2 * x + 1].z, raw[2 * x + 1].w};
         uint32_t t0[4], t1[4];
@@ -207,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           t0[k] = inf ? 0x7f7f7f7fu : w0;
           t1[k] = w1;
         }
-        const uint32_t off = k_off<D>(row, x);
+        const uint32_t off = k_off<D>(row, half * (D / 32) + x);
         *reinterpret_cast<uint4*>(dst + off) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
         *reinterpret_cast<uint4*>(dst + L_::kMat8 + off) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
       }
@@ -222,37 +233,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        mbar_wait(bar(kSFull + i), j & 1, c.err));
       if (!ok) break;
       fence_after_sync();
-      const float4* cn = io.scales(j);
-      const int base = w.k.base(t_begin + j);
-      const bool whole = (a.causal ? base + kKeys <= p_lo + 1 : base + kKeys <= w.q.L) &&
-                         (a.window == 0 || base > p_hi - a.window || base + kKeys <= a.sinks);
-      // S is read twice, 32 columns at a time and the next 32 under way: for the
-      // row's largest logit (within 16 keys of one scale the largest product
-      // gives it), then for the weights
-      float s[2][32];
-      if (!whole) {
-        // what the row does not see goes to -inf first, where it lies
-#pragma unroll 1
-        for (int x = 0; x < 4; ++x) {
-          tmem_ld32(ts + 32 * x, s[0]);
-          tmem_wait_ld32(s[0]);
-          uint32_t u[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) u[k] = sees(base + 32 * x + k) ? __float_as_uint(s[0][k]) : 0xff800000u;
-          tmem_st32(ts + 32 * x, u);
-        }
-        tmem_wait_st();
-      }
+      const float4* cn = io.scales(j) + 4 * half;
+      const int base = w.k.base(t_begin + j) + 64 * half;
+      const bool whole = (a.causal ? base + 64 <= p_lo + 1 : base + 64 <= w.q.L) &&
+                         (a.window == 0 || base > p_hi - a.window || base + 64 <= a.sinks);
+      // S is read in halves of 32 keys, the first of them twice: for the row's
+      // largest logit (within 16 keys of one scale the largest product gives
+      // it), then for the weights
+      float s[32];
       float mt = -INFINITY;
-      tmem_ld32(ts, s[0]);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        tmem_wait_ld32(s[x & 1]);
-        tmem_ld32(ts + 32 * ((x + 1) & 3), s[(x + 1) & 1]);
+      for (int x = 0; x < 2; ++x) {
+        tmem_ld32(ts + 32 * x, s);
+        tmem_wait_ld32(s);
+        if (!whole) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) s[k] = sees(base + 32 * x + k) ? s[k] : -INFINITY;
+        }
 #pragma unroll
         for (int gg = 0; gg < 2; ++gg) {
           const float4 z = cn[2 * x + gg];
-          const float* v = s[x & 1] + 16 * gg;
+          const float* v = s + 16 * gg;
           float t0 = max3(v[0], v[1], v[2]), t1 = max3(v[3], v[4], v[5]);
           t0 = max3(t0, v[6], v[7]), t1 = max3(t1, v[8], v[9]);
           t0 = max3(t0, v[10], v[11]), t1 = max3(t1, v[12], v[13]);
@@ -260,14 +261,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           mt = fmaxf(mt, fmaf(fmaxf(t0, t1), fmaxf(lscale * z.x, kTiny), z.y));
         }
       }
+      mt = fmaxf(mt, other(j & 1, mt));
       if (__any_sync(0xffffffffu, mt > m + kRescale)) {
         const float nm = fmaxf(m, mt);
         const float f = nm == m ? 1.f : ex2(m - nm);
         m = nm;
         l *= f;
         if (j > 0) {
+          // half of the output's columns a thread
 #pragma unroll
-          for (int x = 0; x < D / 16; ++x) {
+          for (int x = 0; x < D / 32; ++x) {
             uint32_t u[16];
             tmem_ld16(to + 16 * x, u);
             tmem_wait_ld16(u);
@@ -278,16 +281,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const float ref = m == -INFINITY ? 0.f : m - kLift;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        tmem_wait_ld32(s[x & 1]);
-        if (x < 3) tmem_ld32(ts + 32 * (x + 1), s[(x + 1) & 1]);
+      auto weigh = [&](int x) {
         uint32_t u[16];
 #pragma unroll
         for (int gg = 0; gg < 2; ++gg) {
           const float4 z = cn[2 * x + gg];
           const float sc = fmaxf(lscale * z.x, kTiny), off = z.y - ref;
-          const float* v = s[x & 1] + 16 * gg;
+          const float* v = s + 16 * gg;
           float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
@@ -299,20 +299,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           l = fmaf(sum0 + sum1, z.z, l);
         }
+        // P takes the first half of this thread's S columns: those of keys 0 .. 31, read by then
+        if (x == 1) tmem_ld32(ts, s);
         tmem_st16(ts + 16 * x, u);
+      };
+      weigh(1);
+      tmem_wait_ld32(s);
+      if (!whole) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) s[k] = sees(base + k) ? s[k] : -INFINITY;
       }
+      weigh(0);
       tmem_wait_st();
       fence_before_sync();
       mbar_arrive(bar(kPFull + i));
     }
     if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(kOFull + i), 0, c.err));
+    if (n > 0) l += other(n & 1, l);
     if (ok) {
       fence_after_sync();
       const size_t orow = (static_cast<size_t>(w.q.q0) + tok) * a.hq + head;
       const size_t prow =
           (((static_cast<size_t>(b) * c.hkv + hk) * pl.row_tiles + rt) * pl.splits + split) * kRows + i * kM + row;
 #pragma unroll
-      for (int x = 0; x < D / 32; ++x) {
+      for (int x = 0; x < D / 64; ++x) {
         float o[32];
         if (n > 0) {
           tmem_ld32(to + 32 * x, o);
@@ -323,21 +333,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int k = 0; live && k < 8; ++k) {
+          const int d4 = half * (D / 8) + 8 * x + k;
           const float4 v = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
           if (w.n_split == 1)
-            finish_row<D>(a, orow, 8 * x + k, v, m, l);
+            finish_row<D>(a, orow, d4, v, m, l);
           else
-            *reinterpret_cast<float4*>(ws.o + prow * D + 32 * x + 4 * k) = v;
+            *reinterpret_cast<float4*>(ws.o + prow * D + 4 * d4) = v;
         }
         __syncwarp();
       }
-      if (live && w.n_split > 1) ws.ml[prow] = make_float2(m, l);
+      if (live && half == 0 && w.n_split > 1) ws.ml[prow] = make_float2(m, l);
     }
   }
   __syncwarp();
   fence_before_sync();
   __syncthreads();
-  if (warp == 12) tmem_dealloc(tmem, 512);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 // Joins the splits of every row that has more than one.
@@ -371,11 +382,10 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const C
   pl.row_tiles = static_cast<int>((rows + kRows - 1) / kRows);
   const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
   const int64_t tiles = max_key_tiles(c, a, kRows, kKeys);
-  // one CTA a SM: split the keys when the row tiles leave SMs without work
-  int64_t splits = base >= n_sm ? 1 : (2LL * n_sm + base - 1) / base;
-  splits = std::min(splits, (tiles + 3) / 4);
-  splits = std::min(splits, static_cast<int64_t>(ws.cap_rows) / (base * kRows));
-  splits = std::max<int64_t>(splits, 1);
+  // one CTA a SM: split the keys when the row tiles do not fill the SMs evenly
+  // (many row tiles do, the longest first)
+  const int64_t splits =
+      base >= 4 * n_sm ? 1 : best_splits(base, n_sm, tiles, static_cast<int64_t>(ws.cap_rows) / (base * kRows));
   pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
   pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
   const int64_t grid = base * pl.splits;
