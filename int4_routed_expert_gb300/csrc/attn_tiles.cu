@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = w.r0 + i * kM + row;
     const bool live = r < w.r1;
     const int tok = live ? r / a.G : 0;
-    const int head = w.hk * a.G + (live ? r - tok * a.G : 0);
+    const int head = hk * a.G + (live ? r - tok * a.G : 0);
     const RowSees sees = row_sees(a, w.q.L, w.base_p + tok, live);
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 * (warp % 4)
     const uint32_t ts = tmem + i * 128 + lanes + half * 64, to = tmem + 256 + i * 128 + lanes + half * (D / 2);
@@ -182,48 +182,53 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = -INFINITY, l = 0.f, lscale = 0.f;  // lscale >= 0: a negative scale turns the query's sign
     bool ok = true;
     if (n > 0) {
-      // the row's query, brought to [2^7, 2^8) by a power of two, as two e4m3 terms
-      const uint4* src = reinterpret_cast<const uint4*>(
-          a.q + (static_cast<int64_t>(w.q.q0) + tok) * a.q_stride + static_cast<int64_t>(head) * D + half * (D / 2));
-      uint4 raw[D / 16];
-      float amax = 0.f;
+      // The rows' queries, each brought to [2^7, 2^8) by a power of two, as two
+      // e4m3 terms: a warp takes 16 of the M tile's rows, D / 8 lanes a row.
+      constexpr int kLanes = D / 8, kPer = 32 / kLanes, kIts = 16 / kPer;  // lanes a row, rows a pass, passes
+      uint4 raw[kIts];
+      const int sub = lane / kLanes, part = lane % kLanes, wrow = (warp & 7) * 16;
 #pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
-        raw[x] = live ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
+      for (int x = 0; x < kIts; ++x) {
+        const int gr = w.r0 + i * kM + wrow + x * kPer + sub;
+        const int tk = gr / a.G;
+        raw[x] = make_uint4(0, 0, 0, 0);
+        if (gr < w.r1)
+          raw[x] = __ldg(reinterpret_cast<const uint4*>(
+                             a.q + (static_cast<int64_t>(w.q.q0) + tk) * a.q_stride +
+                             (static_cast<int64_t>(hk) * a.G + gr - tk * a.G) * D) + part);
+      }
+      char* dst = smem + L_::kQ + i * 2 * L_::kMat8;
+#pragma unroll
+      for (int x = 0; x < kIts; ++x) {
         const uint32_t u[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+        float amax = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           amax = max3(amax, fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xffff0000u)));
-      }
-      amax = fmaxf(amax, other(1, amax));
-      const float f = copysignf(row_factor<7>(amax), a.scale_log2);
-      lscale = a.scale_log2 / f;
-      const bool inf = !(amax < INFINITY);  // (codes saturate: such a row is NaN instead)
-      char* dst = smem + L_::kQ + i * 2 * L_::kMat8;
 #pragma unroll
-      for (int x = 0; x < D / 32; ++x) {
-        const uint32_t u[8] = {raw[2 * x].x,     raw[2 * x].y,     raw[2 * x].z,     raw[2 * x].w,
-                               raw[2 * x + 1].x, raw[2 * x + 1].y, raw[2 * x + 1].z, raw[2 * x + 1].w};
-        uint32_t t0[4], t1[4];
+        for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        const float f = copysignf(row_factor<7>(amax), a.scale_log2);
+        const bool inf = !(amax < INFINITY);  // (codes saturate: such a row is NaN instead)
+        uint32_t t0[2], t1[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t w0 = 0, w1 = 0;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t q1, q2;
-            split_query(u[2 * k + e], f, q1, q2);
-            w0 |= q1 << (16 * e);
-            w1 |= q2 << (16 * e);
-          }
-          t0[k] = inf ? 0x7f7f7f7fu : w0;
-          t1[k] = w1;
+        for (int k = 0; k < 2; ++k) {
+          uint32_t a1, a2, b1, b2;
+          split_query(u[2 * k], f, a1, a2);
+          split_query(u[2 * k + 1], f, b1, b2);
+          t0[k] = inf ? 0x7f7f7f7fu : a1 | (b1 << 16);
+          t1[k] = a2 | (b2 << 16);
         }
-        const uint32_t off = k_off<D>(row, half * (D / 32) + x);
-        *reinterpret_cast<uint4*>(dst + off) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
-        *reinterpret_cast<uint4*>(dst + L_::kMat8 + off) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+        const int qrow = wrow + x * kPer + sub;
+        const uint32_t off = k_off<D>(qrow, part >> 1) + 8 * (part & 1);
+        *reinterpret_cast<uint2*>(dst + off) = make_uint2(t0[0], t0[1]);
+        *reinterpret_cast<uint2*>(dst + L_::kMat8 + off) = make_uint2(t1[0], t1[1]);
+        if (part == 0) pair[256 + qrow] = a.scale_log2 / f;
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(kQFull));
+      named_sync(1 + i, 256);
+      lscale = pair[256 + row];
+      named_sync(1 + i, 256);  // (before the pair buffers' first use)
     }
     // the range that all rows of the CTA see whole
     const int p_lo = w.base_p + w.r0 / a.G, p_hi = w.base_p + (w.r1 - 1) / a.G;
@@ -321,27 +326,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t orow = (static_cast<size_t>(w.q.q0) + tok) * a.hq + head;
       const size_t prow =
           (((static_cast<size_t>(b) * c.hkv + hk) * pl.row_tiles + rt) * pl.splits + split) * kRows + i * kM + row;
+      // A thread's half row goes through shared memory (the queries' room: the
+      // last S of either M tile came before this O), D bytes a row, so that the
+      // warp's stores are whole lines: D / 2 bf16 elements in one go, or fp32
+      // partial sums in two.
+      const bool any = l > 0.f || l != l;
+      const float f = any ? 1.f / l : 0.f;
+      char* stage = smem + L_::kQ + warp * (32 * D);
+      const uint32_t olo = static_cast<uint32_t>(orow);
+      const bool parts = w.n_split > 1;
+      constexpr int kCols = D / 4;  // columns a round
 #pragma unroll
-      for (int x = 0; x < D / 64; ++x) {
-        float o[32];
+      for (int y = 0; y < 2; ++y) {
+        float o[kCols];
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) o[k] = 0.f;
         if (n > 0) {
-          tmem_ld32(to + 32 * x, o);
-          tmem_wait_ld32(o);
+          if constexpr (D == 128) {
+            tmem_ld32(to + kCols * y, o);
+            tmem_wait_ld32(o);
+          } else {
+            tmem_ld16f(to + kCols * y, o);
+            tmem_wait_ld16f(o);
+          }
+        }
+        if (parts) {
+#pragma unroll
+          for (int k = 0; k < kCols / 4; ++k)
+            *reinterpret_cast<uint4*>(stage + k_off<D>(lane, k)) =
+                make_uint4(__float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]),
+                           __float_as_uint(o[4 * k + 3]));
         } else {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0.f;
-        }
+          for (int k = 0; k < kCols / 8; ++k) {
+            uint32_t h[4];
 #pragma unroll
-        for (int k = 0; live && k < 8; ++k) {
-          const int d4 = half * (D / 8) + 8 * x + k;
-          const float4 v = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          if (w.n_split == 1)
-            finish_row<D>(a, orow, d4, v, m, l);
-          else
-            *reinterpret_cast<float4*>(ws.o + prow * D + 4 * d4) = v;
+            for (int e = 0; e < 4; ++e) {
+              const __nv_bfloat162 x = __floats2bfloat162_rn(o[8 * k + 2 * e] * f, o[8 * k + 2 * e + 1] * f);
+              h[e] = *reinterpret_cast<const uint32_t*>(&x);
+            }
+            *reinterpret_cast<uint4*>(stage + k_off<D>(lane, y * (kCols / 8) + k)) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
         }
-        __syncwarp();
+        if (parts || y == 1) {
+          __syncwarp();
+          constexpr int kChunks = D / 16;  // 16-byte chunks of a row
+          const int cc = lane % kChunks;
+#pragma unroll
+          for (int e = 0; e < kChunks; ++e) {
+            const int rr = e * (32 / kChunks) + lane / kChunks;
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + k_off<D>(rr, cc));
+            const uint32_t to_row = __shfl_sync(0xffffffffu, olo, rr);
+            if (__shfl_sync(0xffffffffu, static_cast<int>(live), rr)) {
+              if (parts)
+                *reinterpret_cast<uint4*>(ws.o + (prow - lane + rr) * D + half * (D / 2) + kCols * y + 4 * cc) = v;
+              else
+                *reinterpret_cast<uint4*>(a.out + static_cast<size_t>(to_row) * D + half * (D / 2) + 8 * cc) = v;
+            }
+          }
+          __syncwarp();
+        }
       }
+      if (live && half == 0 && w.n_split == 1 && a.lse)
+        a.lse[orow] = any ? (m - kLift + log2f(l)) * 0.693147180559945f : -INFINITY;
       if (live && half == 0 && w.n_split > 1) ws.ml[prow] = make_float2(m, l);
     }
   }
