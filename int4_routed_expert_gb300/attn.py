@@ -50,10 +50,11 @@ _lib = None
 torch = None    # imported with the library: a call costs a few microseconds, and a module lookup is part of it
 _codes = {}     # torch dtype -> moe_dtype_t
 _raw_stream = None
+_int32 = None
 
 
 def _load() -> C.CDLL:
-    global _lib, torch, _raw_stream
+    global _lib, torch, _raw_stream, _int32
     if _lib is not None:
         return _lib
     import torch as _torch
@@ -76,6 +77,7 @@ def _load() -> C.CDLL:
         fn = getattr(L, name)
         fn.restype, fn.argtypes = res, args
     torch = _torch
+    _int32 = torch.int32
     _codes.update({torch.bfloat16: MOE_BF16, torch.float32: MOE_F32})
     # the stream's handle alone; torch.cuda.current_stream() builds an object, 3 us
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
@@ -91,8 +93,8 @@ def _dtype(t, name: str) -> int:
     return code
 
 
-def _stream(stream, device) -> int:
-    return _raw_stream(device.index) if stream is None else stream.cuda_stream
+def _stream(stream, index: int) -> int:
+    return _raw_stream(index) if stream is None else stream.cuda_stream
 
 
 def _rows(x, name: str, heads: int, dim: int, device) -> int:
@@ -147,6 +149,7 @@ class Rope:
                  factor: float = 1.0, original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
                  inv_freq=None, amplitude: float | None = None):
         self.h = None
+        self._layouts = {}
         if inv_freq is None:
             inv_freq, amp = rope_frequencies(rot_dim, theta, scaling, factor, original_len, beta_fast, beta_slow)
         else:
@@ -166,42 +169,83 @@ class Rope:
         """Rotates q [tokens, heads, head_dim] (and k) at positions [tokens] int32; returns q's result, or
         (q's, k's) when k is given.  Tokens may be strided (parts of one projection); q_out is q rotates in
         place."""
+        if q_out is None and k_out is None:
+            # the checks of a layout (shapes, strides, types) once: a call is a few microseconds
+            key = (q.shape, q.stride(), q.dtype) if k is None else \
+                (q.shape, q.stride(), q.dtype, k.shape, k.stride(), k.dtype)
+            known = self._layouts.get(key)
+            if known is None:
+                known = self._layout(key, q, k)
+            T, D, dt, tq, tk, contiguous = known
+            dev = q.get_device()
+            if dev < 0 or positions.dtype is not _int32 or positions.shape != (T,) or positions.get_device() != dev \
+                    or not positions.is_contiguous() or (tk is not None and k.get_device() != dev):
+                self._refuse(q, k, positions)
+            if contiguous:
+                q_out = torch.empty_like(q)
+                k_out = None if tk is None else torch.empty_like(k)
+            else:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+                k_out = None if tk is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        else:
+            known = self._layout(None, q, k)
+            T, D, dt, tq, tk, _ = known
+            dev = q.get_device()
+            if dev < 0 or positions.dtype is not _int32 or positions.shape != (T,) or positions.get_device() != dev \
+                    or not positions.is_contiguous() or (tk is not None and k.get_device() != dev):
+                self._refuse(q, k, positions)
+            if k is None and k_out is not None:
+                raise ValueError("k_out needs k")
+            q_out, tq.y_stride = self._out("q", q, q_out)
+            if tk is not None:
+                k_out, tk.y_stride = self._out("k", k, k_out)
+        if T:
+            tq.x, tq.y = q.data_ptr(), q_out.data_ptr()
+            if tk is not None:
+                tk.x, tk.y = k.data_ptr(), k_out.data_ptr()
+            st = _lib.moe_rope_apply(self.h, tq, tk, D, dt, positions.data_ptr(), T,
+                                     _raw_stream(dev) if stream is None else stream.cuda_stream)
+            if st != MOE_OK:
+                raise MoeError(st, moe.moe_last_error(None))
+        return q_out if tk is None else (q_out, k_out)
+
+    def _layout(self, key, q, k):
+        """(tokens, head_dim, dtype, q's and k's argument structs, contiguous) of a checked layout."""
         dev, dtype = q.device, q.dtype
         if q.dim() != 3 or not q.is_cuda:
             raise ValueError(f"q must be a CUDA tensor [tokens, heads, head_dim], got {tuple(q.shape)} on {dev}")
         T, H, D = q.shape
-        dt = _codes.get(dtype)
-        if dt is None:
-            raise TypeError(f"q must be fp32 or bf16, got {dtype}")
-        if positions.dtype != torch.int32 or positions.dim() != 1 or positions.shape[0] != T \
-                or positions.device != dev or not positions.is_contiguous():
-            raise ValueError(f"positions must be a contiguous int32 tensor of {T} entries on {dev}")
-        tq, q_out = self._pair("q", q, q_out, T, H, D, dtype, dev)
-        tk = None
+        dt = _dtype(dtype, "q")
+        tq = moe_rope_tensor_t(None, None, H, _rows(q, "q", H, D, dev), H * D)
+        tk, contiguous = None, q.is_contiguous()
         if k is not None:
             if k.dim() != 3 or k.shape[0] != T or k.shape[2] != D or k.dtype != dtype:
                 raise ValueError(f"k must be [{T}, heads, {D}] of {dtype}")
-            tk, k_out = self._pair("k", k, k_out, T, k.shape[1], D, dtype, dev)
-        elif k_out is not None:
-            raise ValueError("k_out needs k")
-        if T:
-            st = _lib.moe_rope_apply(self.h, tq, tk, D, dt, positions.data_ptr(), T, _stream(stream, dev))
-            if st != MOE_OK:
-                raise MoeError(st, moe.moe_last_error(None))
-        return q_out if k is None else (q_out, k_out)
+            tk = moe_rope_tensor_t(None, None, k.shape[1], _rows(k, "k", k.shape[1], D, dev), k.shape[1] * D)
+            contiguous = contiguous and k.is_contiguous()
+        known = (T, D, dt, tq, tk, contiguous)
+        if key is not None:
+            if len(self._layouts) >= 64:
+                self._layouts.clear()
+            self._layouts[key] = known
+        return known
 
     @staticmethod
-    def _pair(name, x, y, T, H, D, dtype, dev):
-        xs = ys = H * D
-        if not x.is_contiguous() or x.device != dev:
-            xs = _rows(x, name, H, D, dev)
+    def _refuse(q, k, positions):
+        if not q.is_cuda:
+            raise ValueError(f"q must be a CUDA tensor [tokens, heads, head_dim], got {tuple(q.shape)} on {q.device}")
+        if k is not None and k.device != q.device:
+            raise ValueError(f"k must be on {q.device}, got {k.device}")
+        raise ValueError(f"positions must be a contiguous int32 tensor of {q.shape[0]} entries on {q.device}")
+
+    @staticmethod
+    def _out(name, x, y):
+        T, H, D = x.shape
         if y is None:
-            y = torch.empty_like(x) if xs == ys else torch.empty((T, H, D), dtype=dtype, device=dev)
-        else:
-            if y.shape != x.shape or y.dtype != dtype:
-                raise ValueError(f"{name}_out must be {(T, H, D)} of {dtype}")
-            ys = _rows(y, name + "_out", H, D, dev)
-        return moe_rope_tensor_t(x.data_ptr(), y.data_ptr(), H, xs, ys), y
+            return torch.empty((T, H, D), dtype=x.dtype, device=x.device), H * D
+        if y.shape != x.shape or y.dtype != x.dtype:
+            raise ValueError(f"{name}_out must be {(T, H, D)} of {x.dtype}")
+        return y, _rows(y, name + "_out", H, D, x.device)
 
     def close(self):
         if self.h:
@@ -230,7 +274,7 @@ class SeqBatch:
         if cu_q.shape[0] != n + 1 or page_table.shape[0] != n:
             raise ValueError(f"{n} sequences need cu_q of {n + 1} entries and page_table of {n} rows")
         self.cu_q, self.kv_len, self.page_table = cu_q, kv_len, page_table
-        self.n_tokens, self.device = n_tokens, cu_q.device
+        self.n_tokens, self.device, self.index = n_tokens, cu_q.device, cu_q.get_device()
         self.c = moe_kv_batch_t(n, n_tokens, max_q_len, max_kv_len, page_table.shape[1], cu_q.data_ptr(),
                                 kv_len.data_ptr(), page_table.data_ptr())
 
@@ -256,6 +300,8 @@ class KVCache:
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
         self.n_q_heads, self.n_kv_heads, self.head_dim, self.page_size = n_q_heads, H, D, S
         self.device = k_codes.device
+        self._index = k_codes.get_device()
+        self._row = {}  # checked layouts of the calls' tensors: (name, shape, stride) -> elements between tokens
         self.default_scale = D ** -0.5
         cfg = moe_kv_config_t(n_q_heads, H, D, S, P, max_seqs, max_tokens, max_kv_len)
         store = moe_kv_store_t(*(t.data_ptr() for t in (k_codes, v_codes, k_scale, v_scale)))
@@ -280,10 +326,16 @@ class KVCache:
             raise MoeError(st, (_lib.moe_kv_last_error(self.h) or b"").decode())
 
     def _tokens(self, x, name, heads, batch):
-        s = _rows(x, name, heads, self.head_dim, self.device)
-        if x.shape[0] != batch.n_tokens or batch.device != self.device:
-            raise ValueError(f"{name} and the batch must have the same tokens and device, got {x.shape[0]} on "
-                             f"{self.device} and {batch.n_tokens} on {batch.device}")
+        key = (name, x.shape, x.stride())
+        s = self._row.get(key)
+        if s is None:
+            s = _rows(x, name, heads, self.head_dim, self.device)
+            if len(self._row) >= 64:
+                self._row.clear()
+            self._row[key] = s
+        if x.shape[0] != batch.n_tokens or x.get_device() != self._index or batch.index != self._index:
+            raise ValueError(f"{name} and the batch must have the same tokens on {self.device}, got {x.shape[0]} on "
+                             f"{x.device} and {batch.n_tokens} on {batch.device}")
         return s
 
     def write(self, k, v, batch: SeqBatch, stream=None) -> None:
@@ -293,7 +345,7 @@ class KVCache:
         if k.dtype != v.dtype:
             raise TypeError("k and v must have one dtype")
         self._check(_lib.moe_kv_write(self.h, k.data_ptr(), ks, v.data_ptr(), vs, _dtype(k.dtype, "k"), batch.c,
-                                      _stream(stream, self.device)))
+                                      _stream(stream, self._index)))
 
     def read(self, batch: SeqBatch, dtype=None, k_out=None, v_out=None, stream=None):
         """The batch's new tokens as values: (keys, values) [tokens, kv heads, head_dim] (bf16 by default)."""
@@ -301,16 +353,16 @@ class KVCache:
         if dtype is None:
             dtype = k_out.dtype if k_out is not None else torch.bfloat16
         code = _dtype(dtype, "dtype")
-        if batch.device != dev:
+        if batch.index != self._index:
             raise ValueError(f"the batch must be on {dev}, got {batch.device}")
-        for name, t in (("k_out", k_out), ("v_out", v_out)):
+        for name, t in (("k_out", k_out), ("v_out", v_out)) if k_out is not None or v_out is not None else ():
             if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.device != dev):
                 raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {dev}")
         if k_out is None:
             k_out = torch.empty(shape, dtype=dtype, device=dev)
         if v_out is None:
             v_out = torch.empty(shape, dtype=dtype, device=dev)
-        self._check(_lib.moe_kv_read(self.h, k_out.data_ptr(), v_out.data_ptr(), code, batch.c, _stream(stream, dev)))
+        self._check(_lib.moe_kv_read(self.h, k_out.data_ptr(), v_out.data_ptr(), code, batch.c, _stream(stream, self._index)))
         return k_out, v_out
 
     def attend(self, q, batch: SeqBatch, out=None, lse=None, scale: float | None = None, causal: bool = True,
@@ -337,7 +389,7 @@ class KVCache:
         mask = moe_kv_mask_t(self.default_scale if scale is None else scale, 1 if causal else 0, window, sinks)
         self._check(_lib.moe_kv_attend(self.h, q.data_ptr(), qs, out.data_ptr(),
                                        lse.data_ptr() if lse is not None else None, mask, batch.c,
-                                       _stream(stream, dev)))
+                                       _stream(stream, self._index)))
         return out
 
     def device_status(self) -> int:
