@@ -147,7 +147,7 @@ moe_status_t moe_kv_read(moe_kv_t* h, void* k_out, void* v_out, moe_dtype_t dtyp
  *   causal == 0, or j <= P and (window == 0 or j > P - window or j < sinks).
  * A row that sees nothing gets 0 (and lse -inf).  window >= 0 and sinks >= 0
  * need causal != 0 when they are not 0.  q, out: [n_tokens][n_q_heads]
- * [head_dim] bf16, q_stride elements between q's tokens; lse: [n_tokens]
+ * [head_dim] bf16, not overlapping, q_stride elements between q's tokens; lse: [n_tokens]
  * [n_q_heads] fp32 natural logarithms of the softmax denominators, or NULL. */
 typedef struct {
   float scale; /* finite; usually head_dim ^ -0.5 */

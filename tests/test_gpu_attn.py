@@ -458,3 +458,37 @@ def test_no_allocation_after_create(m):
         c.attend(q, bt.b, out=out)
     torch.cuda.synchronize()
     assert torch.cuda.mem_get_info()[0] == free
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("scale", [0.0, -0.11, 1.7])
+def test_attend_scales(m, new, scale):
+    """Softmax scales of zero (every visible key counts alike), negative and large."""
+    g = gen(20)
+    bt = R.Batch([300, 77], [new, new], 32, DEV)
+    c = make_cache(m, g, bt, 8, 2, 64, fill="normal")
+    check(c, bt, randn(g, 2 * new, 8, 64, dtype=torch.bfloat16), scale=scale)
+
+
+@pytest.mark.parametrize("new,hq,hkv", [(1, 8, 8), (1, 24, 1), (2, 24, 1), (3, 64, 4), (40, 40, 5)])
+def test_attend_is_repeatable(m, new, hq, hkv):
+    """Many splits, joined in their order whatever the order of arrival: the same bits every time."""
+    g = gen(21)
+    bt = R.Batch([20000, 4097], [new, new], 64, DEV)
+    c = make_cache(m, g, bt, hq, hkv, 128, fill="normal")
+    q = randn(g, 2 * new, hq, 128, dtype=torch.bfloat16)
+    want = check(c, bt, q)
+    for _ in range(20):
+        assert torch.equal(c.attend(q, bt.b), want)
+
+
+def test_decoder_step_example():
+    """Token by token and as a prompt: the cache's blocks differ only in the scales they had on the way (codes
+    rounded once more below 2^-6 of a scale), so the layers agree far inside e4m3's half step of 2^-4."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decoder_step.py")
+    spec = importlib.util.spec_from_file_location("decoder_step", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    assert ex.main() < 2.0 ** -4
