@@ -498,7 +498,7 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
   a.sinks = a.window ? mask->sinks : 0;
   a.hq = h->cfg.n_q_heads;
   a.G = h->cfg.n_q_heads / h->cfg.n_kv_heads;
-  const bool tiles = static_cast<int64_t>(c.max_q) * a.G >= 128;
+  const bool tiles = static_cast<int64_t>(c.max_q) * a.G > 32;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return launched(h, tiles ? moe::attn_tiles_launch(c, a, h->ws, h->maps, h->n_sm, s)
                            : moe::attn_few_launch(c, a, h->ws, h->maps, h->n_sm, s),

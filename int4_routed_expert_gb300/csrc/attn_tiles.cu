@@ -67,7 +67,11 @@ enum Bar {
   kBars = 30
 };
 
-template <int D>
+// DUAL: calls whose sequences have at most 128 rows a kv head.  The two M tiles
+// are the same rows then, each with every other tile of keys and with sums of
+// its own, which the join takes for two splits: one's softmax still runs under
+// the other's products.
+template <int D, bool DUAL>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tiles_kernel(const KvView c, const AttnArgs a, const AttnWs ws, const Plan pl,
                       const __grid_constant__ CUtensorMap k_map) {
@@ -91,11 +95,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int t_begin = split * pl.tiles_per_split;
   const int t_end = min(w.k.n_t, t_begin + pl.tiles_per_split);
   const int n = t_end - t_begin;  // 0 when the rows see nothing
-  const int n_mt = w.r1 - w.r0 > kM ? 2 : 1;
+  const int n_mt = DUAL || w.r1 - w.r0 > kM ? 2 : 1;
 
   auto bar = [&](int i) { return base_u + L_::kBar + 8 * i; };
   if (threadIdx.x == 0) {
-    const int count[kBars] = {256 * n_mt, 1, 1, 1, 1, 1, 1, 1, 1, 128, 128, 128, 128,
+    const int count[kBars] = {DUAL ? 256 : 256 * n_mt, 1, 1, 1, 1, 1, 1, 1, 1, 128, 128, 128, 128,
                               1, 1, 1, 1, 256, 256, 1, 1, 8, 8, 8, 8, 8, 8, 8, 8, 1};
 #pragma unroll
     for (int i = 0; i < kBars; ++i) mbar_init(bar(i), count[i]);
@@ -121,41 +125,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t q_desc = sdesc_k<D>(base_u + L_::kQ), k_desc = sdesc_k<D>(base_u + L_::kK);
       const uint64_t v_desc = sdesc_sw128_mn(base_u + L_::kV, Io<D>::kHalf);
       auto issue_s = [&](int i, int stage) {
-        mma_s<D>(tmem + i * 128, q_desc + i * (2 * L_::kMat8 >> 4), k_desc + stage * (L_::kMat8 >> 4), id_s);
+        mma_s<D>(tmem + i * 128, q_desc + (DUAL ? 0 : i) * (2 * L_::kMat8 >> 4),
+                 k_desc + stage * (L_::kMat8 >> 4), id_s);
         mma_commit(bar(kSFull + i));
       };
-      bool ok = mbar_wait(bar(kQFull), 0, c.err) && mbar_wait(bar(kKFull), 0, c.err);
+      auto k_wait = [&](int j) { return mbar_wait(bar(kKFull + j % kKStages), (j / kKStages) & 1, c.err); };
+      auto issue_o = [&](int i, int j, bool first) {
+        const uint32_t ot = tmem + 256 + i * 128, pt = tmem + i * 128;
+        const uint64_t vd = v_desc + (j & 1) * (L_::kMat >> 4);
+        mma_o(ot, pt, vd, id_o, first);
+        mma_o(ot, pt + 64, vd + (64 * 128 >> 4), id_o, 0);  // P's halves start where S's do
+      };
+      bool ok = mbar_wait(bar(kQFull), 0, c.err) && k_wait(0);
       if (ok) {
         fence_after_sync();
-        for (int i = 0; i < n_mt; ++i) issue_s(i, 0);
+        issue_s(0, 0);
+        if (!DUAL && n_mt == 2) issue_s(1, 0);
         mma_commit(bar(kKEmpty));
+      }
+      if (DUAL && ok && n > 1 && (ok = k_wait(1))) {
+        fence_after_sync();
+        issue_s(1, 1);
+        mma_commit(bar(kKEmpty + 1));
       }
       // S of tile j + 1 goes straight behind O += P V of tile j, whose P it
       // overwrites: one thread's products run on the tensor pipe in the order of
       // their issue.  (Waiting for the product before issuing S costs a commit's
       // and a wait's latency, about 1000 clocks a tile: prompt of 8192, 822 us
       // to 1009 us.)
-      int ks = 0, kph = 0;  // K stage and parity of tile j
-      for (int j = 0; ok && j < n; ++j) {
-        const int st = j & 1;
-        const uint64_t vd = v_desc + st * (L_::kMat >> 4);
-        if (++ks == kKStages) ks = 0, kph ^= 1;  // those of tile j + 1
+      for (int j = 0; DUAL && ok && j < n; ++j) {
+        const int i = j & 1, next = j + 2;
+        ok = mbar_wait(bar(kPFull + i), (j >> 1) & 1, c.err) && mbar_wait(bar(kVFull + i), (j >> 1) & 1, c.err);
+        if (!ok) break;
+        fence_after_sync();
+        issue_o(i, j, j < 2);
+        mma_commit(bar(kVEmpty + i));
+        if (next >= n) {
+          mma_commit(bar(kOFull + i));
+        } else if ((ok = k_wait(next))) {
+          fence_after_sync();
+          issue_s(i, next % kKStages);
+          mma_commit(bar(kKEmpty + next % kKStages));
+        }
+      }
+      for (int j = 0; !DUAL && ok && j < n; ++j) {
         for (int i = 0; ok && i < n_mt; ++i) {
-          ok = mbar_wait(bar(kPFull + i), j & 1, c.err) && (i > 0 || mbar_wait(bar(kVFull + st), (j >> 1) & 1, c.err));
+          ok = mbar_wait(bar(kPFull + i), j & 1, c.err) &&
+               (i > 0 || mbar_wait(bar(kVFull + (j & 1)), (j >> 1) & 1, c.err));
           if (!ok) break;
           fence_after_sync();
-          const uint32_t ot = tmem + 256 + i * 128, pt = tmem + i * 128;
-          mma_o(ot, pt, vd, id_o, j == 0);
-          mma_o(ot, pt + 64, vd + (64 * 128 >> 4), id_o, 0);  // P's halves start where S's do
-          if (i == n_mt - 1) mma_commit(bar(kVEmpty + st));
+          issue_o(i, j, j == 0);
+          if (i == n_mt - 1) mma_commit(bar(kVEmpty + (j & 1)));
           if (j == n - 1) {
             mma_commit(bar(kOFull + i));
-          } else {
-            ok = i > 0 || mbar_wait(bar(kKFull + ks), kph, c.err);
-            if (!ok) break;
+          } else if ((ok = i > 0 || k_wait(j + 1))) {
             fence_after_sync();
-            issue_s(i, ks);
-            if (i == n_mt - 1) mma_commit(bar(kKEmpty + ks));
+            issue_s(i, (j + 1) % kKStages);
+            if (i == n_mt - 1) mma_commit(bar(kKEmpty + (j + 1) % kKStages));
           }
         }
       }
@@ -170,7 +196,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                [&](int j) { return mbar_wait(bar(kVEmpty + (j & 1)), ((j >> 1) & 1) ^ 1, c.err); });
   } else if ((wg >> 1) < n_mt) {
     const int i = wg >> 1, half = wg & 1, row = threadIdx.x & 127;  // M tile, half of the keys
-    const int r = w.r0 + i * kM + row;
+    const int row0 = w.r0 + (DUAL ? 0 : i * kM);  // of the M tile
+    const int r = row0 + row;
     const bool live = r < w.r1;
     const int tok = live ? r / a.G : 0;
     const int head = hk * a.G + (live ? r - tok * a.G : 0);
@@ -179,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = tmem + i * 128 + lanes + half * 64, to = tmem + 256 + i * 128 + lanes + half * (D / 2);
     // what the row's two threads tell each other, two buffers in turn
     float* pair = reinterpret_cast<float*>(smem + L_::kPair) + i * 512;
+    const int mine = DUAL ? (n + 1 - i) >> 1 : n;  // tiles of this M tile
     auto other = [&](int buf, float mine) {
       pair[buf * 256 + half * 128 + row] = mine;
       named_sync(1 + i, 256);
@@ -186,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     float m = -INFINITY, l = 0.f, lscale = 0.f;  // lscale >= 0: a negative scale turns the query's sign
     bool ok = true;
-    if (n > 0) {
+    if (n > 0 && (!DUAL || i == 0)) {
       // The rows' queries, each brought to [2^7, 2^8) by a power of two, as two
       // e4m3 terms: a warp takes 16 of the M tile's rows, D / 8 lanes a row.
       constexpr int kLanes = D / 8, kPer = 32 / kLanes, kIts = 16 / kPer;  // lanes a row, rows a pass, passes
@@ -194,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int sub = lane / kLanes, part = lane % kLanes, wrow = (warp & 7) * 16;
 #pragma unroll
       for (int x = 0; x < kIts; ++x) {
-        const int gr = w.r0 + i * kM + wrow + x * kPer + sub;
+        const int gr = row0 + wrow + x * kPer + sub;
         const int tk = gr / a.G;
         raw[x] = make_uint4(0, 0, 0, 0);
         if (gr < w.r1)
@@ -202,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                              a.q + (static_cast<int64_t>(w.q.q0) + tk) * a.q_stride +
                              (static_cast<int64_t>(hk) * a.G + gr - tk * a.G) * D) + part);
       }
-      char* dst = smem + L_::kQ + i * 2 * L_::kMat8;
+      char* dst = smem + L_::kQ + (DUAL ? 0 : i) * 2 * L_::kMat8;
 #pragma unroll
       for (int x = 0; x < kIts; ++x) {
         const uint32_t u[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
@@ -231,16 +259,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(kQFull));
-      named_sync(1 + i, 256);
-      lscale = pair[256 + row];
-      named_sync(1 + i, 256);  // (before the pair buffers' first use)
+    }
+    // (both barriers of one count: the second comes before the pair buffers' first use)
+    auto all_sync = [&]() { DUAL ? named_sync(3, 512) : named_sync(1 + i, 256); };
+    if (n > 0) {
+      all_sync();
+      lscale = reinterpret_cast<const float*>(smem + L_::kPair)[(DUAL ? 0 : i * 512) + 256 + row];
+      all_sync();
     }
     // the range that all rows of the CTA see whole
     const int p_lo = w.base_p + w.r0 / a.G, p_hi = w.base_p + (w.r1 - 1) / a.G;
-    for (int j = 0; j < n; ++j) {
+    for (int t = 0; t < mine; ++t) {
+      const int j = DUAL ? 2 * t + i : t;
       // (S of this tile says that O += P V of the tile before is done, too)
       ok = __all_sync(0xffffffffu, mbar_wait(bar(kCFull + j % kConstRing), (j / kConstRing) & 1, c.err) &&
-                                       mbar_wait(bar(kSFull + i), j & 1, c.err));
+                                       mbar_wait(bar(kSFull + i), t & 1, c.err));
       if (!ok) break;
       fence_after_sync();
       const float4* cn = io.scales(j) + 4 * half;
@@ -271,13 +304,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           mt = fmaxf(mt, fmaf(fmaxf(t0, t1), fmaxf(lscale * z.x, kTiny), z.y));
         }
       }
-      mt = fmaxf(mt, other(j & 1, mt));
+      mt = fmaxf(mt, other(t & 1, mt));
       if (__any_sync(0xffffffffu, mt > m + kRescale)) {
         const float nm = fmaxf(m, mt);
         const float f = nm == m ? 1.f : ex2(m - nm);
         m = nm;
         l *= f;
-        if (j > 0) {
+        if (t > 0) {
           // half of the output's columns a thread
 #pragma unroll
           for (int x = 0; x < D / 32; ++x) {
@@ -324,8 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_before_sync();
       mbar_arrive(bar(kPFull + i));
     }
-    if (ok && n > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(kOFull + i), 0, c.err));
-    if (n > 0) l += other(n & 1, l);
+    if (ok && mine > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(kOFull + i), 0, c.err));
+    if (mine > 0) l += other(mine & 1, l);
     if (ok) {
       fence_after_sync();
       const size_t orow = (static_cast<size_t>(w.q.q0) + tok) * a.hq + head;
@@ -339,14 +372,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float f = any ? 1.f / l : 0.f;
       char* stage = smem + L_::kQ + warp * (32 * D);
       const uint32_t olo = static_cast<uint32_t>(orow);
-      const bool parts = w.n_split > 1;
+      const bool parts = DUAL || w.n_split > 1;
       constexpr int kCols = D / 4;  // columns a round
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         float o[kCols];
 #pragma unroll
         for (int k = 0; k < kCols; ++k) o[k] = 0.f;
-        if (n > 0) {
+        if (mine > 0) {
           if constexpr (D == 128) {
             tmem_ld32(to + kCols * y, o);
             tmem_wait_ld32(o);
@@ -392,9 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
       }
-      if (live && half == 0 && w.n_split == 1 && a.lse)
+      if (live && half == 0 && !parts && a.lse)
         a.lse[orow] = any ? (m - kLift + log2f(l)) * 0.693147180559945f : -INFINITY;
-      if (live && half == 0 && w.n_split > 1) ws.ml[prow] = make_float2(m, l);
+      if (live && half == 0 && parts) ws.ml[prow] = make_float2(m, l);
     }
   }
   __syncwarp();
@@ -403,9 +436,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// Joins the splits of every row that has more than one.
+// Joins the splits (and the M tiles of DUAL) of every row that has more than one.
 constexpr int kJoinThreads = 256;
-template <int D>
+template <int D, bool DUAL>
 __global__ void __launch_bounds__(kJoinThreads)
     attn_join_kernel(const KvView c, const AttnArgs a, const AttnWs ws, const Plan pl) {
   constexpr int kPer = kJoinThreads / (D / 4);  // rows of a block
@@ -416,18 +449,18 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int64_t s = tile_id / pl.row_tiles;
   const int hk = static_cast<int>(s % c.hkv), b = static_cast<int>(s / c.hkv);
   Work w;
-  if (b >= c.n_seqs || !work_of<kRows>(c, a, pl, b, hk, rt, w) || w.n_split == 1 || w.r0 + row >= w.r1) return;
+  if (b >= c.n_seqs || !work_of<kRows>(c, a, pl, b, hk, rt, w) || (!DUAL && w.n_split == 1) || w.r0 + row >= w.r1) return;
   const int tok = (w.r0 + row) / a.G;
   const size_t orow = (static_cast<size_t>(w.q.q0) + tok) * a.hq + hk * a.G + (w.r0 + row) - tok * a.G;
-  join_row<D>(a, ws, static_cast<size_t>(tile_id) * pl.splits * kRows + row, kRows, w.n_split, orow,
-              threadIdx.x % (D / 4));
+  join_row<D>(a, ws, static_cast<size_t>(tile_id) * pl.splits * kRows + row, DUAL ? kM : kRows,
+              DUAL ? 2 * w.n_split : w.n_split, orow, threadIdx.x % (D / 4));
 }
 
-template <int D>
+template <int D, bool DUAL>
 cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const CUtensorMap& k_map, int n_sm,
                    cudaStream_t s) {
   static std::atomic<size_t> done[kMaxDevices];
-  const void* fn = reinterpret_cast<const void*>(attn_tiles_kernel<D>);
+  const void* fn = reinterpret_cast<const void*>(attn_tiles_kernel<D, DUAL>);
   if (const cudaError_t e = opt_in_smem(fn, done, Lay<D>::kSmem); e != cudaSuccess) return e;
   Plan pl;
   const int64_t rows = static_cast<int64_t>(c.max_q) * a.G;
@@ -442,11 +475,11 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const C
   pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
   const int64_t grid = base * pl.splits;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  attn_tiles_kernel<D><<<static_cast<unsigned>(grid), kThreads, Lay<D>::kSmem, s>>>(c, a, ws, pl, k_map);
+  attn_tiles_kernel<D, DUAL><<<static_cast<unsigned>(grid), kThreads, Lay<D>::kSmem, s>>>(c, a, ws, pl, k_map);
   cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || pl.splits == 1) return e;
+  if (e != cudaSuccess || (!DUAL && pl.splits == 1)) return e;
   const int64_t items = base * kRows, per = kJoinThreads / (D / 4);
-  attn_join_kernel<D><<<static_cast<unsigned>((items + per - 1) / per), kJoinThreads, 0, s>>>(c, a, ws, pl);
+  attn_join_kernel<D, DUAL><<<static_cast<unsigned>((items + per - 1) / per), kJoinThreads, 0, s>>>(c, a, ws, pl);
   return cudaGetLastError();
 }
 
@@ -454,7 +487,9 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const C
 
 cudaError_t attn_tiles_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const KvMaps& maps,
                               int n_sm, cudaStream_t s) {
-  return c.D == 128 ? launch<128>(c, a, ws, maps.k_tile, n_sm, s) : launch<64>(c, a, ws, maps.k_tile, n_sm, s);
+  const bool dual = static_cast<int64_t>(c.max_q) * a.G <= kM;
+  if (c.D == 128) return (dual ? launch<128, true> : launch<128, false>)(c, a, ws, maps.k_tile, n_sm, s);
+  return (dual ? launch<64, true> : launch<64, false>)(c, a, ws, maps.k_tile, n_sm, s);
 }
 
 }  // namespace moe
