@@ -9,7 +9,7 @@
 // to the largest contribution, whatever the blocks' scales are.  m moves only
 // when it would grow by 2^5.
 //
-// A CTA takes N = 16, 32 or 64 rows of a kv head and walks over tiles of 128
+// A CTA takes N = 16 or 32 rows of a kv head and walks over tiles of 128
 // keys, multiplied as they are stored:
 //   S^T[128 keys x 2 N]   = K [Q1; Q2]^T         the bf16 query as two e4m3 terms
 //   P[128 keys x 4 N]                            a thread a key
@@ -37,24 +37,24 @@ constexpr float kFewLift = 5.f, kFewRescale = 3.f;  // weights below 2^8: an e4m
 
 enum Bar {
   kQFull = 0,
-  kKFull = 1,    // [4] key codes
-  kKEmpty = 5,   // [4]
-  kVFull = 9,    // [4] value codes
-  kVEmpty = 13,  // [4]
-  kSFull = 17,   // [2] S^T
-  kPFull = 19,   // [2] P
-  kODone = 21,   // [2] O^T += V^T P, by buffer of P
-  kCFull = 23,   // [8] scales
-  kDrain = 31,
-  kJoin = 32,    // partial results
-  kBars = 33
+  kKFull = 1,    // [3] key codes
+  kKEmpty = 4,   // [3]
+  kVFull = 7,    // [3] value codes
+  kVEmpty = 10,  // [3]
+  kSFull = 13,   // [2] S^T
+  kPFull = 15,   // P
+  kODone = 16,   // O^T += V^T P
+  kCFull = 17,   // [8] scales
+  kDrain = 25,
+  kJoin = 26,    // partial results
+  kBars = 27
 };
 
-// Up to 32 rows keep to half an SM, so that two CTAs cover each other's bubbles.
+// A CTA keeps to half an SM, so that two CTAs cover each other's bubbles.
 template <int D, int N>
 struct Lay {
-  static constexpr int kStages = N == 16 ? 3 : N == 32 ? 2 : 4;  // of key codes and of value codes
-  static constexpr int kCtas = N == 64 ? 1 : 2;  // a SM
+  static constexpr int kStages = N == 16 ? 3 : 2;  // of key codes and of value codes
+  static constexpr int kCtas = 2;                        // a SM
   using Io = TileIo<D, kStages, kStages, 0>;
   static constexpr int kGroups = N / 16;  // softmax groups of 128 threads
   static constexpr int kThreads = 128 * kGroups + 64;
@@ -62,8 +62,7 @@ struct Lay {
   static constexpr int kK = kQ + (2 * N * D + 1023) / 1024 * 1024;
   static constexpr int kV = kK + kStages * Io::kMat8;
   static constexpr int kP = kV + kStages * Io::kMat8;  // [128 keys][4 N]
-  static constexpr int kPs = N == 64 ? 2 : 1;  // buffers of P
-  static constexpr int kConst = kP + kPs * kKeys * 4 * N;
+  static constexpr int kConst = kP + kKeys * 4 * N;
   static constexpr int kRow = kConst + kConstRing * 8 * 16;  // [7][N]: see Rows
   static constexpr int kRed = kRow + 7 * N * 4;              // [4][N] floats
   static constexpr int kBar = kRed + 4 * N * 4;
@@ -87,12 +86,12 @@ struct Rows {
 };
 
 // P's operand layout: a key's terms in a row of 4 N bytes, term by term; rows
-// of 64 (N = 16) or 128 bytes, swizzled (N = 64: two blocks of 128-byte rows).
+// of 64 or 128 bytes, swizzled.
 // Byte offset of 16-byte chunk c of a key.
 template <int N>
 __device__ __forceinline__ uint32_t p_off(int key, int c) {
   if constexpr (N == 16) return key * 64 + ((c ^ ((key >> 1) & 3)) << 4);
-  return (c >> 3) * (kKeys * 128) + key * 128 + (((c & 7) ^ (key & 7)) << 4);
+  return key * 128 + ((c ^ (key & 7)) << 4);
 }
 
 // MN-major operand of e4m3 codes: rows of `row` (64 or 128) bytes along M or N
@@ -217,8 +216,8 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
   auto bar = [&](int i) { return base_u + L_::kBar + 8 * i; };
   if (threadIdx.x == 0) {
     constexpr int kS = 128 * L_::kGroups, kG = L_::kGroups;
-    const int count[kBars] = {kS, 1, 1, 1, 1, kG, kG, kG, kG, 1, 1, 1, 1, 1, 1, 1, 1,
-                              1,  1, kS, kS, 1, 1, 8, 8, 8, 8, 8, 8, 8, 8, 1, 1};
+    const int count[kBars] = {kS, 1, 1, 1, kG, kG, kG, 1, 1, 1, 1, 1, 1, 1,
+                              1,  kS, 1, 8, 8, 8, 8, 8, 8, 8, 8, 1, 1};
 #pragma unroll
     for (int i = 0; i < kBars; ++i) mbar_init(bar(i), count[i]);
     fence_barrier_init();
@@ -246,8 +245,8 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
       const uint64_t q_desc = sdesc_k<D>(base_u + L_::kQ), k_desc = sdesc_k<D>(base_u + L_::kK);
       // heads of 64: the accumulator's other 64 rows take the codes one atom on, and are not read
       const uint64_t v_desc = sdesc_mn8(base_u + L_::kV, D, 8 * D);
-      const uint64_t p_desc = sdesc_mn8(base_u + L_::kP, N == 16 ? 64 : 128, kKeys * 128);
-      constexpr int kVStep = 32 * D, kPStep = 32 * (N == 16 ? 64 : 128);
+      const uint64_t p_desc = sdesc_mn8(base_u + L_::kP, 4 * N, 16);
+      constexpr int kVStep = 32 * D, kPStep = 32 * 4 * N;
       auto issue_s = [&](int j) {
         const int ks = j % L_::kStages;
         if (!mbar_wait(bar(kKFull + ks), (j / L_::kStages) & 1, c.err)) return false;
@@ -259,12 +258,12 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
       bool ok = mbar_wait(bar(kQFull), 0, c.err) && issue_s(0) && (n < 2 || issue_s(1));
       for (int j = 0; ok && j < n; ++j) {
         const int vs = j % L_::kStages;
-        ok = mbar_wait(bar(kPFull + j % L_::kPs), (j / L_::kPs) & 1, c.err) && mbar_wait(bar(kVFull + vs), (j / L_::kStages) & 1, c.err);
+        ok = mbar_wait(bar(kPFull), j & 1, c.err) && mbar_wait(bar(kVFull + vs), (j / L_::kStages) & 1, c.err);
         if (!ok) break;
         fence_after_sync();
         mma_ot<kVStep, kPStep>(ot, v_desc + vs * (Io::kMat8 >> 4),
-                             p_desc + j % L_::kPs * (kKeys * 4 * N >> 4), id_o, j == 0);
-        mma_commit(bar(kODone + j % L_::kPs));
+                             p_desc, id_o, j == 0);
+        mma_commit(bar(kODone));
         ok = j + 2 >= n || issue_s(j + 2);
       }
       if (!ok) {
@@ -409,7 +408,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
           l[r] *= rows.f[g0 + r];
         }
         if (j > 0) {
-          ok = mbar_wait(bar(kODone + (j - 1) % L_::kPs), ((j - 1) / L_::kPs) & 1, c.err);
+          ok = mbar_wait(bar(kODone), (j - 1) & 1, c.err);
           __syncwarp();
           fence_after_sync();
 #pragma unroll
@@ -449,20 +448,19 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
         }
         __syncwarp();
       }
-      // the buffer of P has been read; through with V of that tile (once for all groups), K of this one
-      constexpr int kBack = L_::kPs;
-      if (j >= kBack) ok = ok && mbar_wait(bar(kODone + (j - kBack) % kBack), ((j - kBack) / kBack) & 1, c.err);
+      // P of the tile before has been read; through with its V (once for all groups) and with K of this one
+      if (j > 0) ok = ok && mbar_wait(bar(kODone), (j - 1) & 1, c.err);
       if (t == 0) {
         mbar_arrive(bar(kKEmpty + j % L_::kStages));
-        if (grp == 0 && j >= kBack) mbar_arrive(bar(kVEmpty + (j - kBack) % L_::kStages));
+        if (grp == 0 && j > 0) mbar_arrive(bar(kVEmpty + (j - 1) % L_::kStages));
       }
-      char* p = smem + L_::kP + j % kBack * (kKeys * 4 * N);
+      char* p = smem + L_::kP;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         *reinterpret_cast<uint4*>(p + p_off<N>(t, (i * N + g0) >> 4)) = make_uint4(u[i][0], u[i][1], u[i][2], u[i][3]);
       fence_proxy_async_smem();
       fence_before_sync();
-      mbar_arrive(bar(kPFull + j % kBack));
+      mbar_arrive(bar(kPFull));
     }
     // the weights' sums over the warp's keys: half the rows go each way at a step,
     // so that lanes r and r + 16 end with row r's halves
@@ -478,7 +476,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
     l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
     if (lane < NG) red[(warp & 3) * N + g0 + lane] = l[0];
     if (ok && n > 0)
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(kODone + (n - 1) % L_::kPs), ((n - 1) / L_::kPs) & 1, c.err));
+      ok = __all_sync(0xffffffffu, mbar_wait(bar(kODone), (n - 1) & 1, c.err));
     fence_after_sync();
     // thread t has dim t of every row: the terms' columns, the smallest first
     float o[NG];
@@ -611,7 +609,8 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const K
   const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
   const int64_t tiles = max_key_tiles(c, a, N, kKeys);
   const int64_t resident = static_cast<int64_t>(n_sm) * Lay<D, N>::kCtas;
-  const int64_t splits = best_splits(base, resident, tiles, static_cast<int64_t>(ws.cap_rows) / (base * N));
+  const int64_t splits = best_splits(base, resident, tiles, static_cast<int64_t>(ws.cap_rows) / (base * N),
+                                     c.n_seqs > 1);
   pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
   pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
   const int64_t grid = base * pl.splits;
@@ -627,8 +626,8 @@ cudaError_t attn_few_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws
                             int n_sm, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(c.max_q) * a.G;
   if (c.D == 128)
-    return (rows <= 16 ? launch<128, 16> : rows <= 32 ? launch<128, 32> : launch<128, 64>)(c, a, ws, maps, n_sm, s);
-  return (rows <= 16 ? launch<64, 16> : rows <= 32 ? launch<64, 32> : launch<64, 64>)(c, a, ws, maps, n_sm, s);
+    return (rows <= 16 ? launch<128, 16> : launch<128, 32>)(c, a, ws, maps, n_sm, s);
+  return (rows <= 16 ? launch<64, 16> : launch<64, 32>)(c, a, ws, maps, n_sm, s);
 }
 
 }  // namespace moe

@@ -350,12 +350,19 @@ struct Plan {
 // Splits of `tiles` tiles for `base` row tiles on `resident` CTA slots, at most
 // `most`: the least time in sixteenths of a tile, a CTA costing three tiles
 // beside its own (start, first loads, results) and the join half a sixteenth a
-// split.
-inline int64_t best_splits(int64_t base, int64_t resident, int64_t tiles, int64_t most) {
+// split.  Where there are several sequences, `tiles` comes from a bound that
+// most of them stay below: the time is the sum over a batch at the bound and
+// one at half of it, where empty CTAs leave their slots to others and half a
+// round is lost at the end.
+inline int64_t best_splits(int64_t base, int64_t resident, int64_t tiles, int64_t most, bool ragged) {
   const int64_t end = std::max<int64_t>(std::min<int64_t>({tiles, most, 256}), 1);
-  int64_t least = INT64_MAX, best = 1;
+  double least = 1e300;
+  int64_t best = 1;
   for (int64_t s = 1; s <= end; ++s) {
-    const int64_t cost = (base * s + resident - 1) / resident * ((tiles + s - 1) / s + 3) * 16 + s / 2;
+    const double cta = static_cast<double>((tiles + s - 1) / s + 3);
+    const double full = static_cast<double>((base * s + resident - 1) / resident) * cta;
+    const double half = std::max(0.5 * static_cast<double>(base * s) / static_cast<double>(resident) + 0.5, 1.0) * cta;
+    const double cost = (ragged ? full + half : 2 * full) * 16 + static_cast<double>(s);
     if (cost < least) least = cost, best = s;
   }
   return best;

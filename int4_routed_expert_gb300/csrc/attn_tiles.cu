@@ -470,7 +470,7 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const C
   // one CTA a SM: split the keys when the row tiles do not fill the SMs evenly
   // (many row tiles do, the longest first)
   const int64_t splits =
-      base >= 4 * n_sm ? 1 : best_splits(base, n_sm, tiles, static_cast<int64_t>(ws.cap_rows) / (base * kRows));
+      base >= 4 * n_sm ? 1 : best_splits(base, n_sm, tiles, static_cast<int64_t>(ws.cap_rows) / (base * kRows), c.n_seqs > 1);
   pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
   pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
   const int64_t grid = base * pl.splits;
