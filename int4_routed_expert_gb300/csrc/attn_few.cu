@@ -284,10 +284,11 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
       constexpr int kPer = 128 * L_::kGroups / N, kDims = D / kPer;  // threads a row, dims a thread
       const int r = threadIdx.x / kPer, part = threadIdx.x % kPer, gr = w.r0 + r;
       const bool live = gr < w.r1;
-      const int tok = live ? gr / a.G : 0;
+      int tok = 0, head = 0;
+      if (live) w.row(a, r, tok, head);
       const uint4* src = reinterpret_cast<const uint4*>(
           a.q + (static_cast<int64_t>(w.q.q0) + tok) * a.q_stride +
-          (static_cast<int64_t>(hk) * a.G + (live ? gr - tok * a.G : 0)) * D + part * kDims);
+          (static_cast<int64_t>(hk) * a.G + head) * D + part * kDims);
       uint4 raw[kDims / 8];
       float amax = 0.f;
 #pragma unroll
@@ -326,13 +327,13 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
         rows.m[r] = -INFINITY;
         rows.lo[r] = s.lo;
         rows.hi[r] = s.hi;
-        rows.out[r] = (w.q.q0 + tok) * a.hq + hk * a.G + (live ? gr - tok * a.G : 0);
+        rows.out[r] = (w.q.q0 + tok) * a.hq + hk * a.G + head;
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(kQFull));
     }
     named_sync(8, 128 * L_::kGroups);
-    const int p_lo = w.base_p + w.r0 / a.G, p_hi = w.base_p + (w.r1 - 1) / a.G;
+    const int p_lo = w.p_lo, p_hi = w.p_hi;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 * (warp % 4)
     float* red = reinterpret_cast<float*>(smem + L_::kRed);
     bool ok = true, pending = true;  // a row has no reference yet
@@ -609,7 +610,7 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const K
   const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
   const int64_t tiles = max_key_tiles(c, a, N, kKeys);
   const int64_t resident = static_cast<int64_t>(n_sm) * Lay<D, N>::kCtas;
-  const int64_t splits = best_splits(base, resident, tiles, static_cast<int64_t>(ws.cap_rows) / (base * N),
+  const int64_t splits = best_splits(base, resident, tiles, static_cast<int64_t>(ws.cap_rows) / (base * N), 3,
                                      c.n_seqs > 1);
   pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
   pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);

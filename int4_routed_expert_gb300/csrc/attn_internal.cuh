@@ -87,7 +87,8 @@ struct AttnArgs {
   float* lse;
   float scale_log2;  // softmax scale * log2(e)
   int causal, window, sinks;
-  int hq, G;
+  int hq, G;      // query heads, and those of a kv head
+  float inv_g;    // 1 / G
 };
 
 cudaError_t rope_launch(const uint64_t* inc, int rot_dim, float amplitude, bool interleaved,

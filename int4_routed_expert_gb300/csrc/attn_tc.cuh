@@ -156,6 +156,12 @@ __device__ __forceinline__ void tmem_wait_ld16f(float* v) {
                : "memory");
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // Two fp32 operations an instruction.
 __device__ __forceinline__ void fma2(float& x, float& y, float a0, float a1, float b, float c) {
   asm("{\n\t.reg .b64 a, b, c, d;\n\t"
@@ -348,18 +354,18 @@ struct Plan {
 };
 
 // Splits of `tiles` tiles for `base` row tiles on `resident` CTA slots, at most
-// `most`: the least time in sixteenths of a tile, a CTA costing three tiles
-// beside its own (start, first loads, results) and the join half a sixteenth a
+// `most`: the least time in sixteenths of a tile, a CTA costing `start` tiles
+// beside its own (set-up, first loads, results) and the join half a sixteenth a
 // split.  Where there are several sequences, `tiles` comes from a bound that
 // most of them stay below: the time is the sum over a batch at the bound and
 // one at half of it, where empty CTAs leave their slots to others and half a
 // round is lost at the end.
-inline int64_t best_splits(int64_t base, int64_t resident, int64_t tiles, int64_t most, bool ragged) {
+inline int64_t best_splits(int64_t base, int64_t resident, int64_t tiles, int64_t most, int64_t start, bool ragged) {
   const int64_t end = std::max<int64_t>(std::min<int64_t>({tiles, most, 256}), 1);
   double least = 1e300;
   int64_t best = 1;
   for (int64_t s = 1; s <= end; ++s) {
-    const double cta = static_cast<double>((tiles + s - 1) / s + 3);
+    const double cta = static_cast<double>((tiles + s - 1) / s + start);
     const double full = static_cast<double>((base * s + resident - 1) / resident) * cta;
     const double half = std::max(0.5 * static_cast<double>(base * s) / static_cast<double>(resident) + 0.5, 1.0) * cta;
     const double cost = (ragged ? full + half : 2 * full) * 16 + static_cast<double>(s);
@@ -372,8 +378,18 @@ inline int64_t best_splits(int64_t base, int64_t resident, int64_t tiles, int64_
 struct Work {
   Seq q;
   int b, hk, r0, r1, base_p;
+  int tok0, rem0;  // token and head (of the kv head's) of row r0
+  int p_lo, p_hi;  // positions of the first and the last row
   KeyTiles k;
   int n_split;
+
+  // token and head of row r0 + i: (rem0 + i) / G by its reciprocal, exact as the
+  // dividend is below 2^13 and half away from the next whole number
+  __device__ __forceinline__ void row(const AttnArgs& a, int i, int& tok, int& head) const {
+    const int x = rem0 + i, t = static_cast<int>((static_cast<float>(x) + 0.5f) * a.inv_g);
+    tok = tok0 + t;
+    head = x - t * a.G;
+  }
 };
 
 template <int ROWS>
@@ -388,7 +404,13 @@ __device__ __forceinline__ bool work_of(const KvView& c, const AttnArgs& a, cons
   w.r0 = static_cast<int>(r0);
   w.r1 = static_cast<int>(min(R, r0 + ROWS));
   w.base_p = w.q.L - w.q.n;
-  w.k = key_tiles<kKeys>(a, w.q.L, w.base_p + w.r0 / a.G, w.base_p + (w.r1 - 1) / a.G);
+  w.tok0 = w.r0 / a.G;
+  w.rem0 = w.r0 - w.tok0 * a.G;
+  int last, head;
+  w.row(a, w.r1 - 1 - w.r0, last, head);
+  w.p_lo = w.base_p + w.tok0;
+  w.p_hi = w.base_p + last;
+  w.k = key_tiles<kKeys>(a, w.q.L, w.p_lo, w.p_hi);
   w.n_split = max((w.k.n_t + pl.tiles_per_split - 1) / pl.tiles_per_split, 1);
   return true;
 }

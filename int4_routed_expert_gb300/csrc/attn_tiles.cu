@@ -97,6 +97,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n = t_end - t_begin;  // 0 when the rows see nothing
   const int n_mt = DUAL || w.r1 - w.r0 > kM ? 2 : 1;
 
+  // the softmax warps' queries are on their way while all else is set up
+  constexpr int kLanes = D / 8, kPer = 32 / kLanes, kIts = 16 / kPer;  // lanes a row, rows a pass, passes
+  const int sub = lane / kLanes, part = lane % kLanes, wrow = (warp & 7) * 16;
+  uint4 raw[kIts];
+#pragma unroll
+  for (int x = 0; x < kIts; ++x) {
+    const int i = (DUAL ? 0 : (warp >> 3) * kM) + wrow + x * kPer + sub;  // row of the CTA
+    raw[x] = make_uint4(0, 0, 0, 0);
+    if (n > 0 && warp < (DUAL ? 8 : 16) && w.r0 + i < w.r1) {
+      int tk, hd;
+      w.row(a, i, tk, hd);
+      raw[x] = __ldg(reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(w.q.q0) + tk) * a.q_stride +
+                                                    (static_cast<int64_t>(hk) * a.G + hd) * D) + part);
+    }
+  }
+
   auto bar = [&](int i) { return base_u + L_::kBar + 8 * i; };
   if (threadIdx.x == 0) {
     const int count[kBars] = {DUAL ? 256 : 256 * n_mt, 1, 1, 1, 1, 1, 1, 1, 1, 128, 128, 128, 128,
@@ -199,8 +215,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row0 = w.r0 + (DUAL ? 0 : i * kM);  // of the M tile
     const int r = row0 + row;
     const bool live = r < w.r1;
-    const int tok = live ? r / a.G : 0;
-    const int head = hk * a.G + (live ? r - tok * a.G : 0);
+    int tok = 0, head = 0;
+    if (live) w.row(a, r - w.r0, tok, head);
+    head += hk * a.G;
     const RowSees sees = row_sees(a, w.q.L, w.base_p + tok, live);
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 * (warp % 4)
     const uint32_t ts = tmem + i * 128 + lanes + half * 64, to = tmem + 256 + i * 128 + lanes + half * (D / 2);
@@ -217,19 +234,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (n > 0 && (!DUAL || i == 0)) {
       // The rows' queries, each brought to [2^7, 2^8) by a power of two, as two
       // e4m3 terms: a warp takes 16 of the M tile's rows, D / 8 lanes a row.
-      constexpr int kLanes = D / 8, kPer = 32 / kLanes, kIts = 16 / kPer;  // lanes a row, rows a pass, passes
-      uint4 raw[kIts];
-      const int sub = lane / kLanes, part = lane % kLanes, wrow = (warp & 7) * 16;
-#pragma unroll
-      for (int x = 0; x < kIts; ++x) {
-        const int gr = row0 + wrow + x * kPer + sub;
-        const int tk = gr / a.G;
-        raw[x] = make_uint4(0, 0, 0, 0);
-        if (gr < w.r1)
-          raw[x] = __ldg(reinterpret_cast<const uint4*>(
-                             a.q + (static_cast<int64_t>(w.q.q0) + tk) * a.q_stride +
-                             (static_cast<int64_t>(hk) * a.G + gr - tk * a.G) * D) + part);
-      }
       char* dst = smem + L_::kQ + (DUAL ? 0 : i) * 2 * L_::kMat8;
 #pragma unroll
       for (int x = 0; x < kIts; ++x) {
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       all_sync();
     }
     // the range that all rows of the CTA see whole
-    const int p_lo = w.base_p + w.r0 / a.G, p_hi = w.base_p + (w.r1 - 1) / a.G;
+    const int p_lo = w.p_lo, p_hi = w.p_hi;
     for (int t = 0; t < mine; ++t) {
       const int j = DUAL ? 2 * t + i : t;
       // (S of this tile says that O += P V of the tile before is done, too)
@@ -450,8 +454,9 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int hk = static_cast<int>(s % c.hkv), b = static_cast<int>(s / c.hkv);
   Work w;
   if (b >= c.n_seqs || !work_of<kRows>(c, a, pl, b, hk, rt, w) || (!DUAL && w.n_split == 1) || w.r0 + row >= w.r1) return;
-  const int tok = (w.r0 + row) / a.G;
-  const size_t orow = (static_cast<size_t>(w.q.q0) + tok) * a.hq + hk * a.G + (w.r0 + row) - tok * a.G;
+  int tok, head;
+  w.row(a, row, tok, head);
+  const size_t orow = (static_cast<size_t>(w.q.q0) + tok) * a.hq + hk * a.G + head;
   join_row<D>(a, ws, static_cast<size_t>(tile_id) * pl.splits * kRows + row, DUAL ? kM : kRows,
               DUAL ? 2 * w.n_split : w.n_split, orow, threadIdx.x % (D / 4));
 }
@@ -470,7 +475,8 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const C
   // one CTA a SM: split the keys when the row tiles do not fill the SMs evenly
   // (many row tiles do, the longest first)
   const int64_t splits =
-      base >= 4 * n_sm ? 1 : best_splits(base, n_sm, tiles, static_cast<int64_t>(ws.cap_rows) / (base * kRows), c.n_seqs > 1);
+      base >= 4 * n_sm ? 1 : best_splits(base, n_sm, tiles, static_cast<int64_t>(ws.cap_rows) / (base * kRows), 6,
+                                     c.n_seqs > 1);
   pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
   pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
   const int64_t grid = base * pl.splits;
