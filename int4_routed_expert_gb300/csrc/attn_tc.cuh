@@ -206,7 +206,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // in f16 in the swizzled layout [D / 64][128 keys][128 bytes]), and a ring of
 // the blocks' scales by groups of 16 keys: {key scale, log2 value scale,
 // 1 / value scale, 0}.
-template <int D, int KS, int RS, int VS>
+template <int D, int KS, int RS, int VS, int CT = 128>
 struct TileIo {
   static constexpr int kMat8 = kKeys * D;
   static constexpr int kHalf = kKeys * 128;
@@ -291,13 +291,13 @@ struct TileIo {
     if (bad) atomicOr(c.err, kErrBadBatch);
   }
 
-  // 128 threads: value codes to f16.  Thread t takes 16-byte chunk t % (D / 16)
+  // CT threads: value codes to f16.  Thread t takes 16-byte chunk t % (D / 16)
   // of keys t / (D / 16) + 0, kPer, ...; a chunk becomes two of the operand's.
   // free(j) waits until the product that read the stage of tile j - VS is done.
   template <typename Free>
   __device__ __forceinline__ void convert(const KvView& c, const AttnArgs& a, const KeyTiles& kt, int t_begin, int n,
                                           int tid, Free free) const {
-    constexpr int kChunks = D / 16, kPer = 128 / kChunks;
+    constexpr int kChunks = D / 16, kPer = CT / kChunks;
     const int ch = tid % kChunks, row0 = tid / kChunks;
     // the two halves' lanes store their two chunks in opposite order: no bank conflicts
     const int c0 = 2 * (ch & 3) + (ch >> 2);
@@ -315,8 +315,8 @@ struct TileIo {
       char* dst = smem + (v - base) + vs * kMat;
 #pragma unroll
       for (int p = 0; p < kKeys / kPer; ++p) {
-        uint2 u0 = *reinterpret_cast<const uint2*>(src0 + p * 2048);
-        uint2 u1 = *reinterpret_cast<const uint2*>(src1 + p * 2048);
+        uint2 u0 = *reinterpret_cast<const uint2*>(src0 + p * (CT * 16));
+        uint2 u1 = *reinterpret_cast<const uint2*>(src1 + p * (CT * 16));
         if (!whole) {
           // what no row sees is zero: a NaN there would reach the rows through 0 * NaN
           const int tok = base_key + p * kPer + row0;

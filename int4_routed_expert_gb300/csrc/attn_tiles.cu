@@ -30,12 +30,13 @@ namespace {
 constexpr int kM = 128;        // rows of an M tile
 constexpr int kRows = 2 * kM;  // rows of a CTA
 constexpr int kSoftmax = 512;              // threads: 2 M tiles x 2 halves of the keys x 128 rows
-constexpr int kThreads = kSoftmax + 192;   // 4 conversion warps, MMA warp, load warp
-constexpr int kMmaWarp = kSoftmax / 32 + 4;
+constexpr int kConvert = 64;               // two conversion warps
+constexpr int kThreads = kSoftmax + kConvert + 64;  // MMA warp, load warp
+constexpr int kMmaWarp = (kSoftmax + kConvert) / 32;
 constexpr int kKStages = 3;
 
 template <int D>
-using Io = TileIo<D, kKStages, 2, 2>;
+using Io = TileIo<D, kKStages, 2, 2, kConvert>;
 
 template <int D>
 struct Lay {
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   auto bar = [&](int i) { return base_u + L_::kBar + 8 * i; };
   if (threadIdx.x == 0) {
-    const int count[kBars] = {DUAL ? 256 : 256 * n_mt, 1, 1, 1, 1, 1, 1, 1, 1, 128, 128, 128, 128,
+    const int count[kBars] = {DUAL ? 256 : 256 * n_mt, 1, 1, 1, 1, 1, 1, 1, 1, kConvert, kConvert, kConvert, kConvert,
                               1, 1, 1, 1, 256, 256, 1, 1, 8, 8, 8, 8, 8, 8, 8, 8, 1};
 #pragma unroll
     for (int i = 0; i < kBars; ++i) mbar_init(bar(i), count[i]);
