@@ -50,15 +50,6 @@ __device__ __forceinline__ bool load_seq(const KvView& c, int b, Seq& s) {
   return ok;
 }
 
-// Page of the sequence's tokens i * page ..; -1 (and bit 1) when the table
-// holds no page of the pool there.
-__device__ __forceinline__ int load_page(const KvView& c, int b, int i) {
-  const int p = __ldg(c.table + static_cast<size_t>(b) * c.table_stride + i);
-  if (static_cast<unsigned>(p) < static_cast<unsigned>(c.n_pages)) return p;
-  atomicOr(c.err, kErrBadBatch);
-  return -1;
-}
-
 // The same in two steps, so that a prefetched entry is looked at only when it
 // is used: the entry as it is, then its check.
 __device__ __forceinline__ int raw_page(const KvView& c, int b, int i) {

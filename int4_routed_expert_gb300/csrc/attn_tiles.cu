@@ -494,7 +494,9 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const C
 
 cudaError_t attn_tiles_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const KvMaps& maps,
                               int n_sm, cudaStream_t s) {
-  const bool dual = static_cast<int64_t>(c.max_q) * a.G <= kM;
+  // (the two M tiles' sums have to fit the workspace)
+  const bool dual = static_cast<int64_t>(c.max_q) * a.G <= kM &&
+                    static_cast<size_t>(c.n_seqs) * c.hkv * kRows <= ws.cap_rows;
   if (c.D == 128) return (dual ? launch<128, true> : launch<128, false>)(c, a, ws, maps.k_tile, n_sm, s);
   return (dual ? launch<64, true> : launch<64, false>)(c, a, ws, maps.k_tile, n_sm, s);
 }

@@ -482,6 +482,16 @@ def test_attend_is_repeatable(m, new, hq, hkv):
         assert torch.equal(c.attend(q, bt.b), want)
 
 
+@pytest.mark.parametrize("new,hq,hkv", [(1, 16, 16), (5, 64, 8), (20, 64, 8)])
+def test_attend_many_sequences(m, new, hq, hkv):
+    """More row tiles than the workspace holds partial results for: every row tile ends in its own CTA."""
+    g = gen(22)
+    n = 1100 if new == 1 else 160
+    bt = R.Batch([1 + 7 * i % 61 for i in range(n)], [new] * n, 16, DEV)
+    c = make_cache(m, g, bt, hq, hkv, 64, fill="normal")
+    check(c, bt, randn(g, bt.cu[-1], hq, 64, dtype=torch.bfloat16))
+
+
 def test_decoder_step_example():
     """Token by token and as a prompt: the cache's blocks differ only in the scales they had on the way (codes
     rounded once more below 2^-6 of a scale), so the layers agree far inside e4m3's half step of 2^-4."""
