@@ -32,7 +32,6 @@
 namespace moe {
 namespace {
 
-
 constexpr float kFewLift = 5.f, kFewRescale = 3.f;  // weights below 2^8: an e4m3 ends at 448
 
 enum Bar {
@@ -46,9 +45,12 @@ enum Bar {
   kODone = 16,   // O^T += V^T P
   kCFull = 17,   // [8] scales
   kDrain = 25,
-  kJoin = 26,    // partial results
-  kBars = 27
+  kJoin = 26,    // [2] partial results
+  kBars = 28
 };
+
+// Most splits of a call: the join holds a reference and a sum of each and row.
+constexpr int max_splits(int n) { return 4096 / n; }
 
 // A CTA keeps to half an SM, so that two CTAs cover each other's bubbles.
 template <int D, int N>
@@ -217,7 +219,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
   if (threadIdx.x == 0) {
     constexpr int kS = 128 * L_::kGroups, kG = L_::kGroups;
     const int count[kBars] = {kS, 1, 1, 1, kG, kG, kG, 1, 1, 1, 1, 1, 1, 1,
-                              1,  kS, 1, 8, 8, 8, 8, 8, 8, 8, 8, 1, 1};
+                              1,  kS, 1, 8, 8, 8, 8, 8, 8, 8, 8, 1, 1, 1};
 #pragma unroll
     for (int i = 0; i < kBars; ++i) mbar_init(bar(i), count[i]);
     fence_barrier_init();
@@ -535,68 +537,88 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
   __syncthreads();
   if (!s_last) return;
   __threadfence();
-  // Partial results come from SMs far away: as many splits as fit are copied
-  // over the key and value stages at once, a lane a split, so that their
-  // latencies overlap.
+  // Partial results come from SMs far away: as many splits as fit are on their
+  // way over the key, value and weight stages, in two groups that take turns, a
+  // lane a split, while the splits' factors are worked out.
   constexpr int kEach = (N * (D / 4) + L_::kThreads - 1) / L_::kThreads;
-  constexpr int kRoom = 2 * L_::kStages * Io::kMat8;
+  constexpr int kRoom = L_::kConst - L_::kK;
+  static_assert(kRoom - max_splits(N) * N * 8 >= 2 * N * D * 4, "a split in either group");
   const int live = w.r1 - w.r0;
-  const uint32_t o_bytes = live * D * 4, ml_bytes = N * 8;
-  const int chunk = kRoom / (o_bytes + ml_bytes);
+  const int ml_bytes = w.n_split * N * 8, bytes = live * D * 4;
+  const int group = (kRoom - ml_bytes) / (2 * bytes);
   const size_t first = tile_id * pl.splits * N;
-  float mm[kEach], ll[kEach];
-  float4 v[kEach];
-#pragma unroll
-  for (int k = 0; k < kEach; ++k) mm[k] = -INFINITY, ll[k] = 0.f, v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4* so = reinterpret_cast<const float4*>(smem + L_::kK);
-  bool landed = true;
-  for (int s0 = 0, ph = 0; s0 < w.n_split && landed; s0 += chunk, ph ^= 1) {
-    const int m = min(chunk, w.n_split - s0);
-    const float2* sml = reinterpret_cast<const float2*>(smem + L_::kK + m * o_bytes);
-    if (warp == 0) {
-      // (the results were written by other threads' plain stores, and so were
-      // this buffer's last reads)
-      asm volatile("fence.proxy.async;" ::: "memory");
-      if (lane == 0) mbar_arrive_expect_tx(bar(kJoin), m * (o_bytes + ml_bytes));
-      __syncwarp();
-      for (int s = lane; s < m; s += 32) {
-        const size_t from = first + static_cast<size_t>(s0 + s) * N;
-        bulk_g2s(smem_u32(so) + s * o_bytes, ws.o + from * D, o_bytes, bar(kJoin));
-        bulk_g2s(smem_u32(sml) + s * ml_bytes, ws.ml + from, ml_bytes, bar(kJoin));
-      }
-    }
-    landed = mbar_wait(bar(kJoin), ph, c.err);
-#pragma unroll
-    for (int k = 0; k < kEach; ++k) {
-      const int e = threadIdx.x + k * L_::kThreads;
-      if (e < live * (D / 4)) {
-        const int row = e / (D / 4);
-        float top = mm[k];
-#pragma unroll 4
-        for (int s = 0; s < m; ++s) top = fmaxf(top, sml[s * N + row].x);
-        const float ref = top == -INFINITY ? 0.f : top, back = ex2(mm[k] - ref);
-        mm[k] = top;
-        ll[k] *= back;
-        v[k].x *= back, v[k].y *= back, v[k].z *= back, v[k].w *= back;
-        const float4* y = so + e;
-#pragma unroll 4
-        for (int s = 0; s < m; ++s, y += live * (D / 4)) {
-          const float2 x = sml[s * N + row];
-          const float4 z = *y;
-          const float f = ex2(x.x - ref);
-          ll[k] = fmaf(x.y, f, ll[k]);
-          v[k].x = fmaf(z.x, f, v[k].x), v[k].y = fmaf(z.y, f, v[k].y);
-          v[k].z = fmaf(z.z, f, v[k].z), v[k].w = fmaf(z.w, f, v[k].w);
-        }
-      }
-    }
-    __syncthreads();
+  const uint32_t parts = L_::kK + ml_bytes;  // [2][group][live][D], behind [n_split][N] factors
+  auto fetch = [&](int s0, int buf) {
+    const int m = min(group, w.n_split - s0);
+    if (lane == 0) mbar_arrive_expect_tx(bar(kJoin + buf), m * bytes);
+    __syncwarp();
+    for (int s = lane; s < m; s += 32)
+      bulk_g2s(base_u + parts + (buf * group + s) * bytes, ws.o + (first + static_cast<size_t>(s0 + s) * N) * D, bytes,
+               bar(kJoin + buf));
+  };
+  if (warp == 0) {
+    asm volatile("fence.proxy.async;" ::: "memory");  // (the results were written by other threads' plain stores)
+    fetch(0, 0);
+    if (group < w.n_split) fetch(group, 1);
   }
+  float2* ml = reinterpret_cast<float2*>(smem + L_::kK);
+#pragma unroll 4
+  for (int e = threadIdx.x; e < w.n_split * N; e += L_::kThreads) ml[e] = __ldcg(ws.ml + first + e);
+  __syncthreads();
+  if (const int row = threadIdx.x >> 3, sub = threadIdx.x & 7; row < N) {  // eight lanes a row
+    float top = -INFINITY, l = 0.f;
+#pragma unroll 4
+    for (int s = sub; s < w.n_split; s += 8) top = fmaxf(top, ml[s * N + row].x);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
+    for (int s = sub; s < w.n_split; s += 8) {
+      const float2 x = ml[s * N + row];
+      const float f = ex2(x.x - ref);
+      l = fmaf(x.y, f, l);
+      ml[s * N + row].x = f;
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (sub == 0) rows.m[row] = top, rows.f[row] = l;
+  }
+  __syncthreads();
+  int el[kEach], of[kEach];
+  float4 v[kEach];
 #pragma unroll
   for (int k = 0; k < kEach; ++k) {
     const int e = threadIdx.x + k * L_::kThreads;
-    if (e < live * (D / 4)) finish_row<D>(a, rows.out[e / (D / 4)], e % (D / 4), v[k], mm[k], ll[k]);
+    el[k] = e < live * (D / 4) ? e : 0;
+    of[k] = el[k] / (D / 4);
+    v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  for (int s0 = 0, buf = 0, ph = 0, end = w.n_split; s0 < end; s0 += group) {
+    const bool landed = mbar_wait(bar(kJoin + buf), ph, c.err);
+    const int m = min(group, w.n_split - s0);
+    const char* at = smem + parts + buf * group * bytes;
+#pragma unroll 2
+    for (int s = 0; s < m; ++s) {
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        const float f = ml[(s0 + s) * N + of[k]].x;
+        const float4 z = reinterpret_cast<const float4*>(at + s * bytes)[el[k]];
+        v[k].x = fmaf(z.x, f, v[k].x), v[k].y = fmaf(z.y, f, v[k].y);
+        v[k].z = fmaf(z.z, f, v[k].z), v[k].w = fmaf(z.w, f, v[k].w);
+      }
+    }
+    // (after a timeout only what is under way is waited for)
+    if (!__syncthreads_and(landed)) end = min(end, s0 + 2 * group);
+    if (warp == 0 && s0 + 2 * group < end) {
+      fence_proxy_async_smem();  // the buffer's last reads
+      fetch(s0 + 2 * group, buf);
+    }
+    buf ^= 1, ph ^= buf == 0;
+  }
+#pragma unroll
+  for (int k = 0; k < kEach; ++k)
+    if (threadIdx.x + k * L_::kThreads < live * (D / 4))
+      finish_row<D>(a, rows.out[of[k]], el[k] % (D / 4), v[k], rows.m[of[k]], rows.f[of[k]]);
 }
 
 template <int D, int N>
@@ -609,9 +631,10 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const K
   pl.row_tiles = static_cast<int>((rows + N - 1) / N);
   const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
   const int64_t tiles = max_key_tiles(c, a, N, kKeys);
-  const int64_t resident = static_cast<int64_t>(n_sm) * Lay<D, N>::kCtas;
-  const int64_t splits = best_splits(base, resident, tiles, static_cast<int64_t>(ws.cap_rows) / (base * N), 3,
-                                     c.n_seqs > 1);
+  // (32 rows of 8000 keys and 8 kv heads of 128, splits of 8, 4 and 2 tiles:
+  // 27.3, 23.3 and 27.2 us)
+  const int64_t most = std::min<int64_t>(static_cast<int64_t>(ws.cap_rows) / (base * N), max_splits(N));
+  const int64_t splits = best_splits(base, n_sm, tiles, most, c.n_seqs > 1, {Lay<D, N>::kCtas, 3., 0.25});
   pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
   pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
   const int64_t grid = base * pl.splits;

@@ -335,22 +335,30 @@ struct Plan {
   int row_tiles, splits, tiles_per_split;
 };
 
-// Splits of `tiles` tiles for `base` row tiles on `resident` CTA slots, at most
-// `most`: the least time in sixteenths of a tile, a CTA costing `start` tiles
-// beside its own (set-up, first loads, results) and the join half a sixteenth a
-// split.  Where there are several sequences, `tiles` comes from a bound that
-// most of them stay below: the time is the sum over a batch at the bound and
-// one at half of it, where empty CTAs leave their slots to others and half a
-// round is lost at the end.
-inline int64_t best_splits(int64_t base, int64_t resident, int64_t tiles, int64_t most, int64_t start, bool ragged) {
+// What a kernel's CTAs cost, in the time that a CTA with an SM of its own takes
+// for a tile of keys.
+struct Costs {
+  int per_sm;    // CTAs of an SM: the tiles of two take half as long again
+  double start;  // set-up, first loads, results
+  double join;   // a split's part of the join
+};
+
+// Splits of `tiles` tiles for `base` row tiles, at most `most`: the least time.
+// Where there are several sequences, `tiles` comes from a bound that most of
+// them stay below: the time is the sum over a batch at the bound and one at half
+// of it, where empty CTAs leave their slots to others and half a round is lost
+// at the end.
+inline int64_t best_splits(int64_t base, int64_t n_sm, int64_t tiles, int64_t most, bool ragged, const Costs& k) {
   const int64_t end = std::max<int64_t>(std::min<int64_t>({tiles, most, 256}), 1);
+  const int64_t resident = n_sm * k.per_sm;
   double least = 1e300;
   int64_t best = 1;
   for (int64_t s = 1; s <= end; ++s) {
-    const double cta = static_cast<double>((tiles + s - 1) / s + start);
+    const double tile = base * s > n_sm && k.per_sm > 1 ? 1.5 : 1.;
+    const double cta = tile * static_cast<double>((tiles + s - 1) / s) + k.start;
     const double full = static_cast<double>((base * s + resident - 1) / resident) * cta;
     const double half = std::max(0.5 * static_cast<double>(base * s) / static_cast<double>(resident) + 0.5, 1.0) * cta;
-    const double cost = (ragged ? full + half : 2 * full) * 16 + static_cast<double>(s);
+    const double cost = (ragged ? 0.5 * (full + half) : full) + k.join * static_cast<double>(s);
     if (cost < least) least = cost, best = s;
   }
   return best;

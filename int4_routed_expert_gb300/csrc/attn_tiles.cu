@@ -475,9 +475,9 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const C
   const int64_t tiles = max_key_tiles(c, a, kRows, kKeys);
   // one CTA a SM: split the keys when the row tiles do not fill the SMs evenly
   // (many row tiles do, the longest first)
+  const int64_t most = static_cast<int64_t>(ws.cap_rows) / (base * kRows);
   const int64_t splits =
-      base >= 4 * n_sm ? 1 : best_splits(base, n_sm, tiles, static_cast<int64_t>(ws.cap_rows) / (base * kRows), 6,
-                                     c.n_seqs > 1);
+      base >= 4 * n_sm ? 1 : best_splits(base, n_sm, tiles, most, c.n_seqs > 1, {1, 6., 1. / 32});
   pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
   pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
   const int64_t grid = base * pl.splits;
