@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import math
+from threading import get_ident
 
 from . import moe
 from .moe import MOE_BF16, MOE_F32, MOE_OK, MoeError
@@ -170,9 +171,10 @@ class Rope:
         (q's, k's) when k is given.  Tokens may be strided (parts of one projection); q_out is q rotates in
         place."""
         if q_out is None and k_out is None:
-            # the checks of a layout (shapes, strides, types) once: a call is a few microseconds
-            key = (q.shape, q.stride(), q.dtype) if k is None else \
-                (q.shape, q.stride(), q.dtype, k.shape, k.stride(), k.dtype)
+            # the checks of a layout (shapes, strides, types) once: a call is a few microseconds; the argument
+            # structs are a thread's own
+            key = (get_ident(), q.shape, q.stride(), q.dtype) if k is None else \
+                (get_ident(), q.shape, q.stride(), q.dtype, k.shape, k.stride(), k.dtype)
             known = self._layouts.get(key)
             if known is None:
                 known = self._layout(key, q, k)

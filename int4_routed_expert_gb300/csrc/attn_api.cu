@@ -85,8 +85,8 @@ const char* check_kv_config(const moe_kv_config_t* c) {
   return nullptr;
 }
 
-// Rows of partial results: 2^18 hold six CTAs of 256 rows a SM; the splits of
-// a call are limited to what fits.
+// Rows of partial results (64 or 128 MB of sums): six CTAs of 256 rows a SM; the
+// splits of a call are limited to what fits.
 constexpr size_t kPartRows = 1u << 18;
 
 struct KvLayout {
@@ -499,10 +499,11 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
   a.hq = h->cfg.n_q_heads;
   a.G = h->cfg.n_q_heads / h->cfg.n_kv_heads;
   a.inv_g = 1.f / static_cast<float>(a.G);
-  // Rows of a kv head, up to 32: keys as the products' M dimension, each code
-  // multiplied as stored; more: rows as M.  At 64 rows of 16 x 16384 keys the
-  // first kernel took 209 us and the second 180 us, at 32 rows 89 us and 180 us
-  // (4 kv heads and 8).
+  // Rows of a kv head, up to 32: keys as the products' M dimension; more: rows as
+  // M.  At 32 rows the first kernel takes 90 us and the second 101 us (16 x 16384
+  // keys, 4 kv heads), at 16 rows 103 and 175 us (8 kv heads), at 8 rows 208 and
+  // 350 us (64 sequences).  33 rows would be two passes of the first over keys
+  // that the second reads once.
   const bool tiles = static_cast<int64_t>(c.max_q) * a.G > 32;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return launched(h, tiles ? moe::attn_tiles_launch(c, a, h->ws, h->maps, h->n_sm, s)

@@ -1,15 +1,18 @@
-// Attention over the 8-bit cache for many rows (prompts, chunks) on tcgen05.
+// Attention over the 8-bit cache for many rows (prompts, chunks, verification of
+// several tokens) on tcgen05.
 //
-// The mathematics is that of attn_rows.cu: weights 2^(s + log2 v - m + lift)
-// with the block's value scale in the exponent, o = sum w c / sum w / v, an
-// online softmax whose reference m moves only when it would grow by 2^5.
+// Mathematics.  Row r (a query head of a new token) sees keys j with logits
+// s_j = scale * q . k_j.  With the block's value scale v_j in the exponent,
+// w_j = 2^(s_j log2 e + log2 v_j - m + lift), the output is
+//   o = sum_j w_j c_j / sum_j (w_j / v_j),   c_j the value's e4m3 code,
+// an online softmax whose reference m moves only when it would grow by 2^5.
 //
 // One CTA takes 256 rows (a row is a query head of a token; the heads that
 // share a kv head are packed into the rows, so K and V are read once for all
 // of them) as two M = 128 tiles, and walks over 128-key tiles:
 //   1 warp    TMA: key codes into the swizzled operand layout (three stages),
 //             value codes as they lie (two stages), the blocks' scales
-//   4 warps   value codes -> f16 (exact) in the swizzled operand layout
+//   2 warps   value codes -> f16 (exact) in the swizzled operand layout
 //   1 thread  tcgen05.mma: S = Q K^T in e4m3, then O += P V in f16 (P from
 //             tensor memory, V as it lies, MN-major)
 //   2 x 8     softmax warps, two groups a M tile, two threads a row, 64 keys
@@ -21,7 +24,16 @@
 // operands: a weight of 11 bits would be three e4m3 terms.
 // The two M tiles take turns, so one's softmax runs under the other's products.
 // Tensor memory: S0, S1 (P in their first half), O0, O1: 512 columns.
-// Bound by the tensor pipe: 2 * 2 * 128 * 128 * D flops a tile and M tile.
+// The tensor pipe has 1024 clocks of products a tile and M tile of heads of 128
+// (64 a step of M = N = 128; S two terms of four e4m3 steps, O eight f16 ones),
+// the softmax warps about as many issue slots (a multiply-add, an exponential, a
+// share of the sum, the maximum, the conversion and the tensor memory's traffic
+// a logit).  What bounds it is the chain S -> weights -> O of either M tile, of
+// which only two are under way: 718 us for a prompt of 8192 tokens with 48 query
+// and 8 kv heads of 128, 1149 TFLOP/s, about half of the pipe's rate.  Heads of
+// 64 have half the products to the same softmax: 704 TFLOP/s (16384 tokens).
+// 20 warps leave 96 registers a thread; two conversion warps instead of four
+// (80 registers) brought 729 us down to 718 us.
 #include "attn_tc.cuh"
 
 namespace moe {
@@ -71,7 +83,8 @@ enum Bar {
 // DUAL: calls whose sequences have at most 128 rows a kv head.  The two M tiles
 // are the same rows then, each with every other tile of keys and with sums of
 // its own, which the join takes for two splits: one's softmax still runs under
-// the other's products.
+// the other's products.  48 rows a kv head (four sequences of up to 131072
+// keys, 4 kv heads): 143 us, and 198 us as one M tile.
 template <int D, bool DUAL>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tiles_kernel(const KvView c, const AttnArgs a, const AttnWs ws, const Plan pl,
@@ -474,10 +487,8 @@ cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const C
   const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
   const int64_t tiles = max_key_tiles(c, a, kRows, kKeys);
   // one CTA a SM: split the keys when the row tiles do not fill the SMs evenly
-  // (many row tiles do, the longest first)
   const int64_t most = static_cast<int64_t>(ws.cap_rows) / (base * kRows);
-  const int64_t splits =
-      base >= 4 * n_sm ? 1 : best_splits(base, n_sm, tiles, most, c.n_seqs > 1, {1, 6., 1. / 32});
+  const int64_t splits = best_splits(base, n_sm, tiles, most, c.n_seqs > 1, {1, 6., 1. / 32});
   pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
   pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
   const int64_t grid = base * pl.splits;

@@ -10,7 +10,9 @@
 // lost against a free scale, since e4m3 is a floating format.
 //
 // Read.  A thread turns chunks of 16 codes into 16 values.  Both are bound by
-// memory, so a thread has several independent loads under way.
+// memory, so a thread has several independent loads under way.  (Blocks of 64 x 128
+// bf16: 3 x up to 8191 tokens written in 26.6 us, 4.5 TB/s; 5 x up to 16384 read
+// in 55 us, 4.7 TB/s.)
 #include <climits>
 
 #include "attn_internal.cuh"

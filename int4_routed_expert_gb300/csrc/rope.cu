@@ -3,10 +3,10 @@
 // The angles' sines and cosines of a CTA's tokens go to shared memory once for
 // all heads; then a thread holds its 8 pairs' ones in registers and streams
 // its place of the token's heads (8 pairs, or 16 copied elements).  The angle
-// of pair i at position p is p *
-// inc[i] mod 2^64, a 64-bit fraction of a turn: an integer product wraps
-// exactly, so far positions lose nothing.  Bound by memory: x is read once and
-// y written once.
+// of pair i at position p is p * inc[i] mod 2^64, a 64-bit fraction of a turn:
+// an integer product wraps exactly, so far positions lose nothing.  Bound by
+// memory: x is read once and y written once (8192 tokens of 56 heads of 128,
+// bf16: 42.9 us, 5.5 TB/s).
 #include "attn_internal.cuh"
 
 namespace moe {
@@ -163,6 +163,7 @@ cudaError_t rope_launch(const uint64_t* inc, int rot_dim, float amplitude, bool 
   P.head_dim = head_dim;
   P.T = T;
   // one token a CTA while that fills the device once; four share the angles' phase then
+  // (8192 tokens: 42.9 us, and 45.1 us with one)
   P.tokens = T >= 2048 ? kTokens : 1;
   const int per_head = head_dim / 16, threads = kThreads / per_head * per_head;
   const int grid = (T + P.tokens - 1) / P.tokens;
