@@ -182,18 +182,6 @@ __device__ __forceinline__ bool mbar_wait2(uint32_t b0, uint32_t p0, uint32_t b1
   return ok != 0 || (mbar_wait(b0, p0, err) && mbar_wait(b1, p1, err));
 }
 
-// Whether any of a softmax group's 128 threads says yes (a barrier among them).
-__device__ __forceinline__ bool vote(int group, bool yes) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(static_cast<uint32_t>(yes)), "r"(1 + group)
-      : "memory");
-  return r != 0;
-}
-
 template <int D, int N>
 __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
     attn_few_kernel(const KvView c, const AttnArgs a, const AttnWs ws, const Plan pl,
@@ -385,8 +373,8 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
       }
 #pragma unroll
       for (int r = 0; r < NG; r += 2) top = max3(top, z[r], z[r + 1]);
-      if (vote(grp, pending || top > kFewLift + kFewRescale || !ok)) {
-        ok = !vote(grp, !ok);
+      if (named_vote(1 + grp, 128, pending || top > kFewLift + kFewRescale || !ok)) {
+        ok = !named_vote(1 + grp, 128, !ok);
         if (!ok) break;
         // some reference moves: the rows' maxima over the tile, warp by warp
 #pragma unroll
@@ -429,7 +417,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
           tmem_wait_st();
         }
         // (a barrier, too: red and f are free again)
-        pending = vote(grp, t < NG && rows.m[g0 + t % NG] == -INFINITY && rows.hi[g0 + t % NG] >= 0);
+        pending = named_vote(1 + grp, 128, t < NG && rows.m[g0 + t % NG] == -INFINITY && rows.hi[g0 + t % NG] >= 0);
       }
       // the weights, and their terms: row pairs of term i in u[i]
       uint32_t u[4][4];

@@ -17,6 +17,18 @@ constexpr int kKeys = 128;       // keys of a tile
 constexpr int kConstRing = 8;    // tiles whose blocks' scales are kept
 constexpr float kTiny = 1e-37f;  // keeps what is hidden at -inf where a block's scale is 0
 
+// Whether any of a barrier's `count` threads says yes.
+__device__ __forceinline__ bool named_vote(int id, int count, bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(yes)), "r"(id), "r"(count)
+      : "memory");
+  return r != 0;
+}
+
 // The one thread that issues products is on every step's path: the MMAs of a
 // product stand in one block, their descriptors a constant apart.
 //

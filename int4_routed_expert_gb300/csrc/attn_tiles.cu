@@ -235,16 +235,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const RowSees sees = row_sees(a, w.q.L, w.base_p + tok, live);
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 * (warp % 4)
     const uint32_t ts = tmem + i * 128 + lanes + half * 64, to = tmem + 256 + i * 128 + lanes + half * (D / 2);
-    // what the row's two threads tell each other, two buffers in turn
+    // What the row's two threads tell each other, two buffers in turn.  A warp
+    // whose wait gave up waits no more but still comes to every barrier, and the
+    // loop ends for all.
+    bool ok = true;
     float* pair = reinterpret_cast<float*>(smem + L_::kPair) + i * 512;
     const int mine = DUAL ? (n + 1 - i) >> 1 : n;  // tiles of this M tile
     auto other = [&](int buf, float mine) {
       pair[buf * 256 + half * 128 + row] = mine;
-      named_sync(1 + i, 256);
+      ok = !named_vote(1 + i, 256, !ok);
       return pair[buf * 256 + (half ^ 1) * 128 + row];
     };
     float m = -INFINITY, l = 0.f, lscale = 0.f;  // lscale >= 0: a negative scale turns the query's sign
-    bool ok = true;
     if (n > 0 && (!DUAL || i == 0)) {
       // The rows' queries, each brought to [2^7, 2^8) by a power of two, as two
       // e4m3 terms: a warp takes 16 of the M tile's rows, D / 8 lanes a row.
@@ -292,7 +294,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (S of this tile says that O += P V of the tile before is done, too)
       ok = __all_sync(0xffffffffu, mbar_wait(bar(kCFull + j % kConstRing), (j / kConstRing) & 1, c.err) &&
                                        mbar_wait(bar(kSFull + i), t & 1, c.err));
-      if (!ok) break;
       fence_after_sync();
       const float4* cn = io.scales(j) + 4 * half;
       const int base = w.k.base(t_begin + j) + 64 * half;
@@ -323,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       mt = fmaxf(mt, other(t & 1, mt));
+      if (!ok) break;
       if (__any_sync(0xffffffffu, mt > m + kRescale)) {
         const float nm = fmaxf(m, mt);
         const float f = nm == m ? 1.f : ex2(m - nm);
