@@ -48,6 +48,13 @@ struct RowSees {
   __device__ __forceinline__ bool operator()(int tok) const {
     return tok <= hi && (tok >= lo || tok < sinks);
   }
+  // The same for keys tok .. tok + 31, a bit each.
+  __device__ __forceinline__ uint32_t bits(int tok) const {
+    return below(hi + 1 - tok) & (~below(lo - tok) | below(sinks - tok));
+  }
+  static __device__ __forceinline__ uint32_t below(int n) {  // the lowest n bits
+    return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u;
+  }
 };
 __device__ __forceinline__ RowSees row_sees(const AttnArgs& a, int L, int p, bool live) {
   RowSees r;

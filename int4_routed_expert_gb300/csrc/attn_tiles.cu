@@ -304,14 +304,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // it), then for the weights
       float s[32];
       float mt = -INFINITY;
+      auto hide = [&](int x) {
+        const uint32_t seen = sees.bits(base + 32 * x);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) s[k] = seen & (1u << k) ? s[k] : -INFINITY;
+      };
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         tmem_ld32(ts + 32 * x, s);
         tmem_wait_ld32(s);
-        if (!whole) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) s[k] = sees(base + 32 * x + k) ? s[k] : -INFINITY;
-        }
+        if (!whole) hide(x);
 #pragma unroll
         for (int gg = 0; gg < 2; ++gg) {
           const float4 z = cn[2 * x + gg];
@@ -368,10 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       weigh(1);
       tmem_wait_ld32(s);
-      if (!whole) {
-#pragma unroll
-        for (int k = 0; k < 32; ++k) s[k] = sees(base + k) ? s[k] : -INFINITY;
-      }
+      if (!whole) hide(0);
       weigh(0);
       tmem_wait_st();
       fence_before_sync();
