@@ -17,6 +17,11 @@ constexpr int kKeys = 128;       // keys of a tile
 constexpr int kConstRing = 8;    // tiles whose blocks' scales are kept
 constexpr float kTiny = 1e-37f;  // keeps what is hidden at -inf where a block's scale is 0
 
+// 16 bytes to shared memory, the last 16 - n of them zero.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+
 // Whether any of a barrier's `count` threads says yes.
 __device__ __forceinline__ bool named_vote(int id, int count, bool yes) {
   uint32_t r;

@@ -111,19 +111,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int n = t_end - t_begin;  // 0 when the rows see nothing
   const int n_mt = DUAL || w.r1 - w.r0 > kM ? 2 : 1;
 
-  // the softmax warps' queries are on their way while all else is set up
+  // The softmax warps' queries are on their way while all else is set up, each
+  // row to where its two terms will stand.  (This loop and the next two that run
+  // once a CTA stay rolled: code met for the first time costs more to fetch than
+  // to run.)
   constexpr int kLanes = D / 8, kPer = 32 / kLanes, kIts = 16 / kPer;  // lanes a row, rows a pass, passes
   const int sub = lane / kLanes, part = lane % kLanes, wrow = (warp & 7) * 16;
-  uint4 raw[kIts];
-#pragma unroll
-  for (int x = 0; x < kIts; ++x) {
-    const int i = (DUAL ? 0 : (warp >> 3) * kM) + wrow + x * kPer + sub;  // row of the CTA
-    raw[x] = make_uint4(0, 0, 0, 0);
-    if (n > 0 && warp < (DUAL ? 8 : 16) && w.r0 + i < w.r1) {
+  const uint32_t q_tile = L_::kQ + (DUAL ? 0 : warp >> 3) * 2 * L_::kMat8;
+  const uint32_t q_raw = q_tile + part / (D / 16) * L_::kMat8;
+  if (n > 0 && warp < (DUAL ? 8 : 16)) {
+#pragma unroll 2
+    for (int x = 0; x < kIts; ++x) {
+      const int r = wrow + x * kPer + sub, i = (DUAL ? 0 : (warp >> 3) * kM) + r;  // row of the M tile, of the CTA
+      const bool in = w.r0 + i < w.r1;
       int tk, hd;
-      w.row(a, i, tk, hd);
-      raw[x] = __ldg(reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(w.q.q0) + tk) * a.q_stride +
-                                                    (static_cast<int64_t>(hk) * a.G + hd) * D) + part);
+      w.row(a, in ? i : 0, tk, hd);
+      cp_async16(base_u + q_raw + k_off<D>(r, part % (D / 16)),
+                 a.q + (static_cast<int64_t>(w.q.q0) + tk) * a.q_stride + (static_cast<int64_t>(hk) * a.G + hd) * D +
+                     8 * part,
+                 in ? 16 : 0);
     }
   }
 
@@ -250,10 +256,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (n > 0 && (!DUAL || i == 0)) {
       // The rows' queries, each brought to [2^7, 2^8) by a power of two, as two
       // e4m3 terms: a warp takes 16 of the M tile's rows, D / 8 lanes a row.
-      char* dst = smem + L_::kQ + (DUAL ? 0 : i) * 2 * L_::kMat8;
-#pragma unroll
+      char* dst = smem + q_tile;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 2
       for (int x = 0; x < kIts; ++x) {
-        const uint32_t u[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+        const int qrow = wrow + x * kPer + sub;
+        const uint4 raw = *reinterpret_cast<const uint4*>(smem + q_raw + k_off<D>(qrow, part % (D / 16)));
+        const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
         float amax = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -271,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           t0[k] = inf ? 0x7f7f7f7fu : a1 | (b1 << 16);
           t1[k] = a2 | (b2 << 16);
         }
-        const int qrow = wrow + x * kPer + sub;
+        __syncwarp();  // the row's lanes have read it
         const uint32_t off = k_off<D>(qrow, part >> 1) + 8 * (part & 1);
         *reinterpret_cast<uint2*>(dst + off) = make_uint2(t0[0], t0[1]);
         *reinterpret_cast<uint2*>(dst + L_::kMat8 + off) = make_uint2(t1[0], t1[1]);
@@ -393,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t olo = static_cast<uint32_t>(orow);
       const bool parts = DUAL || w.n_split > 1;
       constexpr int kCols = D / 4;  // columns a round
-#pragma unroll
+#pragma unroll 1
       for (int y = 0; y < 2; ++y) {
         float o[kCols];
 #pragma unroll
