@@ -93,6 +93,9 @@ __device__ __forceinline__ float row_factor(float amax) {
   return __uint_as_float(static_cast<uint32_t>(min(127 + TOP + 127 - e, 254)) << 23);
 }
 
+// 1 / f of a power of two in [2^-126, 2^126]
+__device__ __forceinline__ float inverse(float f) { return __uint_as_float((254u << 23) - __float_as_uint(f)); }
+
 // Row `row` of the output (and of lse): sums over sum of weights, both
 // relative to reference mm - kLift.  A row that saw nothing is 0.
 template <int D>

@@ -337,14 +337,14 @@ struct TileIo {
   }
 };
 
-// Two consecutive query elements (a bf16 pair times f) as two e4m3 terms:
-// their sum is exact down to 2^-18 of the row's largest.
+// Two consecutive query elements (a bf16 pair times f, at most 2^8) as two e4m3
+// terms: their sum is exact down to 2^-18 of the row's largest.  (f16 holds the
+// product's 8 bits, from 2^-17 on rounded to 2^-25.)
 __device__ __forceinline__ void split_query(uint32_t pair, float f, uint32_t& q1, uint32_t& q2) {
-  const float2 v = make_float2(__uint_as_float(pair << 16) * f, __uint_as_float(pair & 0xffff0000u) * f);
-  q1 = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-  const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(q1), __NV_E4M3);
-  const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-  q2 = __nv_cvt_float2_to_fp8x2(make_float2(v.x - back.x, v.y - back.y), __NV_SATFINITE, __NV_E4M3);
+  const __half2 v = __floats2half2_rn(__uint_as_float(pair << 16) * f, __uint_as_float(pair & 0xffff0000u) * f);
+  q1 = __nv_cvt_halfraw2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+  const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(q1), __NV_E4M3);
+  q2 = __nv_cvt_halfraw2_to_fp8x2(__hsub2(v, __half2(back)), __NV_SATFINITE, __NV_E4M3);
 }
 
 // How a call's rows and keys are cut into CTAs.

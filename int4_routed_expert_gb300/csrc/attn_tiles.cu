@@ -263,12 +263,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int qrow = wrow + x * kPer + sub;
         const uint4 raw = *reinterpret_cast<const uint4*>(smem + q_raw + k_off<D>(qrow, part % (D / 16)));
         const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-        float amax = 0.f;
+        // the row's largest magnitude: as bf16 bits magnitudes order like integers (NaN above all)
+        uint32_t top = __vmaxu2(__vmaxu2(u[0] & 0x7fff7fffu, u[1] & 0x7fff7fffu),
+                                __vmaxu2(u[2] & 0x7fff7fffu, u[3] & 0x7fff7fffu));
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          amax = max3(amax, fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xffff0000u)));
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        for (int o = kLanes / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float amax = __uint_as_float(max(top << 16, top & 0xffff0000u));
         const float f = copysignf(row_factor<7>(amax), a.scale_log2);
         const bool inf = !(amax < INFINITY);  // (codes saturate: such a row is NaN instead)
         uint32_t t0[2], t1[2];
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t off = k_off<D>(qrow, part >> 1) + 8 * (part & 1);
         *reinterpret_cast<uint2*>(dst + off) = make_uint2(t0[0], t0[1]);
         *reinterpret_cast<uint2*>(dst + L_::kMat8 + off) = make_uint2(t1[0], t1[1]);
-        if (part == 0) pair[256 + qrow] = a.scale_log2 / f;
+        if (part == 0) pair[256 + qrow] = fabsf(a.scale_log2) * inverse(fabsf(f));
       }
       fence_proxy_async_smem();
       mbar_arrive(bar(kQFull));
