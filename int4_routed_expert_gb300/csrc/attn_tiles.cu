@@ -29,11 +29,13 @@
 // the softmax warps about as many issue slots (a multiply-add, an exponential, a
 // share of the sum, the maximum, the conversion and the tensor memory's traffic
 // a logit).  What bounds it is the chain S -> weights -> O of either M tile, of
-// which only two are under way: 718 us for a prompt of 8192 tokens with 48 query
-// and 8 kv heads of 128, 1149 TFLOP/s, about half of the pipe's rate.  Heads of
-// 64 have half the products to the same softmax: 704 TFLOP/s (16384 tokens).
+// which only two are under way: 694 us for a prompt of 8192 tokens with 48 query
+// and 8 kv heads of 128, 1187 TFLOP/s, about half of the pipe's rate.  Of a
+// tile's 3500 clocks 1024 are products, 1900 softmax and the rest the way from
+// one to the other; a CTA's beginning and end cost as much as five tiles.  Heads
+// of 64 have half the products to the same softmax: 728 TFLOP/s (16384 tokens).
 // 20 warps leave 96 registers a thread; two conversion warps instead of four
-// (80 registers) brought 729 us down to 718 us.
+// (80 registers) brought 729 us down to 718 us at the time.
 #include "attn_tc.cuh"
 
 namespace moe {
