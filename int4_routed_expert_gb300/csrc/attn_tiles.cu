@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int sub = lane / kLanes, part = lane % kLanes, wrow = (warp & 7) * 16;
   const uint32_t q_tile = L_::kQ + (DUAL ? 0 : warp >> 3) * 2 * L_::kMat8;
   const uint32_t q_raw = q_tile + part / (D / 16) * L_::kMat8;
-  if (n > 0 && warp < (DUAL ? 8 : 16)) {
+  if (n > 0 && warp < (DUAL ? 8 : 8 * n_mt)) {
 #pragma unroll 2
     for (int x = 0; x < kIts; ++x) {
       const int r = wrow + x * kPer + sub, i = (DUAL ? 0 : (warp >> 3) * kM) + r;  // row of the M tile, of the CTA
