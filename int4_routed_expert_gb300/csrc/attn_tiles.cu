@@ -23,7 +23,10 @@
 // what one f16 product would and no key is converted.  Values stay f16
 // operands: a weight of 11 bits would be three e4m3 terms.
 // The two M tiles take turns, so one's softmax runs under the other's products.
-// Tensor memory: S0, S1 (P in their first half), O0, O1: 512 columns.
+// Tensor memory: S0, S1, O0, O1: 512 columns.  P stands in the second half of
+// either 64 columns of S that a thread holds: the first half's second read is
+// under way when the first weights are stored, and nothing orders a store behind
+// a load of the same columns but a wait for it.
 // The tensor pipe has 1024 clocks of products a tile and M tile of heads of 128
 // (64 a step of M = N = 128; S two terms of four e4m3 steps, O eight f16 ones),
 // the softmax warps about as many issue slots (a multiply-add, an exponential, a
@@ -48,6 +51,7 @@ constexpr int kConvert = 64;               // two conversion warps
 constexpr int kThreads = kSoftmax + kConvert + 64;  // MMA warp, load warp
 constexpr int kMmaWarp = (kSoftmax + kConvert) / 32;
 constexpr int kKStages = 3;
+constexpr int kPAt = 32;  // P's first column of the 64 columns of S that a thread holds
 
 template <int D>
 using Io = TileIo<D, kKStages, 2, 2, kConvert>;
@@ -169,10 +173,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       auto k_wait = [&](int j) { return mbar_wait(bar(kKFull + j % kKStages), (j / kKStages) & 1, c.err); };
       auto issue_o = [&](int i, int j, bool first) {
-        const uint32_t ot = tmem + 256 + i * 128, pt = tmem + i * 128;
+        const uint32_t ot = tmem + 256 + i * 128, pt = tmem + i * 128 + kPAt;
         const uint64_t vd = v_desc + (j & 1) * (L_::kMat >> 4);
         mma_o(ot, pt, vd, id_o, first);
-        mma_o(ot, pt + 64, vd + (64 * 128 >> 4), id_o, 0);  // P's halves start where S's do
+        mma_o(ot, pt + 64, vd + (64 * 128 >> 4), id_o, 0);  // P's halves stand as far apart as S's
       };
       bool ok = mbar_wait(bar(kQFull), 0, c.err) && k_wait(0);
       if (ok) {
@@ -375,9 +379,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           l = fmaf(sum0 + sum1, z.z, l);
         }
-        // P takes the first half of this thread's S columns: those of keys 0 .. 31, read by then
+        // P takes the second half of this thread's S columns, those of keys 32 .. 63: they are in
+        // registers or used up, while the load of the first half is still under way
         if (x == 1) tmem_ld32(ts, s);
-        tmem_st16(ts + 16 * x, u);
+        tmem_st16(ts + kPAt + 16 * x, u);
       };
       weigh(1);
       tmem_wait_ld32(s);
