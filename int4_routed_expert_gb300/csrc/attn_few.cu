@@ -469,8 +469,9 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
     }
     l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
     if (lane < NG) red[(warp & 3) * N + g0 + lane] = l[0];
-    if (ok && n > 0)
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(kODone), (n - 1) & 1, c.err));
+    // (a lane whose wait gave up in the last tile has had no vote since: the warp decides here,
+    // as its lanes go on to loads and barriers together)
+    ok = __all_sync(0xffffffffu, ok && (n == 0 || mbar_wait(bar(kODone), (n - 1) & 1, c.err)));
     fence_after_sync();
     // thread t has dim t of every row: the terms' columns, the smallest first
     float o[NG];

@@ -58,3 +58,28 @@ def test_products_read_the_weights_where_they_are_stored():
     assert re.search(r"pt = tmem \+ i \* 128 \+ kPAt\b", text)
     # the second 64 keys' weights: as far on as their thread's columns
     assert re.search(r"ts = tmem \+ i \* 128 \+ lanes \+ half \* 64\b", text) and "mma_o(ot, pt + 64," in text
+
+
+@pytest.mark.parametrize("name", KERNELS)
+def test_a_lane_that_gave_up_does_not_part_from_its_warp(name):
+    """A bounded wait can give up in one lane and succeed in its neighbour.  Where the outcome decides whether a
+    warp goes on to something that all its lanes have to reach, the warp has agreed on it before: else the lanes
+    that go on wait for the others without limit."""
+    text = code(name)
+    softmax = text[text.index("float* red =" if name == "attn_few.cu" else "const RowSees sees ="):]
+    collective = r"tmem_ld|tmem_st|__\w+_sync\(|named_sync|break;"
+    found = 0
+    for c in re.finditer(r"\bif \(", softmax):
+        end, depth = c.end(), 1
+        while depth:
+            depth += {"(": 1, ")": -1}.get(softmax[end], 0)
+            end += 1
+        condition, rest = softmax[c.end():end - 1], softmax[end:].lstrip()
+        body = rest[:rest.index("}" if rest[0] == "{" else ";") + 1]
+        if not re.search(r"\bok\b", condition) or not re.search(collective, body):
+            continue
+        found += 1
+        last = re.findall(r"\bok = ([^;]*);", softmax[:c.start()])[-1]
+        agreed = condition + last  # (a vote in the condition is an agreement itself)
+        assert "__all_sync(" in agreed or "named_vote(" in agreed, f"{name}: [if ({condition})] after [ok = {last}]"
+    assert found >= 3
