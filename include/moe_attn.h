@@ -11,7 +11,10 @@
  * synchronising, arguments checked on the host before any launch, no CPU
  * fallback, one handle used by one thread and one stream at a time.  Tensor
  * pointers that the CUDA driver does not know as device or mapped pinned
- * memory are refused with MOE_ERR_INVALID_ARG.
+ * memory are refused with MOE_ERR_INVALID_ARG.  Calls work on the device that
+ * was current when the cache's handle was made, rotary positions on that of
+ * their tensors, whichever is current at the call; `stream` belongs to that
+ * device (NULL: its default stream), device memory of another one is refused.
  */
 #ifndef MOE_ATTN_H_
 #define MOE_ATTN_H_

@@ -44,8 +44,9 @@ void fail(moe_kv_t* h, const char* fmt, ...) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// A tensor as the kernels address it, or NULL with the reason in *why.
-const void* resolve(const void* p, const char** why) {
+// A tensor as the kernels address it, or NULL with the reason in *why.  Device
+// memory has to lie on *device; -1 becomes the tensor's device.
+const void* resolve(const void* p, int* device, const char** why) {
   if (!p) {
     *why = "is NULL";
     return nullptr;
@@ -58,6 +59,11 @@ const void* resolve(const void* p, const char** why) {
   if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
     cudaGetLastError();
     *why = "is not known to the CUDA driver";
+    return nullptr;
+  }
+  if (at.type == cudaMemoryTypeDevice && *device < 0) *device = at.device;
+  if (at.type == cudaMemoryTypeDevice && at.device != *device) {
+    *why = "lies on another device than the handle or the first tensor";
     return nullptr;
   }
   if (at.type == cudaMemoryTypeDevice || at.type == cudaMemoryTypeManaged) return p;
@@ -131,7 +137,7 @@ moe_status_t view(moe_kv_t* h, const moe_kv_batch_t* b, moe::KvView* v) {
   const char* name[3] = {"cu_q", "kv_len", "page_table"};
   for (int i = 0; i < 3; ++i) {
     const char* why = nullptr;
-    p[i] = resolve(p[i], &why);
+    p[i] = resolve(p[i], &h->device, &why);
     if (!p[i]) {
       fail(h, "%s %s", name[i], why);
       return MOE_ERR_INVALID_ARG;
@@ -156,9 +162,9 @@ moe_status_t check_stride(moe_kv_t* h, const char* name, int64_t stride, int64_t
   return MOE_OK;
 }
 
-moe_status_t tensor(moe_kv_t* h, const char* name, const void** p) {
+moe_status_t tensor(moe_kv_t* h, int* device, const char* name, const void** p) {
   const char* why = nullptr;
-  const void* r = resolve(*p, &why);
+  const void* r = resolve(*p, device, &why);
   if (!r) {
     fail(h, "%s %s", name, why);
     return MOE_ERR_INVALID_ARG;
@@ -166,6 +172,29 @@ moe_status_t tensor(moe_kv_t* h, const char* name, const void** p) {
   *p = r;
   return MOE_OK;
 }
+
+// Makes a device current while a call works on it, and the caller's again.  A
+// launch (and the stream NULL) goes to the current device, which need not be the
+// one whose memory the call was given.
+class OnDevice {
+ public:
+  explicit OnDevice(int device) {
+    error = cudaGetDevice(&back_);
+    if (error != cudaSuccess || device < 0 || back_ == device)
+      back_ = -1;
+    else
+      error = cudaSetDevice(device);
+  }
+  ~OnDevice() {
+    if (back_ >= 0) cudaSetDevice(back_);
+  }
+  OnDevice(const OnDevice&) = delete;
+  OnDevice& operator=(const OnDevice&) = delete;
+  cudaError_t error;
+
+ private:
+  int back_ = -1;
+};
 
 moe_status_t launched(moe_kv_t* h, cudaError_t e, const char* what) {
   if (e == cudaSuccess) return MOE_OK;
@@ -281,6 +310,7 @@ moe_status_t moe_rope_apply(const moe_rope_t* r, const moe_rope_tensor_t* q,
   const char* names[2][4] = {{"q.x", "q.y", "q.x_stride", "q.y_stride"},
                              {"k.x", "k.y", "k.x_stride", "k.y_stride"}};
   moe_rope_tensor_t t[2];
+  int device = -1;
   for (int w = 0; w < 2; ++w) {
     if (!in[w]) continue;
     t[w] = *in[w];
@@ -293,9 +323,9 @@ moe_status_t moe_rope_apply(const moe_rope_t* r, const moe_rope_tensor_t* q,
     if (st == MOE_OK) st = check_stride(nullptr, names[w][3], t[w].y_stride, row, esz);
     if (st != MOE_OK) return st;
     if (n_tokens == 0) continue;
-    if ((st = tensor(nullptr, names[w][0], &t[w].x)) != MOE_OK) return st;
+    if ((st = tensor(nullptr, &device, names[w][0], &t[w].x)) != MOE_OK) return st;
     const void* y = t[w].y;
-    if ((st = tensor(nullptr, names[w][1], &y)) != MOE_OK) return st;
+    if ((st = tensor(nullptr, &device, names[w][1], &y)) != MOE_OK) return st;
     t[w].y = const_cast<void*>(y);
     if (t[w].x == t[w].y && t[w].x_stride != t[w].y_stride) {
       fail(nullptr, "in place, %s and %s must be equal", names[w][2], names[w][3]);
@@ -304,7 +334,9 @@ moe_status_t moe_rope_apply(const moe_rope_t* r, const moe_rope_tensor_t* q,
   }
   if (n_tokens == 0) return MOE_OK;
   const void* pos = positions;
-  if (const moe_status_t st = tensor(nullptr, "positions", &pos); st != MOE_OK) return st;
+  if (const moe_status_t st = tensor(nullptr, &device, "positions", &pos); st != MOE_OK) return st;
+  const OnDevice on(device);
+  if (on.error != cudaSuccess) return launched(nullptr, on.error, "moe_rope_apply");
   return launched(nullptr,
                   moe::rope_launch(r->inc, r->rot_dim, r->amplitude, r->interleaved, &t[0],
                                    k ? &t[1] : nullptr, head_dim, dtype,
@@ -404,6 +436,7 @@ moe_status_t moe_kv_create(const moe_kv_config_t* cfg, const moe_kv_store_t* sto
 
 void moe_kv_destroy(moe_kv_t* h) {
   if (!h) return;
+  const OnDevice on(h->device);
   cudaDeviceSynchronize();
   cudaFree(h->base);
   delete h;
@@ -427,8 +460,10 @@ moe_status_t moe_kv_write(moe_kv_t* h, const void* k, int64_t k_stride, const vo
   const int64_t row = static_cast<int64_t>(h->cfg.n_kv_heads) * h->cfg.head_dim;
   if ((st = check_stride(h, "k_stride", k_stride, row, esz)) != MOE_OK) return st;
   if ((st = check_stride(h, "v_stride", v_stride, row, esz)) != MOE_OK) return st;
-  if ((st = tensor(h, "k", &k)) != MOE_OK) return st;
-  if ((st = tensor(h, "v", &v)) != MOE_OK) return st;
+  if ((st = tensor(h, &h->device, "k", &k)) != MOE_OK) return st;
+  if ((st = tensor(h, &h->device, "v", &v)) != MOE_OK) return st;
+  const OnDevice on(h->device);
+  if (on.error != cudaSuccess) return launched(h, on.error, "moe_kv_write");
   return launched(h, moe::kv_write_launch(c, k, k_stride, v, v_stride, dtype,
                                           static_cast<cudaStream_t>(stream)),
                   "moe_kv_write");
@@ -448,8 +483,10 @@ moe_status_t moe_kv_read(moe_kv_t* h, void* k_out, void* v_out, moe_dtype_t dtyp
   moe_status_t st = view(h, batch, &c);
   if (st != MOE_OK || c.n_seqs == 0 || (!k_out && !v_out)) return st;
   const void* p[2] = {k_out, v_out};
-  if (p[0] && (st = tensor(h, "k_out", &p[0])) != MOE_OK) return st;
-  if (p[1] && (st = tensor(h, "v_out", &p[1])) != MOE_OK) return st;
+  if (p[0] && (st = tensor(h, &h->device, "k_out", &p[0])) != MOE_OK) return st;
+  if (p[1] && (st = tensor(h, &h->device, "v_out", &p[1])) != MOE_OK) return st;
+  const OnDevice on(h->device);
+  if (on.error != cudaSuccess) return launched(h, on.error, "moe_kv_read");
   return launched(h, moe::kv_read_launch(c, const_cast<void*>(p[0]), const_cast<void*>(p[1]), dtype,
                                          static_cast<cudaStream_t>(stream)),
                   "moe_kv_read");
@@ -483,9 +520,9 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
   const int64_t row = static_cast<int64_t>(h->cfg.n_q_heads) * h->cfg.head_dim;
   if ((st = check_stride(h, "q_stride", q_stride, row, 2)) != MOE_OK) return st;
   const void *o = out, *z = lse;
-  if ((st = tensor(h, "q", &q)) != MOE_OK) return st;
-  if ((st = tensor(h, "out", &o)) != MOE_OK) return st;
-  if (lse && (st = tensor(h, "lse", &z)) != MOE_OK) return st;
+  if ((st = tensor(h, &h->device, "q", &q)) != MOE_OK) return st;
+  if ((st = tensor(h, &h->device, "out", &o)) != MOE_OK) return st;
+  if (lse && (st = tensor(h, &h->device, "lse", &z)) != MOE_OK) return st;
   moe::AttnArgs a{};
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.q_stride = q_stride;
@@ -506,6 +543,8 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
   // that the second reads once.
   const bool tiles = static_cast<int64_t>(c.max_q) * a.G > 32;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const OnDevice on(h->device);
+  if (on.error != cudaSuccess) return launched(h, on.error, "moe_kv_attend");
   return launched(h, tiles ? moe::attn_tiles_launch(c, a, h->ws, h->maps, h->n_sm, s)
                            : moe::attn_few_launch(c, a, h->ws, h->maps, h->n_sm, s),
                   "moe_kv_attend");
@@ -517,7 +556,9 @@ moe_status_t moe_kv_device_status(moe_kv_t* h, int32_t* flags) {
     return MOE_ERR_INVALID_ARG;
   }
   int32_t v = 0;
-  cudaError_t e = cudaDeviceSynchronize();
+  const OnDevice on(h->device);
+  cudaError_t e = on.error;
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e == cudaSuccess) e = cudaMemcpy(&v, h->err, 4, cudaMemcpyDeviceToHost);
   if (e == cudaSuccess && v) {
     e = cudaMemset(h->err, 0, 4);
