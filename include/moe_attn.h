@@ -34,8 +34,9 @@ extern "C" {
  * interleaved; elements from rot_dim on are copied.  Frequencies are the
  * caller's, so every scaling of them for long contexts fits.  An angle is
  * kept as a 64-bit fraction of a turn per position, whose product with the
- * position wraps: the error of a phase is below 2^-33 turns at every int32
- * position (negative ones turn backwards).
+ * position wraps and is rounded to 32 bits: together off by less than 2^-31
+ * turns at every int32 position (negative ones turn backwards) for frequencies
+ * below 2^38; sine and cosine are fp32 ones of that angle.
  *
  * moe_rope_create: rot_dim a multiple of 16 in [16, 256]; inv_freq: rot_dim/2
  *   finite doubles on the host, copied; amplitude finite.  Host only.

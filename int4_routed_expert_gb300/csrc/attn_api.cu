@@ -76,6 +76,26 @@ const char* check_dtype(moe_dtype_t dt) {
   return dt == MOE_F32 || dt == MOE_BF16 ? nullptr : "dtype must be MOE_F32 or MOE_BF16";
 }
 
+// x in [0, 1) as a 64-bit fraction: two 32-bit steps carry every bit down to 2^-64.
+uint64_t fixed64(double x) {
+  const double hi = floor(x * 4294967296.0);
+  const double lo = (x * 4294967296.0 - hi) * 4294967296.0;
+  return (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(lo + 0.5);
+}
+
+// |f| / (2 pi) mod 1 as a 64-bit fraction of a turn.  A double of the quotient
+// is off by 2^-56 of a turn, which a position of 2^31 makes 2^-25; so 2 pi and the
+// quotient have a second double each, and what is left is the fraction's own
+// step, for |f| below 2^38.
+uint64_t turn_fraction(double f) {
+  constexpr double kHi = 6.283185307179586477, kLo = 2.4492935982947064e-16;  // 2 pi
+  f = fabs(f);
+  const double q1 = f / kHi;
+  const double q2 = fma(-q1, kLo, fma(-q1, kHi, f)) / kHi;
+  const double a1 = q1 - floor(q1), a2 = fabs(q2) - floor(fabs(q2));
+  return q2 < 0 ? fixed64(a1) - fixed64(a2) : fixed64(a1) + fixed64(a2);
+}
+
 const char* check_kv_config(const moe_kv_config_t* c) {
   if (!c) return "cfg is NULL";
   if (c->n_kv_heads < 1 || c->n_kv_heads > 256) return "n_kv_heads must be in [1, 256]";
@@ -272,13 +292,8 @@ moe_status_t moe_rope_create(int rot_dim, const double* inv_freq, float amplitud
   r->amplitude = amplitude;
   r->interleaved = interleaved != 0;
   for (int i = 0; i < rot_dim / 2; ++i) {
-    // the fraction of a turn per position in [0, 1), in two 32-bit steps so
-    // that a 53-bit double carries every bit of the 64
-    double turn = inv_freq[i] / 6.283185307179586476925;
-    turn -= floor(turn);
-    const double hi = floor(turn * 4294967296.0);
-    const double lo = (turn * 4294967296.0 - hi) * 4294967296.0;
-    r->inc[i] = (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(lo + 0.5);
+    const uint64_t turn = turn_fraction(inv_freq[i]);
+    r->inc[i] = inv_freq[i] < 0 ? 0 - turn : turn;
   }
   *out = r;
   return MOE_OK;

@@ -23,6 +23,7 @@ constexpr int kDevices = 4;
 int g_current = 0, g_flags = 0;
 uintptr_t g_next[kDevices];
 std::string g_log, g_error;
+uint64_t g_inc[128];  // the last rotary call's fractions of a turn per position
 
 int device_of(const void* p) {
   const auto d = static_cast<long long>(reinterpret_cast<uintptr_t>(p) >> 40) - 1;
@@ -44,6 +45,7 @@ int fake_current() { return g_current; }
 void fake_set_flags(int flags) { g_flags = flags; }
 const char* fake_log() { return g_log.c_str(); }
 void fake_clear_log() { g_log.clear(); }
+uint64_t fake_rope_inc(int i) { return g_inc[i]; }
 
 cudaError_t cudaGetDevice(int* d) {
   *d = g_current;
@@ -122,8 +124,9 @@ void set_thread_error(const char* fmt, ...) {
 const char* device_extent_error(const void* p, size_t, int device) {
   return device_of(p) == device ? nullptr : "lies elsewhere";
 }
-cudaError_t rope_launch(const uint64_t*, int, float, bool, const moe_rope_tensor_t*, const moe_rope_tensor_t*, int,
+cudaError_t rope_launch(const uint64_t* inc, int rot_dim, float, bool, const moe_rope_tensor_t*, const moe_rope_tensor_t*, int,
                         moe_dtype_t, const int32_t*, int, cudaStream_t) {
+  memcpy(g_inc, inc, sizeof(uint64_t) * (rot_dim / 2));
   note("rope");
   return cudaSuccess;
 }

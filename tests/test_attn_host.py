@@ -3,10 +3,15 @@ call works on, what it refuses.  Only host code runs."""
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
+import random
 import subprocess
+from fractions import Fraction
 
 import pytest
+
+from turns import TWO_PI
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 INVALID = -1
@@ -28,6 +33,7 @@ def lib(tmp_path_factory):
     L.moe_kv_last_error.argtypes = L.moe_last_error.argtypes = [vp]
     L.moe_rope_create.argtypes = [i32, C.POINTER(C.c_double), C.c_float, i32, C.POINTER(vp)]
     L.moe_rope_apply.argtypes = [vp, vp, vp, i32, i32, vp, i32, vp]
+    L.fake_rope_inc.restype = C.c_uint64
     L.moe_rope_destroy.argtypes = L.moe_kv_destroy.argtypes = [vp]
     L.moe_kv_create.argtypes = [vp, vp, C.POINTER(vp)]
     L.moe_kv_write.argtypes = [vp, vp, i64, vp, i64, i32, vp, vp]
@@ -129,3 +135,19 @@ def test_rope_works_on_its_tensors_device(lib):
     assert apply(at(1, 1 << 24), at(1, 1 << 25), pos=at(0)) == INVALID
     assert lib.fake_log() == b""
     lib.moe_rope_destroy(r)
+
+
+def test_rope_fractions_of_a_turn(lib):
+    """The 64-bit fractions are off by at most a step of theirs, which every int32 position multiplies."""
+    lib.fake_reset(0)
+    r = random.Random(3)
+    freq = [1.0, -1.0, 0.75, 2 * math.pi, 1e-30, 2.0 ** 37, -1e9] + \
+        [r.choice((-1, 1)) * math.exp(r.uniform(-30, 3)) for _ in range(57)] + [r.uniform(0.5, 1.2) for _ in range(64)]
+    h = C.c_void_p()
+    assert lib.moe_rope_create(256, (C.c_double * 128)(*freq), 1.0, 0, C.byref(h)) == 0
+    t = lib.A.moe_rope_tensor_t(at(0), at(0), 1, 256, 256)
+    assert lib.moe_rope_apply(h, C.byref(t), None, 256, BF16, at(0, 1 << 20), 1, None) == 0
+    for i, f in enumerate(freq):
+        off = (lib.fake_rope_inc(i) - Fraction(f) / TWO_PI * 2 ** 64) % 2 ** 64
+        assert min(off, 2 ** 64 - off) <= 1, f
+    lib.moe_rope_destroy(h)
