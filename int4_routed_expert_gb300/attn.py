@@ -6,6 +6,8 @@ A decoder layer next to the MoE layer calls, per step:
     out = cache.attend(q, batch)                  # attention over the cache, the new tokens included
 ``SeqBatch`` describes the step's tokens (device arrays and the host's bounds).  As in moe.py, torch supplies
 device memory and streams only; every step runs in the library's kernels and there is no fallback.
+Calls run on torch's current stream, or on ``stream``, whose memory their results are then; that the inputs are
+ready there, and stay until it has run, is the caller's to see to, as with every other stream of torch.
 """
 from __future__ import annotations
 
@@ -98,6 +100,15 @@ def _stream(stream, index: int) -> int:
     return _raw_stream(index) if stream is None else stream.cuda_stream
 
 
+def _results(shape, dtype, device, stream):
+    """A result tensor in memory of the stream that writes it: memory of another one may still be in use there,
+    and be given away there before the call's kernels have run."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _rows(x, name: str, heads: int, dim: int, device) -> int:
     """Checks a [tokens][heads][dim] (or [tokens][heads * dim]) CUDA tensor whose tokens may be strided and
     whose rows are whole; returns the elements between tokens."""
@@ -183,7 +194,10 @@ class Rope:
             if dev < 0 or positions.dtype is not _int32 or positions.shape != (T,) or positions.get_device() != dev \
                     or not positions.is_contiguous() or (tk is not None and k.get_device() != dev):
                 self._refuse(q, k, positions)
-            if contiguous:
+            if stream is not None:
+                q_out = _results(q.shape, q.dtype, q.device, stream)
+                k_out = None if tk is None else _results(k.shape, k.dtype, k.device, stream)
+            elif contiguous:
                 q_out = torch.empty_like(q)
                 k_out = None if tk is None else torch.empty_like(k)
             else:
@@ -198,9 +212,9 @@ class Rope:
                 self._refuse(q, k, positions)
             if k is None and k_out is not None:
                 raise ValueError("k_out needs k")
-            q_out, tq.y_stride = self._out("q", q, q_out)
+            q_out, tq.y_stride = self._out("q", q, q_out, stream)
             if tk is not None:
-                k_out, tk.y_stride = self._out("k", k, k_out)
+                k_out, tk.y_stride = self._out("k", k, k_out, stream)
         if T:
             tq.x, tq.y = q.data_ptr(), q_out.data_ptr()
             if tk is not None:
@@ -241,10 +255,10 @@ class Rope:
         raise ValueError(f"positions must be a contiguous int32 tensor of {q.shape[0]} entries on {q.device}")
 
     @staticmethod
-    def _out(name, x, y):
+    def _out(name, x, y, stream):
         T, H, D = x.shape
         if y is None:
-            return torch.empty((T, H, D), dtype=x.dtype, device=x.device), H * D
+            return _results((T, H, D), x.dtype, x.device, stream), H * D
         if y.shape != x.shape or y.dtype != x.dtype:
             raise ValueError(f"{name}_out must be {(T, H, D)} of {x.dtype}")
         return y, _rows(y, name + "_out", H, D, x.device)
@@ -361,9 +375,9 @@ class KVCache:
             if t is not None and (t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.device != dev):
                 raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {dev}")
         if k_out is None:
-            k_out = torch.empty(shape, dtype=dtype, device=dev)
+            k_out = _results(shape, dtype, dev, stream)
         if v_out is None:
-            v_out = torch.empty(shape, dtype=dtype, device=dev)
+            v_out = _results(shape, dtype, dev, stream)
         self._check(_lib.moe_kv_read(self.h, k_out.data_ptr(), v_out.data_ptr(), code, batch.c, _stream(stream, self._index)))
         return k_out, v_out
 
@@ -380,8 +394,8 @@ class KVCache:
             raise TypeError(f"q must be bf16, got {q.dtype}")
         shape = (batch.n_tokens, H, self.head_dim)
         if out is None:
-            out = torch.empty_like(q) if q.is_contiguous() and q.dim() == 3 else \
-                torch.empty(shape, dtype=bf16, device=dev)
+            out = torch.empty_like(q) if stream is None and q.dim() == 3 and q.is_contiguous() else \
+                _results(shape, bf16, dev, stream)
         elif out.numel() != shape[0] * shape[1] * shape[2] or out.dtype != bf16 or not out.is_contiguous() \
                 or out.device != dev:
             raise ValueError(f"out must be a contiguous bf16 tensor {shape} on {dev}")
