@@ -364,10 +364,11 @@ class KVCache:
                                       _stream(stream, self._index)))
 
     def read(self, batch: SeqBatch, dtype=None, k_out=None, v_out=None, stream=None):
-        """The batch's new tokens as values: (keys, values) [tokens, kv heads, head_dim] (bf16 by default)."""
+        """The batch's new tokens as values: (keys, values) [tokens, kv heads, head_dim] of dtype (that of a result
+        which is given; bf16 without one)."""
         shape, dev = (batch.n_tokens, self.n_kv_heads, self.head_dim), self.device
         if dtype is None:
-            dtype = k_out.dtype if k_out is not None else torch.bfloat16
+            dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else torch.bfloat16
         code = _dtype(dtype, "dtype")
         if batch.index != self._index:
             raise ValueError(f"the batch must be on {dev}, got {batch.device}")

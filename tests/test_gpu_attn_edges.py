@@ -75,3 +75,15 @@ def test_results_belong_to_the_stream_that_writes_them(m):
     s.synchronize()
     assert [owner(t) for t in results] == [s.cuda_stream] * len(results)
     assert owner(c.attend(q, bt.b)) == owner(q) != s.cuda_stream
+
+
+def test_read_takes_the_type_of_a_given_result(m):
+    bt, c, _ = batch(m, [90, 40], [90, 40], 16, 64, 2, 4)
+    want = c.read(bt.b, dtype=torch.float32)
+    for name in ("k_out", "v_out"):
+        given = torch.empty_like(want[0])
+        got = c.read(bt.b, **{name: given})
+        assert got[name == "v_out"] is given
+        assert all(y.dtype == torch.float32 and torch.equal(y, x) for x, y in zip(want, got))
+    with pytest.raises(ValueError):
+        c.read(bt.b, k_out=torch.empty_like(want[0]), v_out=torch.empty_like(want[0]).bfloat16())
