@@ -72,7 +72,11 @@ void moe_rope_destroy(moe_rope_t* r);
  *   k_scale, v_scale  [n_pages][n_kv_heads] fp32
  * A value is code * scale of its page and head (the scale's block).  The
  * storage is the caller's, borrowed for the handle's lifetime; pages may hold
- * anything before they are written.
+ * anything before they are written.  Pages that the caller fills itself take
+ * any scale >= 0 and any code but NaN; attend counts a value scale below 2^-64
+ * (which write never makes) as 2^-64, so that a value is off by less than 2^-55.
+ * A scale that is negative, NaN or infinite in a page that attend reads sets bit 2
+ * of moe_kv_device_status; the rows that see the page are not valid then.
  *
  * A batch describes the tokens of one call.  Sequence b holds kv_len[b] tokens
  * (those of this call included); its last cu_q[b+1] - cu_q[b] tokens are the
@@ -165,7 +169,8 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
 /* Copies the handle's device error word to *flags (synchronous) and clears it;
  * MOE_ERR_CUDA when it was not 0.  Bit 0: a bounded wait gave up (the call's
  * outputs are not valid); bit 1: a batch broke its bounds; bit 2: NaN or
- * infinity was written to the cache. */
+ * infinity was written to the cache, or attend met a scale that is negative, NaN
+ * or infinite. */
 moe_status_t moe_kv_device_status(moe_kv_t* h, int32_t* flags);
 
 #ifdef __cplusplus

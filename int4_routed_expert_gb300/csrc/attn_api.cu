@@ -585,7 +585,7 @@ moe_status_t moe_kv_device_status(moe_kv_t* h, int32_t* flags) {
   *flags = v;
   if (!v) return MOE_OK;
   fail(h, "device error word %d:%s%s%s", v, v & 1 ? " a bounded wait gave up;" : "",
-       v & 2 ? " a batch broke its bounds;" : "", v & 4 ? " NaN or infinity was written;" : "");
+       v & 2 ? " a batch broke its bounds;" : "", v & 4 ? " NaN or infinity was written, or a scale met that is negative or not finite;" : "");
   return MOE_ERR_CUDA;
 }
 

@@ -13,7 +13,7 @@
 namespace moe {
 
 constexpr int kErrBadBatch = 2;   // device error bit: a batch broke its bounds
-constexpr int kErrNonFinite = 4;  // device error bit: NaN or infinity written to the cache
+constexpr int kErrNonFinite = 4;  // device error bit: NaN or infinity written to the cache, or a scale not in [0, inf) met
 constexpr float kMinBlockScale = 5.421010862427522e-20f;  // 2^-64
 
 // What the kernels know of the cache and of a batch (by value).

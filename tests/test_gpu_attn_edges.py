@@ -49,7 +49,8 @@ def batch(m, lens, news, page, dim, hkv, hq, seed=0):
     shape = (bt.n_pages, hkv, page, dim)
     codes = [torch.randn(*shape, device=DEV, generator=g).to(R.F8) for _ in range(2)]
     scales = [torch.exp2(torch.randint(-6, 3, shape[:2], device=DEV, generator=g).float()) for _ in range(2)]
-    c = m.KVCache(*codes, *scales, n_q_heads=hq, max_seqs=len(lens), max_tokens=bt.cu[-1], max_kv_len=max(lens))
+    c = m.KVCache(*codes, *scales, n_q_heads=hq, max_seqs=len(lens), max_tokens=max(bt.cu[-1], sum(lens)),
+                  max_kv_len=max(lens))
     return bt, c, torch.randn(bt.cu[-1], hq, dim, device=DEV, generator=g).bfloat16()
 
 
@@ -87,3 +88,45 @@ def test_read_takes_the_type_of_a_given_result(m):
         assert all(y.dtype == torch.float32 and torch.equal(y, x) for x, y in zip(want, got))
     with pytest.raises(ValueError):
         c.read(bt.b, k_out=torch.empty_like(want[0]), v_out=torch.empty_like(want[0]).bfloat16())
+
+
+@pytest.mark.parametrize("new", [1, 70])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attend_and_read_agree_about_small_scales(m, new, dim):
+    """Value scales at and below 2^-64, zero among them, on some pages and on all of them: attend's result is the
+    softmax of what read returns, to attend's own tolerance and the 448 * 2^-64 that such a value may be off by."""
+    bt, c, q = batch(m, [300, 90], [new, 1], 16, dim, 2, 8, seed=1)
+    small = [2.0 ** -64, 2.0 ** -65, 2.0 ** -80, 2.0 ** -126, 2.0 ** -140, 0.0]
+    lse = torch.empty(q.shape[:2], device=DEV)
+    for whole in (False, True):
+        for p in range(bt.n_pages):
+            if whole or p % 2:
+                c.v_scale[p] = small[p // 2 % 6]
+        out = c.attend(q, bt.b, lse=lse)
+        o, ref_lse, tol = R.attend(q, c.k_codes, c.v_codes, c.k_scale, c.v_scale, bt, dim ** -0.5)
+        assert ((out.double() - o).abs() <= tol + 448 * 2.0 ** -64).all()
+        assert ((lse.double() - ref_lse).abs() <= 2.0 ** -16 * (1 + ref_lse.abs())).all()
+        assert c.device_status() == 0
+    every = R.Batch([300, 90], [300, 90], 16, DEV, seed=1)
+    assert every.table == bt.table
+    values = c.read(every.b, dtype=torch.float32)[1].double()
+    assert float(values.abs().max()) <= 448 * 2.0 ** -64
+
+
+@pytest.mark.parametrize("new", [1, 70])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -1.0])
+def test_attend_says_that_it_met_a_bad_scale(m, new, bad):
+    bt, c, q = batch(m, [300, 90], [new, 1], 16, 64, 2, 8, seed=2)
+    want = c.attend(q, bt.b)
+    for scales in (c.k_scale, c.v_scale):
+        keep = scales.clone()
+        unused = next(p for p in range(bt.n_pages) if all(p not in row for row in bt.table))
+        scales[unused] = bad
+        assert torch.equal(c.attend(q, bt.b), want) and c.device_status() == 0
+        scales[bt.table[0][3], 1] = bad
+        out = c.attend(q, bt.b)
+        with pytest.raises(m.MoeError, match="scale"):
+            c.device_status()
+        assert torch.equal(out[:, :4], want[:, :4]) and torch.equal(out[bt.cu[1]:], want[bt.cu[1]:])
+        scales.copy_(keep)
+    assert torch.equal(c.attend(q, bt.b), want) and c.device_status() == 0
