@@ -90,7 +90,10 @@ void moe_rope_destroy(moe_rope_t* r);
  * A batch whose device arrays break the bounds (cu_q not ascending within
  * [0, n_tokens], lengths above the bounds, a needed page id outside
  * [0, n_pages)) sets bit 1 of moe_kv_device_status; the sequence's work that
- * needs them is left out, nothing out of bounds is read or written.
+ * needs them is left out, nothing out of bounds is read or written.  Rows of a
+ * result that no sequence covers, or whose sequence has such an offset or length,
+ * keep what they held; where a page id was bad, attend's rows that need the page
+ * are written, but not valid.
  * write: no two sequences of a batch may write to one page. */
 typedef struct moe_kv moe_kv_t;
 typedef struct {

@@ -279,7 +279,8 @@ class SeqBatch:
     """The tokens of one call: sequence b has kv_len[b] cached tokens, the last cu_q[b + 1] - cu_q[b] of them are
     the call's (rows cu_q[b] onwards), token t lies in page page_table[b][t // page_size].  The three int32
     tensors stay on the device and may change between calls (also between replays of a captured graph) within
-    the host's bounds: n_tokens rows, max_q_len new and max_kv_len cached tokens of any sequence."""
+    the host's bounds: n_tokens rows, max_q_len new and max_kv_len cached tokens of any sequence.  Rows that no
+    sequence covers are not written: in results that a call makes itself they hold anything."""
 
     def __init__(self, cu_q, kv_len, page_table, n_tokens: int, max_q_len: int, max_kv_len: int):
         _load()

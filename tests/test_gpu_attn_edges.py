@@ -130,3 +130,31 @@ def test_attend_says_that_it_met_a_bad_scale(m, new, bad):
         assert torch.equal(out[:, :4], want[:, :4]) and torch.equal(out[bt.cu[1]:], want[bt.cu[1]:])
         scales.copy_(keep)
     assert torch.equal(c.attend(q, bt.b), want) and c.device_status() == 0
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_rows_that_no_sequence_covers_keep_what_they_held(m, new):
+    """A graph may be replayed with fewer tokens than it was captured for, and a sequence may break its bounds."""
+    bt, c, q = batch(m, [200, 90, 60], [new, new, new], 16, 64, 2, 8, seed=3)
+    want, values = c.attend(q, bt.b), c.read(bt.b)
+    assert c.device_status() == 0
+
+    def run():
+        out = torch.full_like(q, 7)
+        lse = torch.full(q.shape[:2], 7.0, device=DEV)
+        read = [torch.full_like(x, 7) for x in values]
+        c.attend(q, bt.b, out=out, lse=lse)
+        c.read(bt.b, k_out=read[0], v_out=read[1])
+        return out, lse, *read
+
+    bt.b.cu_q[3] = bt.cu[2]  # the last sequence has no tokens now
+    bt.b.kv_len[2] = 0
+    for x, y in zip(run(), (want, None, *values)):
+        assert (x[2 * new:] == 7).all() and (y is None or torch.equal(x[:2 * new], y[:2 * new]))
+    assert c.device_status() == 0
+    bt.b.cu_q[3], bt.b.kv_len[2], bt.b.kv_len[1] = bt.cu[3], 60, -1
+    for x, y in zip(run(), (want, None, *values)):
+        assert (x[new:2 * new] == 7).all()
+        assert y is None or (torch.equal(x[:new], y[:new]) and torch.equal(x[2 * new:], y[2 * new:]))
+    with pytest.raises(m.MoeError, match="bounds"):
+        c.device_status()
