@@ -86,7 +86,8 @@ void moe_rope_destroy(moe_rope_t* r);
  * bounds: n_tokens rows in all, max_q_len new tokens and max_kv_len cached
  * tokens of any sequence (a launch is sized for them).  Tokens at positions
  * below 0 (more new tokens than the sequence's length: an idle slot) are
- * skipped by write and read and see nothing in attend.
+ * skipped by write and read and see nothing in causal attend; without causal
+ * they see every cached token, as all rows do.
  * A batch whose device arrays break the bounds (cu_q not ascending within
  * [0, n_tokens], lengths above the bounds, a needed page id outside
  * [0, n_pages)) sets bit 1 of moe_kv_device_status; the sequence's work that

@@ -158,3 +158,16 @@ def test_rows_that_no_sequence_covers_keep_what_they_held(m, new):
         assert y is None or (torch.equal(x[:new], y[:new]) and torch.equal(x[2 * new:], y[2 * new:]))
     with pytest.raises(m.MoeError, match="bounds"):
         c.device_status()
+
+
+@pytest.mark.parametrize("new", [5, 60])
+def test_rows_below_position_zero(m, new):
+    """More new tokens than cached ones: nothing to see for the first rows under the causal mask, all without."""
+    bt, c, q = batch(m, [3, 0], [new, 2], 16, 64, 1, 2, seed=4)
+    q[1:new] = q[0]  # the rows then differ by what they see alone
+    lse = torch.empty(q.shape[:2], device=DEV)
+    out = c.attend(q, bt.b, lse=lse)
+    assert not out[:new - 3].any() and lse[:new - 3].isneginf().all() and lse[new - 3:new].isfinite().all()
+    whole = c.attend(q, bt.b, lse=lse, causal=False)
+    assert torch.equal(whole[:new], out[new - 1:new].expand(new, 2, 64)) and lse[:new].isfinite().all()
+    assert not whole[new:].any() and lse[new:].isneginf().all() and c.device_status() == 0
