@@ -160,7 +160,8 @@ moe_status_t moe_kv_read(moe_kv_t* h, void* k_out, void* v_out, moe_dtype_t dtyp
  * A row that sees nothing gets 0 (and lse -inf).  window >= 0 and sinks >= 0
  * need causal != 0 when they are not 0.  q, out: [n_tokens][n_q_heads]
  * [head_dim] bf16, not overlapping, q_stride elements between q's tokens; lse: [n_tokens]
- * [n_q_heads] fp32 natural logarithms of the softmax denominators, or NULL. */
+ * [n_q_heads] fp32 natural logarithms of the softmax denominators, or NULL.
+ * n_tokens * n_q_heads is below 2^31 (MOE_ERR_UNSUPPORTED). */
 typedef struct {
   float scale; /* finite; usually head_dim ^ -0.5 */
   int causal;

@@ -1,5 +1,6 @@
 // C ABI of the attention-side operators (include/moe_attn.h): argument checks,
 // workspace, dispatch.
+#include <limits.h>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -532,6 +533,10 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
   moe::KvView c{};
   moe_status_t st = view(h, batch, &c);
   if (st != MOE_OK || c.n_seqs == 0) return st;
+  if (static_cast<int64_t>(c.n_tokens) * h->cfg.n_q_heads > INT_MAX) {  // the kernels number rows in 32 bits
+    fail(h, "%d tokens of %d query heads are more rows than one call takes", c.n_tokens, h->cfg.n_q_heads);
+    return MOE_ERR_UNSUPPORTED;
+  }
   const int64_t row = static_cast<int64_t>(h->cfg.n_q_heads) * h->cfg.head_dim;
   if ((st = check_stride(h, "q_stride", q_stride, row, 2)) != MOE_OK) return st;
   const void *o = out, *z = lse;

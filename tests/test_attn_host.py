@@ -52,11 +52,11 @@ def at(device, offset=0):
 class Kv:
     """A handle on a device, with a batch of three single tokens there."""
 
-    def __init__(self, lib, device):
+    def __init__(self, lib, device, q_heads=8, max_tokens=64):
         A = lib.A
         lib.fake_reset(device)
         self.lib, self.h = lib, C.c_void_p()
-        cfg = A.moe_kv_config_t(8, 2, 64, 16, 10, 4, 64, 128)
+        cfg = A.moe_kv_config_t(q_heads, 2, 64, 16, 10, 4, max_tokens, 128)
         st = A.moe_kv_store_t(*(at(device, i << 20) for i in range(4)))
         assert lib.moe_kv_create(C.byref(cfg), C.byref(st), C.byref(self.h)) == 0
         self.batch = A.moe_kv_batch_t(3, 3, 1, 100, 8, *(at(device, (8 + i) << 20) for i in range(3)))
@@ -73,8 +73,8 @@ class Kv:
         return self.lib.moe_kv_read(self.h, k or at(self.device, 1 << 24), v or at(self.device, 1 << 25), BF16,
                                     C.byref(self.batch), None)
 
-    def attend(self, q=None, out=None, lse=None):
-        return self.lib.moe_kv_attend(self.h, q or at(self.device, 1 << 24), 512, out or at(self.device, 1 << 25), lse,
+    def attend(self, q=None, out=None, lse=None, stride=512):
+        return self.lib.moe_kv_attend(self.h, q or at(self.device, 1 << 24), stride, out or at(self.device, 1 << 25), lse,
                                       C.byref(self.mask), C.byref(self.batch), None)
 
     def log(self):
@@ -114,6 +114,15 @@ def test_tensors_of_another_device_are_refused(lib):
         setattr(kv.batch, field, old)
     assert kv.log() == []
     assert kv.attend(lse=at(1, 1 << 26)) == 0
+    lib.moe_kv_destroy(kv.h)
+
+
+def test_attend_refuses_more_rows_than_32_bits_number(lib):
+    kv = Kv(lib, 0, q_heads=256, max_tokens=1 << 24)
+    kv.batch.n_tokens = 1 << 23
+    assert kv.attend(stride=256 * 64) == -2 and b"rows" in lib.moe_kv_last_error(kv.h) and kv.log() == []
+    kv.batch.n_tokens -= 1
+    assert kv.attend(stride=256 * 64) == 0 and len(kv.log()) == 1
     lib.moe_kv_destroy(kv.h)
 
 
