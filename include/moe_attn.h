@@ -163,7 +163,7 @@ moe_status_t moe_kv_read(moe_kv_t* h, void* k_out, void* v_out, moe_dtype_t dtyp
  * [n_q_heads] fp32 natural logarithms of the softmax denominators, or NULL.
  * n_tokens * n_q_heads is below 2^31 (MOE_ERR_UNSUPPORTED). */
 typedef struct {
-  float scale; /* finite; usually head_dim ^ -0.5 */
+  float scale; /* finite, its product with log2 e too; usually head_dim ^ -0.5 */
   int causal;
   int window;
   int sinks;

@@ -518,8 +518,9 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
     fail(h, "mask is NULL");
     return MOE_ERR_INVALID_ARG;
   }
-  if (!isfinite(mask->scale)) {
-    fail(h, "scale must be finite");
+  const float scale_log2 = mask->scale * 1.4426950408889634f;
+  if (!isfinite(scale_log2)) {
+    fail(h, "scale must be finite, in base 2 too");
     return MOE_ERR_INVALID_ARG;
   }
   if (mask->window < 0 || mask->sinks < 0) {
@@ -548,7 +549,7 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
   a.q_stride = q_stride;
   a.out = static_cast<__nv_bfloat16*>(const_cast<void*>(o));
   a.lse = static_cast<float*>(const_cast<void*>(z));
-  a.scale_log2 = mask->scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.causal = mask->causal != 0;
   // a window that reaches every cached token is none
   a.window = mask->window >= c.max_kv ? 0 : mask->window;

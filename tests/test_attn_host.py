@@ -126,6 +126,16 @@ def test_attend_refuses_more_rows_than_32_bits_number(lib):
     lib.moe_kv_destroy(kv.h)
 
 
+@pytest.mark.parametrize("scale,status", [(2.3e38, 0), (2.4e38, INVALID), (-2.4e38, INVALID), (math.inf, INVALID),
+                                          (math.nan, INVALID), (0.0, 0)])
+def test_attend_refuses_scales_that_overflow(lib, scale, status):
+    """The kernels take scale * log2 e, which is infinite in fp32 from 2.36e38 on: every result would be NaN."""
+    kv = Kv(lib, 0)
+    kv.mask.scale = scale
+    assert kv.attend() == status and len(kv.log()) == (status == 0)
+    lib.moe_kv_destroy(kv.h)
+
+
 def test_rope_works_on_its_tensors_device(lib):
     T = lib.A.moe_rope_tensor_t
     lib.fake_reset(0)
