@@ -125,7 +125,9 @@ typedef struct {
 } moe_kv_batch_t;
 
 /* Checks cfg (MOE_ERR_UNSUPPORTED) and that the store's arrays lie in device
- * memory and hold the bytes that cfg implies, allocates the workspace. */
+ * memory and hold the bytes that cfg implies, allocates the workspace: what the
+ * largest call within cfg can use, at most 70 MB for heads of 64 and 137 MB for
+ * heads of 128. */
 moe_status_t moe_kv_create(const moe_kv_config_t* cfg, const moe_kv_store_t* store,
                            moe_kv_t** out);
 size_t moe_kv_workspace_bytes(const moe_kv_config_t* cfg); /* 0 if cfg is invalid */

@@ -5,6 +5,7 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <algorithm>
 #include <new>
 
 #include "attn_internal.cuh"
@@ -112,19 +113,30 @@ const char* check_kv_config(const moe_kv_config_t* c) {
   return nullptr;
 }
 
-// Rows of partial results (64 or 128 MB of sums): six CTAs of 256 rows a SM; the
-// splits of a call are limited to what fits.
-constexpr size_t kPartRows = 1u << 18;
+// Rows of partial results: as many as the largest call within the handle's bounds
+// can use, that is every tile of keys of every row tile a split (at most 256, or
+// 4096 rows in the kernel for few rows), but at most 2^18 (64 or 128 MB of sums):
+// six CTAs of 256 rows a SM.  The splits of a call are limited to what fits.
+size_t part_rows(const moe_kv_config_t* c) {
+  const int64_t tiles = (static_cast<int64_t>(c->max_kv_len) + 127) / 128;
+  const int64_t heads = static_cast<int64_t>(c->n_kv_heads) * c->max_seqs;
+  const int64_t rows = static_cast<int64_t>(c->max_tokens) * (c->n_q_heads / c->n_kv_heads);
+  const int64_t few = heads * std::min<int64_t>(32 * tiles, 4096);
+  const int64_t most = rows > 32 ? (rows + 255) / 256 * 256 * std::min<int64_t>(tiles, 256) : 0;
+  constexpr int64_t kEnd = 1 << 18;
+  return static_cast<size_t>(std::min(kEnd, std::max(few, most >= kEnd ? kEnd : heads * most)));
+}
 
 struct KvLayout {
-  size_t o, ml, count, err, total;
+  size_t rows, o, ml, count, err, total;
 };
 KvLayout kv_layout(const moe_kv_config_t* c) {
   KvLayout L;
+  L.rows = part_rows(c);
   L.o = 0;
-  L.ml = L.o + kPartRows * c->head_dim * 4;
-  L.count = L.ml + kPartRows * 8;
-  L.err = L.count + kPartRows / 16 * 4;
+  L.ml = L.o + L.rows * c->head_dim * 4;
+  L.count = L.ml + L.rows * 8;
+  L.err = L.count + L.rows / 16 * 4;
   L.total = L.err + 256;
   return L;
 }
@@ -429,7 +441,7 @@ moe_status_t moe_kv_create(const moe_kv_config_t* cfg, const moe_kv_store_t* sto
     }
   char* base = static_cast<char*>(h->base);
   h->ws = moe::AttnWs{reinterpret_cast<float*>(base + L.o), reinterpret_cast<float2*>(base + L.ml),
-                      reinterpret_cast<unsigned*>(base + L.count), kPartRows};
+                      reinterpret_cast<unsigned*>(base + L.count), L.rows};
   h->count_bytes = L.err - L.count;
   h->err = reinterpret_cast<int*>(base + L.err);
   e = cudaMemset(base + L.count, 0, L.total - L.count);

@@ -136,6 +136,39 @@ def test_attend_refuses_scales_that_overflow(lib, scale, status):
     lib.moe_kv_destroy(kv.h)
 
 
+def _rows(lib, cfg):
+    """Rows of partial results in a configuration's workspace: sums, a reference and a weight sum, a counter for 16."""
+    L = lib.moe_kv_workspace_bytes
+    L.restype = C.c_size_t
+    rows, rest = divmod((L(C.byref(cfg)) - 256) * 4, (cfg.head_dim * 4 + 8) * 4 + 1)
+    assert rest == 0 and rows % 32 == 0
+    return rows
+
+
+def test_workspace_holds_what_the_bounds_can_use(lib):
+    """Room for a split of every tile of keys, up to each kernel's limits, for every call within the bounds; no more."""
+    cfg = lib.A.moe_kv_config_t
+    assert _rows(lib, cfg(48, 8, 128, 64, 100, 64, 8192, 131072)) == 1 << 18
+    assert _rows(lib, cfg(8, 2, 64, 16, 10, 1, 1, 128)) == 64  # one token, one tile of keys
+    assert _rows(lib, cfg(48, 8, 128, 64, 100, 1, 1, 4096)) == 8 * 32 * 32
+    assert _rows(lib, cfg(4, 2, 64, 16, 64, 2, 64, 64)) == 2 * 2 * 256  # a tile of keys, 128 rows of 256
+    r = random.Random(1)
+    for _ in range(2000):
+        hkv, g = r.choice((1, 2, 8, 256)), r.choice((1, 3, 16))
+        seqs, tokens, kv = (int(2 ** r.uniform(0, b)) for b in (15.9, 24, 30))
+        cap = _rows(lib, cfg(hkv * g, hkv, r.choice((64, 128)), 16, 10, seqs, tokens, kv))
+        assert cap <= 1 << 18
+        for _ in range(20):
+            n, q = r.randint(1, seqs), r.randint(1, min(tokens, r.choice((1, 8, 100, tokens))))
+            tiles = -(-r.randint(1, kv) // 128)
+            if q * g <= 32:
+                rows = 16 if q * g <= 16 else 32
+                need = n * hkv * rows * min(tiles, 256, 4096 // rows)
+            else:
+                need = n * hkv * -(-q * g // 256) * 256 * min(tiles, 256)
+            assert need <= cap or cap == 1 << 18
+
+
 def test_rope_works_on_its_tensors_device(lib):
     T = lib.A.moe_rope_tensor_t
     lib.fake_reset(0)
