@@ -74,6 +74,8 @@ __device__ __forceinline__ void codes_to_half(uint32_t four, uint32_t& lo, uint3
       : "r"(four));
 }
 
+// 2^x, off by 2^-22 of itself at most, and 0 below 2^-126: a weight goes on with f16's 11 bits, and one of
+// 2^-126 is 2^-136 of the row's reference.
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

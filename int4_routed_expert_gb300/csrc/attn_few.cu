@@ -28,8 +28,9 @@
 // Warps: 4 softmax for every 16 rows, MMA, load.
 // Bound by memory: 2 D bytes a key and kv head.  64 sequences of up to 16384
 // keys, 64 query and 8 kv heads of 128: 208 us, 5.1 TB/s; 32 rows a kv head
-// (16 x 16384 keys, 4 kv heads) 90 us, 3.0 TB/s, where a tile's chain S -> weights
-// -> O, twice as much softmax, bounds it.
+// (16 x 16384 keys, 4 kv heads) 89 us, 3.0 TB/s, where a tile's chain S -> weights
+// -> O, twice as much softmax, bounds it; two such CTAs a SM leave 96 registers a
+// thread, and 60 bytes are spilt.
 #include "attn_tc.cuh"
 
 namespace moe {

@@ -32,13 +32,14 @@
 // the softmax warps about as many issue slots (a multiply-add, an exponential, a
 // share of the sum, the maximum, the conversion and the tensor memory's traffic
 // a logit).  What bounds it is the chain S -> weights -> O of either M tile, of
-// which only two are under way: 694 us for a prompt of 8192 tokens with 48 query
-// and 8 kv heads of 128, 1187 TFLOP/s, about half of the pipe's rate.  Of a
+// which only two are under way: 696 us for a prompt of 8192 tokens with 48 query
+// and 8 kv heads of 128, 1185 TFLOP/s, about half of the pipe's rate.  Of a
 // tile's 3500 clocks 1024 are products, 1900 softmax and the rest the way from
 // one to the other; a CTA's beginning and end cost as much as five tiles.  Heads
-// of 64 have half the products to the same softmax: 728 TFLOP/s (16384 tokens).
-// 20 warps leave 96 registers a thread; two conversion warps instead of four
-// (80 registers) brought 729 us down to 718 us at the time.
+// of 64 have half the products to the same softmax: 716 TFLOP/s (16384 tokens).
+// 20 warps leave 96 registers a thread (and 4 to 36 bytes of them spilt); two
+// conversion warps instead of four (80 registers) brought 729 us down to 718 us at
+// the time.
 #include "attn_tc.cuh"
 
 namespace moe {
@@ -90,7 +91,7 @@ enum Bar {
 // are the same rows then, each with every other tile of keys and with sums of
 // its own, which the join takes for two splits: one's softmax still runs under
 // the other's products.  48 rows a kv head (four sequences of up to 131072
-// keys, 4 kv heads): 143 us, and 198 us as one M tile.
+// keys, 4 kv heads): 142 us, and 198 us as one M tile.
 template <int D, bool DUAL>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tiles_kernel(const KvView c, const AttnArgs a, const AttnWs ws, const Plan pl,
@@ -194,7 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // overwrites: one thread's products run on the tensor pipe in the order of
       // their issue.  (Waiting for the product before issuing S costs a commit's
       // and a wait's latency, about 1000 clocks a tile: prompt of 8192, 822 us
-      // to 1009 us.)
+      // to 1009 us; with a thread that looks in turn which M tile can go on,
+      // 695 us to 884 us.)
       for (int j = 0; DUAL && ok && j < n; ++j) {
         const int i = j & 1, next = j + 2;
         ok = mbar_wait(bar(kPFull + i), (j >> 1) & 1, c.err) && mbar_wait(bar(kVFull + i), (j >> 1) & 1, c.err);
@@ -375,6 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             fma2(w0, w1, v[k], v[k + 1], sc, off);
             w0 = ex2(w0), w1 = ex2(w1);
             add2(sum0, sum1, w0, w1);
+            // (f16's 11 bits for the product: an output's error stays below its own rounding to
+            // bf16's 8; the sum takes the weights as they are)
             u[8 * gg + k / 2] = half2_bits(w0, w1);
           }
           l = fmaf(sum0 + sum1, z.z, l);
