@@ -2,7 +2,9 @@
 no sequence covers, other streams."""
 from __future__ import annotations
 
+import importlib.util
 import math
+import os
 import random
 from fractions import Fraction
 
@@ -171,3 +173,21 @@ def test_rows_below_position_zero(m, new):
     whole = c.attend(q, bt.b, lse=lse, causal=False)
     assert torch.equal(whole[:new], out[new - 1:new].expand(new, 2, 64)) and lse[:new].isfinite().all()
     assert not whole[new:].any() and lse[new:].isneginf().all() and c.device_status() == 0
+
+
+def test_the_example_does_not_hide_what_is_not_finite(m, monkeypatch):
+    """Its difference is NaN where a result is, for both sequences and for the second alone."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decoder_step.py")
+    spec = importlib.util.spec_from_file_location("decoder_step", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    step = ex.DecoderLayer.step
+    for bad in (slice(None), slice(1, 2)):
+        def broken(self, x, news):
+            y = step(self, x, news)
+            if news == [1, 1]:
+                y[bad] = math.nan
+            return y
+
+        monkeypatch.setattr(ex.DecoderLayer, "step", broken)
+        assert math.isnan(ex.main())
