@@ -12,7 +12,7 @@ Every case has a plain form in elementary torch operations (``own`` False) and t
 The layouts are those of the package:
   cache codes  [pages][kv heads][page][dim] float8_e4m3fn, one fp32 scale per (page, kv head), for keys and values
   a pool       table [slots][width] page ids (-1: none), kv_len [slots], ref [pages] uses of each page, all int32
-  moves        [n][3] int32: source page, destination page, tokens; the list ends at the first negative source
+  moves        [n][3] int32: source page, destination page, tokens; a negative source is no move
   a prefix     group g holds sequences cu_seq[g] .. cu_seq[g + 1] - 1, whose first prefix_len[g] tokens lie in
                page_table[g]
 """
