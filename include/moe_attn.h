@@ -4,7 +4,8 @@
  * positions, a paged key/value cache held in 8 bits with a scale for each
  * block of tokens and head, and attention over that cache, for prompts and
  * for single tokens, with an optional sliding window and first tokens that
- * stay visible.  Part of libmoe.so.
+ * stay visible.  Part of libmoe.so; which sequence has which pages is the
+ * caller's to say, or moe_pages.h's.
  *
  * Conventions are those of moe.h: device pointers (16-byte aligned) owned by
  * the caller, work enqueued on `stream` (cudaStream_t as void*) without
@@ -151,6 +152,19 @@ moe_status_t moe_kv_write(moe_kv_t* h, const void* k, int64_t k_stride, const vo
  * of dtype (either may be NULL).  Rows of skipped tokens are set to 0. */
 moe_status_t moe_kv_read(moe_kv_t* h, void* k_out, void* v_out, moe_dtype_t dtype,
                          const moe_kv_batch_t* batch, void* stream);
+
+/* Copies pages within the store: keys, values and scales.  moves: [n_moves] on the
+ * device; the first `tokens` tokens of page src (0 .. page_size) go to page dst, whose
+ * other tokens and, but for its scales, all else stay.  A move with a negative src is
+ * left out.  No page may be the destination of two moves, or of one and the source of
+ * another.  A move whose pages lie outside [0, n_pages) or whose tokens are outside
+ * [0, page_size] is left out and sets bit 1 of moe_kv_device_status. */
+typedef struct {
+  int32_t src;
+  int32_t dst;
+  int32_t tokens;
+} moe_page_move_t;
+moe_status_t moe_kv_copy(moe_kv_t* h, const moe_page_move_t* moves, int n_moves, void* stream);
 
 /* Attention of the batch's new tokens over the cache (write them first):
  *   out[t][h] = sum_j p_j v_j,  p = softmax_j(scale * q[t][h] . k_j)

@@ -3,8 +3,9 @@
 The layer lives in the C-ABI library ``libmoe.so`` (include/moe.h); this
 package holds its CUDA sources (``csrc/``), the in-tree build
 (``build.py``) and the ctypes bindings: ``moe.py`` (the layer, the expert
-tier) and ``attn.py`` (rotary positions, the 8-bit paged cache and attention
-over it, include/moe_attn.h).
+tier), ``attn.py`` (rotary positions, the 8-bit paged cache and attention
+over it, include/moe_attn.h) and ``pages.py`` (the cache's page pool,
+include/moe_pages.h).
 """
 from .attn import (  # noqa: F401
     KVCache,
@@ -12,6 +13,7 @@ from .attn import (  # noqa: F401
     SeqBatch,
     rope_frequencies,
 )
+from .pages import PagePool  # noqa: F401
 from .moe import (  # noqa: F401
     EXPORTED,
     ExpertTier,

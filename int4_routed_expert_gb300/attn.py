@@ -43,7 +43,7 @@ class moe_kv_mask_t(C.Structure):
 
 
 EXPORTED = ("moe_rope_create", "moe_rope_apply", "moe_rope_destroy", "moe_kv_create", "moe_kv_workspace_bytes",
-            "moe_kv_last_error", "moe_kv_destroy", "moe_kv_write", "moe_kv_read", "moe_kv_attend",
+            "moe_kv_last_error", "moe_kv_destroy", "moe_kv_write", "moe_kv_read", "moe_kv_copy", "moe_kv_attend",
             "moe_kv_device_status")
 
 # bits of moe_kv_device_status
@@ -73,6 +73,7 @@ def _load() -> C.CDLL:
         "moe_kv_destroy": (None, [vp]),
         "moe_kv_write": (i32, [vp, vp, i64, vp, i64, i32, C.POINTER(moe_kv_batch_t), vp]),
         "moe_kv_read": (i32, [vp, vp, vp, i32, C.POINTER(moe_kv_batch_t), vp]),
+        "moe_kv_copy": (i32, [vp, vp, i32, vp]),
         "moe_kv_attend": (i32, [vp, vp, i64, vp, vp, C.POINTER(moe_kv_mask_t), C.POINTER(moe_kv_batch_t), vp]),
         "moe_kv_device_status": (i32, [vp, C.POINTER(C.c_int32)]),
     }
@@ -382,6 +383,15 @@ class KVCache:
             v_out = _results(shape, dtype, dev, stream)
         self._check(_lib.moe_kv_read(self.h, k_out.data_ptr(), v_out.data_ptr(), code, batch.c, _stream(stream, self._index)))
         return k_out, v_out
+
+    def copy(self, moves, stream=None) -> None:
+        """Copies pages: moves [n, 3] int32 (source page, destination page, tokens), such as PagePool.fork and
+        PagePool.compact give; a negative source is no move."""
+        if moves.dtype is not torch.int32 or moves.dim() != 2 or moves.shape[1] != 3 or not moves.is_contiguous() \
+                or moves.get_device() != self._index:
+            raise ValueError(f"moves must be a contiguous int32 tensor [n, 3] on {self.device}, got {moves.dtype} "
+                             f"{tuple(moves.shape)} on {moves.device}")
+        self._check(_lib.moe_kv_copy(self.h, moves.data_ptr(), moves.shape[0], _stream(stream, self._index)))
 
     def attend(self, q, batch: SeqBatch, out=None, lse=None, scale: float | None = None, causal: bool = True,
                window: int = 0, sinks: int = 0, stream=None):
