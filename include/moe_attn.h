@@ -49,7 +49,15 @@ extern "C" {
  *   overlap.  head_dim: a multiple of 16, rot_dim <= head_dim <= 256.
  *   positions: [n_tokens] int32 on the device.  n_tokens == 0 is a no-op.
  *   Arithmetic in fp32, one rounding to dtype.
- * Messages of both go to moe_last_error(NULL). */
+ *
+ * Positions with several axes (time, height and width of an image's or a video's
+ * patches): pair i turns by axis axis[i]'s position.
+ * moe_rope_create_axes: as moe_rope_create; n_axes in [1, 4]; axis: rot_dim/2
+ *   entries in [0, n_axes) on the host, copied.
+ * moe_rope_apply_axes: as moe_rope_apply, with positions [n_axes][n_tokens] on the
+ *   device, the axes position_stride entries apart (at least n_tokens).  It takes
+ *   every handle; moe_rope_apply those of one axis.
+ * Messages of all go to moe_last_error(NULL). */
 typedef struct moe_rope moe_rope_t;
 typedef struct {
   const void* x;
@@ -64,6 +72,13 @@ moe_status_t moe_rope_create(int rot_dim, const double* inv_freq, float amplitud
 moe_status_t moe_rope_apply(const moe_rope_t* r, const moe_rope_tensor_t* q,
                             const moe_rope_tensor_t* k, int head_dim, moe_dtype_t dtype,
                             const int32_t* positions, int n_tokens, void* stream);
+moe_status_t moe_rope_create_axes(int rot_dim, const double* inv_freq, float amplitude,
+                                  int interleaved, int n_axes, const int32_t* axis,
+                                  moe_rope_t** out);
+moe_status_t moe_rope_apply_axes(const moe_rope_t* r, const moe_rope_tensor_t* q,
+                                 const moe_rope_tensor_t* k, int head_dim, moe_dtype_t dtype,
+                                 const int32_t* positions, int64_t position_stride,
+                                 int n_tokens, void* stream);
 void moe_rope_destroy(moe_rope_t* r);
 
 /* ---- The cache ------------------------------------------------------------

@@ -11,6 +11,7 @@ from .attn import (  # noqa: F401
     KVCache,
     Rope,
     SeqBatch,
+    rope_axes,
     rope_frequencies,
 )
 from .pages import PagePool  # noqa: F401

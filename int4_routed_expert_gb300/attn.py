@@ -42,9 +42,9 @@ class moe_kv_mask_t(C.Structure):
     _fields_ = [("scale", C.c_float), ("causal", C.c_int), ("window", C.c_int), ("sinks", C.c_int)]
 
 
-EXPORTED = ("moe_rope_create", "moe_rope_apply", "moe_rope_destroy", "moe_kv_create", "moe_kv_workspace_bytes",
-            "moe_kv_last_error", "moe_kv_destroy", "moe_kv_write", "moe_kv_read", "moe_kv_copy", "moe_kv_attend",
-            "moe_kv_device_status")
+EXPORTED = ("moe_rope_create", "moe_rope_create_axes", "moe_rope_apply", "moe_rope_apply_axes", "moe_rope_destroy",
+            "moe_kv_create", "moe_kv_workspace_bytes", "moe_kv_last_error", "moe_kv_destroy", "moe_kv_write",
+            "moe_kv_read", "moe_kv_copy", "moe_kv_attend", "moe_kv_device_status")
 
 # bits of moe_kv_device_status
 KV_WAIT_GAVE_UP, KV_BAD_BATCH, KV_NON_FINITE = 1, 2, 4
@@ -66,6 +66,9 @@ def _load() -> C.CDLL:
     sig = {
         "moe_rope_create": (i32, [i32, C.POINTER(C.c_double), C.c_float, i32, C.POINTER(vp)]),
         "moe_rope_apply": (i32, [vp, C.POINTER(moe_rope_tensor_t), C.POINTER(moe_rope_tensor_t), i32, i32, vp, i32, vp]),
+        "moe_rope_create_axes": (i32, [i32, C.POINTER(C.c_double), C.c_float, i32, i32, C.POINTER(C.c_int32), C.POINTER(vp)]),
+        "moe_rope_apply_axes": (i32, [vp, C.POINTER(moe_rope_tensor_t), C.POINTER(moe_rope_tensor_t), i32, i32, vp, i64, i32,
+                                      vp]),
         "moe_rope_destroy": (None, [vp]),
         "moe_kv_create": (i32, [C.POINTER(moe_kv_config_t), C.POINTER(moe_kv_store_t), C.POINTER(vp)]),
         "moe_kv_workspace_bytes": (C.c_size_t, [C.POINTER(moe_kv_config_t)]),
@@ -155,14 +158,37 @@ def rope_frequencies(rot_dim: int, theta: float = 10000.0, scaling: str | None =
     return [x * (1 - r) + x / factor * r for x, r in zip(f, ramp)], 0.1 * math.log(factor) + 1.0
 
 
+def rope_axes(rot_dim: int, sections, turns: bool = False):
+    """The axis of each of rot_dim / 2 pairs: sections[a] pairs turn by axis a, one axis behind the other, or
+    (turns) the axes take turns while they have pairs left."""
+    left, half = list(sections), rot_dim // 2
+    if sum(left) != half or min(left) < 0:
+        raise ValueError(f"the sections must add up to {half} pairs, got {list(sections)}")
+    if not turns:
+        return [a for a, n in enumerate(left) for _ in range(n)]
+    out = []
+    while len(out) < half:
+        for a, n in enumerate(left):
+            if n:
+                out.append(a)
+                left[a] -= 1
+    return out
+
+
 class Rope:
-    """Rotary positions (moe_rope_*).  Frequencies by rope_frequencies, or given (radians per position)."""
+    """Rotary positions (moe_rope_*).  Frequencies by rope_frequencies, or given (radians per position).  axes: the
+    axis (0 .. 3) of each pair, for tokens that have several positions (time, height and width of a patch), as
+    rope_axes makes it; positions are then [axes, tokens]."""
 
     def __init__(self, rot_dim: int, theta: float = 10000.0, interleaved: bool = False, scaling: str | None = None,
                  factor: float = 1.0, original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
-                 inv_freq=None, amplitude: float | None = None):
+                 inv_freq=None, amplitude: float | None = None, axes=None):
         self.h = None
         self._layouts = {}
+        if axes is not None and len(axes) != rot_dim // 2:
+            raise ValueError(f"axes must have {rot_dim // 2} entries, got {len(axes)}")
+        self.axes = None if axes is None else [int(a) for a in axes]
+        self.n_axes = 1 if axes is None else max(self.axes, default=0) + 1
         if inv_freq is None:
             inv_freq, amp = rope_frequencies(rot_dim, theta, scaling, factor, original_len, beta_fast, beta_slow)
         else:
@@ -172,15 +198,19 @@ class Rope:
         self.rot_dim, self.interleaved = rot_dim, interleaved
         self.inv_freq, self.amplitude = inv_freq, amp if amplitude is None else amplitude
         h = C.c_void_p()
-        st = _load().moe_rope_create(rot_dim, (C.c_double * max(1, len(inv_freq)))(*inv_freq), self.amplitude,
-                                     1 if interleaved else 0, C.byref(h))
+        freq = (C.c_double * max(1, len(inv_freq)))(*inv_freq)
+        if axes is None:
+            st = _load().moe_rope_create(rot_dim, freq, self.amplitude, 1 if interleaved else 0, C.byref(h))
+        else:
+            st = _load().moe_rope_create_axes(rot_dim, freq, self.amplitude, 1 if interleaved else 0, self.n_axes,
+                                              (C.c_int32 * max(1, len(self.axes)))(*self.axes), C.byref(h))
         if st != MOE_OK:
             raise MoeError(st, moe.moe_last_error(None))
         self.h = h
 
     def apply(self, q, positions, k=None, q_out=None, k_out=None, stream=None):
-        """Rotates q [tokens, heads, head_dim] (and k) at positions [tokens] int32; returns q's result, or
-        (q's, k's) when k is given.  Tokens may be strided (parts of one projection); q_out is q rotates in
+        """Rotates q [tokens, heads, head_dim] (and k) at positions [tokens] int32 ([axes, tokens] with axes, whose
+        rows may be further apart); returns q's result, or (q's, k's) when k is given.  Tokens may be strided (parts of one projection); q_out is q rotates in
         place."""
         if q_out is None and k_out is None:
             # the checks of a layout (shapes, strides, types) once: a call is a few microseconds; the argument
@@ -192,8 +222,8 @@ class Rope:
                 known = self._layout(key, q, k)
             T, D, dt, tq, tk, contiguous = known
             dev = q.get_device()
-            if dev < 0 or positions.dtype is not _int32 or positions.shape != (T,) or positions.get_device() != dev \
-                    or not positions.is_contiguous() or (tk is not None and k.get_device() != dev):
+            if dev < 0 or not self._placed(positions, T) or positions.get_device() != dev \
+                    or (tk is not None and k.get_device() != dev):
                 self._refuse(q, k, positions)
             if stream is not None:
                 q_out = _results(q.shape, q.dtype, q.device, stream)
@@ -208,8 +238,8 @@ class Rope:
             known = self._layout(None, q, k)
             T, D, dt, tq, tk, _ = known
             dev = q.get_device()
-            if dev < 0 or positions.dtype is not _int32 or positions.shape != (T,) or positions.get_device() != dev \
-                    or not positions.is_contiguous() or (tk is not None and k.get_device() != dev):
+            if dev < 0 or not self._placed(positions, T) or positions.get_device() != dev \
+                    or (tk is not None and k.get_device() != dev):
                 self._refuse(q, k, positions)
             if k is None and k_out is not None:
                 raise ValueError("k_out needs k")
@@ -220,8 +250,12 @@ class Rope:
             tq.x, tq.y = q.data_ptr(), q_out.data_ptr()
             if tk is not None:
                 tk.x, tk.y = k.data_ptr(), k_out.data_ptr()
-            st = _lib.moe_rope_apply(self.h, tq, tk, D, dt, positions.data_ptr(), T,
-                                     _raw_stream(dev) if stream is None else stream.cuda_stream)
+            s = _raw_stream(dev) if stream is None else stream.cuda_stream
+            if self.axes is None:
+                st = _lib.moe_rope_apply(self.h, tq, tk, D, dt, positions.data_ptr(), T, s)
+            else:
+                st = _lib.moe_rope_apply_axes(self.h, tq, tk, D, dt, positions.data_ptr(),
+                                              positions.stride(0) if self.n_axes > 1 else T, T, s)
             if st != MOE_OK:
                 raise MoeError(st, moe.moe_last_error(None))
         return q_out if tk is None else (q_out, k_out)
@@ -247,12 +281,21 @@ class Rope:
             self._layouts[key] = known
         return known
 
-    @staticmethod
-    def _refuse(q, k, positions):
+    def _placed(self, positions, T):
+        if positions.dtype is not _int32:
+            return False
+        if self.axes is None:
+            return positions.shape == (T,) and positions.is_contiguous()
+        return positions.shape == (self.n_axes, T) and (T == 1 or positions.stride(1) == 1) and \
+            (self.n_axes == 1 or positions.stride(0) >= T)
+
+    def _refuse(self, q, k, positions):
         if not q.is_cuda:
             raise ValueError(f"q must be a CUDA tensor [tokens, heads, head_dim], got {tuple(q.shape)} on {q.device}")
         if k is not None and k.device != q.device:
             raise ValueError(f"k must be on {q.device}, got {k.device}")
+        if self.axes is not None:
+            raise ValueError(f"positions must be int32 [{self.n_axes}, {q.shape[0]}] with contiguous rows on {q.device}")
         raise ValueError(f"positions must be a contiguous int32 tensor of {q.shape[0]} entries on {q.device}")
 
     @staticmethod

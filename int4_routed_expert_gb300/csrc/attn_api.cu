@@ -111,6 +111,13 @@ extern "C" {
 
 moe_status_t moe_rope_create(int rot_dim, const double* inv_freq, float amplitude,
                              int interleaved, moe_rope_t** out) {
+  static const int32_t kFirst[128] = {};
+  return moe_rope_create_axes(rot_dim, inv_freq, amplitude, interleaved, 1, kFirst, out);
+}
+
+moe_status_t moe_rope_create_axes(int rot_dim, const double* inv_freq, float amplitude,
+                                  int interleaved, int n_axes, const int32_t* axis,
+                                  moe_rope_t** out) {
   if (!out) {
     fail(nullptr, "out is NULL");
     return MOE_ERR_INVALID_ARG;
@@ -133,6 +140,19 @@ moe_status_t moe_rope_create(int rot_dim, const double* inv_freq, float amplitud
       fail(nullptr, "inv_freq[%d] must be finite", i);
       return MOE_ERR_INVALID_ARG;
     }
+  if (n_axes < 1 || n_axes > 4) {
+    fail(nullptr, "n_axes must be in [1, 4], got %d", n_axes);
+    return MOE_ERR_UNSUPPORTED;
+  }
+  if (!axis) {
+    fail(nullptr, "axis is NULL");
+    return MOE_ERR_INVALID_ARG;
+  }
+  for (int i = 0; i < rot_dim / 2; ++i)
+    if (axis[i] < 0 || axis[i] >= n_axes) {
+      fail(nullptr, "axis[%d] must be in [0, %d), got %d", i, n_axes, axis[i]);
+      return MOE_ERR_INVALID_ARG;
+    }
   moe_rope_t* r = new (std::nothrow) moe_rope();
   if (!r) {
     fail(nullptr, "host allocation failed");
@@ -141,7 +161,9 @@ moe_status_t moe_rope_create(int rot_dim, const double* inv_freq, float amplitud
   r->rot_dim = rot_dim;
   r->amplitude = amplitude;
   r->interleaved = interleaved != 0;
+  r->n_axes = n_axes;
   for (int i = 0; i < rot_dim / 2; ++i) {
+    r->axis[i] = static_cast<uint8_t>(axis[i]);
     const uint64_t turn = turn_fraction(inv_freq[i]);
     r->inc[i] = inv_freq[i] < 0 ? 0 - turn : turn;
   }
@@ -154,48 +176,12 @@ void moe_rope_destroy(moe_rope_t* r) { delete r; }
 moe_status_t moe_rope_apply(const moe_rope_t* r, const moe_rope_tensor_t* q,
                             const moe_rope_tensor_t* k, int head_dim, moe_dtype_t dtype,
                             const int32_t* positions, int n_tokens, void* stream) {
-  if (!r || !q) {
-    fail(nullptr, "the rope handle or q is NULL");
-    return MOE_ERR_INVALID_ARG;
-  }
-  if (head_dim % 16 != 0 || head_dim < r->rot_dim || head_dim > 256) {
-    fail(nullptr, "head_dim must be a multiple of 16 in [%d, 256], got %d", r->rot_dim, head_dim);
-    return MOE_ERR_UNSUPPORTED;
-  }
-  if (const char* m = check_dtype(dtype)) {
-    fail(nullptr, "%s", m);
-    return MOE_ERR_INVALID_ARG;
-  }
-  if (n_tokens < 0) {
-    fail(nullptr, "n_tokens must be >= 0 (got %d)", n_tokens);
-    return MOE_ERR_INVALID_ARG;
-  }
-  const size_t esz = dtype == MOE_BF16 ? 2 : 4;
-  const moe_rope_tensor_t* in[2] = {q, k};
-  const char* names[2][4] = {{"q.x", "q.y", "q.x_stride", "q.y_stride"},
-                             {"k.x", "k.y", "k.x_stride", "k.y_stride"}};
   moe_rope_tensor_t t[2];
-  int device = -1;
-  for (int w = 0; w < 2; ++w) {
-    if (!in[w]) continue;
-    t[w] = *in[w];
-    if (t[w].n_heads < 1 || t[w].n_heads > 4096) {
-      fail(nullptr, "n_heads must be in [1, 4096], got %d", t[w].n_heads);
-      return MOE_ERR_UNSUPPORTED;
-    }
-    const int64_t row = static_cast<int64_t>(t[w].n_heads) * head_dim;
-    moe_status_t st = check_stride(nullptr, names[w][2], t[w].x_stride, row, esz);
-    if (st == MOE_OK) st = check_stride(nullptr, names[w][3], t[w].y_stride, row, esz);
-    if (st != MOE_OK) return st;
-    if (n_tokens == 0) continue;
-    if ((st = tensor(nullptr, &device, names[w][0], &t[w].x)) != MOE_OK) return st;
-    const void* y = t[w].y;
-    if ((st = tensor(nullptr, &device, names[w][1], &y)) != MOE_OK) return st;
-    t[w].y = const_cast<void*>(y);
-    if (t[w].x == t[w].y && t[w].x_stride != t[w].y_stride) {
-      fail(nullptr, "in place, %s and %s must be equal", names[w][2], names[w][3]);
-      return MOE_ERR_INVALID_ARG;
-    }
+  int device;
+  if (const moe_status_t st = rope_args(r, q, k, head_dim, dtype, n_tokens, t, device); st != MOE_OK) return st;
+  if (r->n_axes != 1) {
+    fail(nullptr, "the rope handle has %d axes: moe_rope_apply_axes", r->n_axes);
+    return MOE_ERR_INVALID_ARG;
   }
   if (n_tokens == 0) return MOE_OK;
   const void* pos = positions;

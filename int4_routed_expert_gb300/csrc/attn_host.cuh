@@ -24,7 +24,9 @@ struct moe_rope {
   int rot_dim;
   float amplitude;
   bool interleaved;
+  int n_axes;
   uint64_t inc[128];
+  uint8_t axis[128];  // of each pair
 };
 
 struct moe_kv : moe::HandleBase {
@@ -148,6 +150,54 @@ inline moe_status_t tensor(HandleBase* h, int* device, const char* name, const v
     return MOE_ERR_INVALID_ARG;
   }
   *p = r;
+  return MOE_OK;
+}
+
+// Checks a rotation's arguments: its tensors as the kernels address them, and their device.
+inline moe_status_t rope_args(const moe_rope_t* r, const moe_rope_tensor_t* q, const moe_rope_tensor_t* k, int head_dim,
+                              moe_dtype_t dtype, int n_tokens, moe_rope_tensor_t (&t)[2], int& device) {
+  if (!r || !q) {
+    fail(nullptr, "the rope handle or q is NULL");
+    return MOE_ERR_INVALID_ARG;
+  }
+  if (head_dim % 16 != 0 || head_dim < r->rot_dim || head_dim > 256) {
+    fail(nullptr, "head_dim must be a multiple of 16 in [%d, 256], got %d", r->rot_dim, head_dim);
+    return MOE_ERR_UNSUPPORTED;
+  }
+  if (const char* m = check_dtype(dtype)) {
+    fail(nullptr, "%s", m);
+    return MOE_ERR_INVALID_ARG;
+  }
+  if (n_tokens < 0) {
+    fail(nullptr, "n_tokens must be >= 0 (got %d)", n_tokens);
+    return MOE_ERR_INVALID_ARG;
+  }
+  const size_t esz = dtype == MOE_BF16 ? 2 : 4;
+  const moe_rope_tensor_t* in[2] = {q, k};
+  const char* names[2][4] = {{"q.x", "q.y", "q.x_stride", "q.y_stride"},
+                             {"k.x", "k.y", "k.x_stride", "k.y_stride"}};
+  device = -1;
+  for (int w = 0; w < 2; ++w) {
+    if (!in[w]) continue;
+    t[w] = *in[w];
+    if (t[w].n_heads < 1 || t[w].n_heads > 4096) {
+      fail(nullptr, "n_heads must be in [1, 4096], got %d", t[w].n_heads);
+      return MOE_ERR_UNSUPPORTED;
+    }
+    const int64_t row = static_cast<int64_t>(t[w].n_heads) * head_dim;
+    moe_status_t st = check_stride(nullptr, names[w][2], t[w].x_stride, row, esz);
+    if (st == MOE_OK) st = check_stride(nullptr, names[w][3], t[w].y_stride, row, esz);
+    if (st != MOE_OK) return st;
+    if (n_tokens == 0) continue;
+    if ((st = tensor(nullptr, &device, names[w][0], &t[w].x)) != MOE_OK) return st;
+    const void* y = t[w].y;
+    if ((st = tensor(nullptr, &device, names[w][1], &y)) != MOE_OK) return st;
+    t[w].y = const_cast<void*>(y);
+    if (t[w].x == t[w].y && t[w].x_stride != t[w].y_stride) {
+      fail(nullptr, "in place, %s and %s must be equal", names[w][2], names[w][3]);
+      return MOE_ERR_INVALID_ARG;
+    }
+  }
   return MOE_OK;
 }
 

@@ -85,6 +85,9 @@ struct AttnArgs {
 cudaError_t rope_launch(const uint64_t* inc, int rot_dim, float amplitude, bool interleaved,
                         const moe_rope_tensor_t* q, const moe_rope_tensor_t* k, int head_dim,
                         moe_dtype_t dt, const int32_t* pos, int T, cudaStream_t s);
+cudaError_t rope_axes_launch(const uint64_t* inc, const uint8_t* axis, int rot_dim, float amplitude, bool interleaved,
+                             const moe_rope_tensor_t* q, const moe_rope_tensor_t* k, int head_dim, moe_dtype_t dt,
+                             const int32_t* pos, int64_t pos_stride, int T, cudaStream_t s);
 cudaError_t kv_write_launch(const KvView& c, const void* k, int64_t ks, const void* v, int64_t vs,
                             moe_dtype_t dt, cudaStream_t s);
 cudaError_t kv_read_launch(const KvView& c, void* k, void* v, moe_dtype_t dt, cudaStream_t s);

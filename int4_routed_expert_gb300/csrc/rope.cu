@@ -25,9 +25,11 @@ struct RopeParams {
   const void* y[2];
   int64_t xs[2], ys[2];
   const int32_t* pos;
+  int64_t pos_stride;  // between axes
   float amplitude;
   int heads[2];
   int rot, head_dim, T, tokens;
+  uint8_t axis[128];
 };
 
 // 8 elements as they lie, and as fp32
@@ -77,15 +79,16 @@ struct Raw {
   }
 };
 
-template <typename T, bool INTERLEAVED>
+template <typename T, bool INTERLEAVED, bool AXES>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams P) {
   __shared__ float2 cs[kTokens][128];  // cosine, sine
   const int half = P.rot >> 1;
   const int t0 = blockIdx.x * P.tokens, tn = min(P.tokens, P.T - t0);
   for (int i = threadIdx.x; i < tn * half; i += blockDim.x) {
     const int tk = i / half, pair = i - tk * half;
-    const uint64_t phase =
-        static_cast<uint64_t>(static_cast<int64_t>(__ldg(P.pos + t0 + tk))) * P.inc[pair];
+    const int32_t* pos = P.pos + t0 + tk;
+    if constexpr (AXES) pos += P.axis[pair] * P.pos_stride;
+    const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(__ldg(pos))) * P.inc[pair];
     const uint32_t turn = static_cast<uint32_t>((phase + 0x80000000u) >> 32);  // in 2^-32 turns
     const uint32_t quarter = (turn + 0x20000000u) >> 30;
     const int32_t rest = static_cast<int32_t>(turn - (quarter << 30));  // [-2^29, 2^29)
@@ -153,13 +156,15 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   }
 }
 
-}  // namespace
-
-cudaError_t rope_launch(const uint64_t* inc, int rot_dim, float amplitude, bool interleaved,
-                        const moe_rope_tensor_t* q, const moe_rope_tensor_t* k, int head_dim,
-                        moe_dtype_t dt, const int32_t* pos, int T, cudaStream_t s) {
+template <bool AXES>
+cudaError_t launch(const uint64_t* inc, const uint8_t* axis, int rot_dim, float amplitude, bool interleaved,
+                   const moe_rope_tensor_t* q, const moe_rope_tensor_t* k, int head_dim, moe_dtype_t dt, const int32_t* pos,
+                   int64_t pos_stride, int T, cudaStream_t s) {
   RopeParams P;
-  for (int i = 0; i < 128; ++i) P.inc[i] = i < rot_dim / 2 ? inc[i] : 0;
+  for (int i = 0; i < 128; ++i) {
+    P.inc[i] = i < rot_dim / 2 ? inc[i] : 0;
+    P.axis[i] = axis && i < rot_dim / 2 ? axis[i] : 0;
+  }
   const moe_rope_tensor_t* ts[2] = {q, k};
   for (int w = 0; w < 2; ++w) {
     P.x[w] = ts[w] ? ts[w]->x : nullptr;
@@ -169,6 +174,7 @@ cudaError_t rope_launch(const uint64_t* inc, int rot_dim, float amplitude, bool 
     P.heads[w] = ts[w] ? ts[w]->n_heads : 0;
   }
   P.pos = pos;
+  P.pos_stride = pos_stride;
   P.amplitude = amplitude;
   P.rot = rot_dim;
   P.head_dim = head_dim;
@@ -180,16 +186,30 @@ cudaError_t rope_launch(const uint64_t* inc, int rot_dim, float amplitude, bool 
   const int grid = (T + P.tokens - 1) / P.tokens;
   if (dt == MOE_BF16) {
     if (interleaved)
-      rope_kernel<__nv_bfloat16, true><<<grid, threads, 0, s>>>(P);
+      rope_kernel<__nv_bfloat16, true, AXES><<<grid, threads, 0, s>>>(P);
     else
-      rope_kernel<__nv_bfloat16, false><<<grid, threads, 0, s>>>(P);
+      rope_kernel<__nv_bfloat16, false, AXES><<<grid, threads, 0, s>>>(P);
   } else {
     if (interleaved)
-      rope_kernel<float, true><<<grid, threads, 0, s>>>(P);
+      rope_kernel<float, true, AXES><<<grid, threads, 0, s>>>(P);
     else
-      rope_kernel<float, false><<<grid, threads, 0, s>>>(P);
+      rope_kernel<float, false, AXES><<<grid, threads, 0, s>>>(P);
   }
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t rope_launch(const uint64_t* inc, int rot_dim, float amplitude, bool interleaved,
+                        const moe_rope_tensor_t* q, const moe_rope_tensor_t* k, int head_dim,
+                        moe_dtype_t dt, const int32_t* pos, int T, cudaStream_t s) {
+  return launch<false>(inc, nullptr, rot_dim, amplitude, interleaved, q, k, head_dim, dt, pos, 0, T, s);
+}
+
+cudaError_t rope_axes_launch(const uint64_t* inc, const uint8_t* axis, int rot_dim, float amplitude, bool interleaved,
+                             const moe_rope_tensor_t* q, const moe_rope_tensor_t* k, int head_dim, moe_dtype_t dt,
+                             const int32_t* pos, int64_t pos_stride, int T, cudaStream_t s) {
+  return launch<true>(inc, axis, rot_dim, amplitude, interleaved, q, k, head_dim, dt, pos, pos_stride, T, s);
 }
 
 }  // namespace moe
