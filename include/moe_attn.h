@@ -4,8 +4,8 @@
  * positions, a paged key/value cache held in 8 bits with a scale for each
  * block of tokens and head, and attention over that cache, for prompts and
  * for single tokens, with an optional sliding window and first tokens that
- * stay visible.  Part of libmoe.so; which sequence has which pages is the
- * caller's to say, or moe_pages.h's.
+ * stay visible, or for sequences that share a prefix.  Part of libmoe.so; which
+ * sequence has which pages is the caller's to say, or moe_pages.h's.
  *
  * Conventions are those of moe.h: device pointers (16-byte aligned) owned by
  * the caller, work enqueued on `stream` (cudaStream_t as void*) without
@@ -201,6 +201,39 @@ typedef struct {
 } moe_kv_mask_t;
 moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* out, float* lse,
                            const moe_kv_mask_t* mask, const moe_kv_batch_t* batch, void* stream);
+
+/* The same for sequences that share a prefix, whose keys and values are read once for
+ * all of them.  Group g holds the batch's sequences cu_seq[g] .. cu_seq[g+1] - 1; their
+ * tokens 0 .. prefix_len[g] - 1 are those of row g of the prefix's own page_table (the
+ * entries of the batch's table for pages that end within the prefix are not looked at).
+ * A sequence takes part when its new tokens all lie behind the prefix (kv_len - number
+ * of new tokens >= prefix_len); another one, and one that no group holds, has all of its
+ * tokens by its own table, as in moe_kv_attend.  The arrays live on the device; the host
+ * gives bounds: max_group_tokens new tokens of any group (their rows are those from its
+ * first sequence's to its last one's), max_prefix_len tokens of any prefix.  A group whose
+ * arrays break them (cu_seq not ascending within [0, n_seqs], a length outside
+ * [0, max_prefix_len], a needed page id outside [0, n_pages)) sets bit 1 of
+ * moe_kv_device_status, and its rows are not valid.  With mask->causal == 0 the rows see
+ * all of the prefix and of their own tokens.  window and sinks are not supported: the rows
+ * of windowed layers do not see the whole prefix.
+ * workspace: device memory of at least moe_kv_shared_workspace_bytes (0 when the arguments
+ * are not valid), used until the call has run; it needs no preparation and keeps nothing.
+ * n_groups: 0 (which makes moe_kv_attend of it) to 65535. */
+typedef struct {
+  int n_groups;
+  int max_group_tokens;
+  int max_prefix_len;
+  int table_stride;          /* entries of a row of page_table */
+  const int32_t* cu_seq;     /* [n_groups + 1] */
+  const int32_t* prefix_len; /* [n_groups] */
+  const int32_t* page_table; /* [n_groups][table_stride] */
+} moe_kv_prefix_t;
+size_t moe_kv_shared_workspace_bytes(const moe_kv_t* h, const moe_kv_batch_t* batch,
+                                     const moe_kv_prefix_t* prefix);
+moe_status_t moe_kv_attend_shared(moe_kv_t* h, const void* q, int64_t q_stride, void* out,
+                                  float* lse, const moe_kv_mask_t* mask,
+                                  const moe_kv_batch_t* batch, const moe_kv_prefix_t* prefix,
+                                  void* workspace, size_t workspace_bytes, void* stream);
 
 /* Copies the handle's device error word to *flags (synchronous) and clears it;
  * MOE_ERR_CUDA when it was not 0.  Bit 0: a bounded wait gave up (the call's

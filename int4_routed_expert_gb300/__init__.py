@@ -11,6 +11,7 @@ from .attn import (  # noqa: F401
     KVCache,
     Rope,
     SeqBatch,
+    SharedPrefix,
     rope_axes,
     rope_frequencies,
 )

@@ -42,9 +42,15 @@ class moe_kv_mask_t(C.Structure):
     _fields_ = [("scale", C.c_float), ("causal", C.c_int), ("window", C.c_int), ("sinks", C.c_int)]
 
 
+class moe_kv_prefix_t(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("n_groups", "max_group_tokens", "max_prefix_len", "table_stride")] + \
+               [(n, C.c_void_p) for n in ("cu_seq", "prefix_len", "page_table")]
+
+
 EXPORTED = ("moe_rope_create", "moe_rope_create_axes", "moe_rope_apply", "moe_rope_apply_axes", "moe_rope_destroy",
             "moe_kv_create", "moe_kv_workspace_bytes", "moe_kv_last_error", "moe_kv_destroy", "moe_kv_write",
-            "moe_kv_read", "moe_kv_copy", "moe_kv_attend", "moe_kv_device_status")
+            "moe_kv_read", "moe_kv_copy", "moe_kv_attend", "moe_kv_shared_workspace_bytes", "moe_kv_attend_shared",
+            "moe_kv_device_status")
 
 # bits of moe_kv_device_status
 KV_WAIT_GAVE_UP, KV_BAD_BATCH, KV_NON_FINITE = 1, 2, 4
@@ -78,6 +84,9 @@ def _load() -> C.CDLL:
         "moe_kv_read": (i32, [vp, vp, vp, i32, C.POINTER(moe_kv_batch_t), vp]),
         "moe_kv_copy": (i32, [vp, vp, i32, vp]),
         "moe_kv_attend": (i32, [vp, vp, i64, vp, vp, C.POINTER(moe_kv_mask_t), C.POINTER(moe_kv_batch_t), vp]),
+        "moe_kv_shared_workspace_bytes": (C.c_size_t, [vp, C.POINTER(moe_kv_batch_t), C.POINTER(moe_kv_prefix_t)]),
+        "moe_kv_attend_shared": (i32, [vp, vp, i64, vp, vp, C.POINTER(moe_kv_mask_t), C.POINTER(moe_kv_batch_t),
+                                       C.POINTER(moe_kv_prefix_t), vp, C.c_size_t, vp]),
         "moe_kv_device_status": (i32, [vp, C.POINTER(C.c_int32)]),
     }
     for name, (res, args) in sig.items():
@@ -340,6 +349,26 @@ class SeqBatch:
                                 kv_len.data_ptr(), page_table.data_ptr())
 
 
+class SharedPrefix:
+    """Prefixes that sequences of a batch share (KVCache.attend): group g holds sequences cu_seq[g] .. cu_seq[g + 1] - 1,
+    whose first prefix_len[g] tokens lie in the pages page_table[g].  Sequences whose new tokens do not all lie behind
+    the prefix have their tokens by the batch's table alone.  The three int32 tensors stay on the device, as a
+    SeqBatch's; the host's bounds: max_group_tokens new tokens of any group, max_prefix_len tokens of any prefix."""
+
+    def __init__(self, cu_seq, prefix_len, page_table, max_group_tokens: int, max_prefix_len: int):
+        _load()
+        for name, t, dims in (("cu_seq", cu_seq, 1), ("prefix_len", prefix_len, 1), ("page_table", page_table, 2)):
+            if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous() or t.device != cu_seq.device:
+                raise ValueError(f"{name} must be a contiguous {dims}-D int32 tensor on {cu_seq.device}")
+        n = prefix_len.shape[0]
+        if cu_seq.shape[0] != n + 1 or page_table.shape[0] != n:
+            raise ValueError(f"{n} groups need cu_seq of {n + 1} entries and page_table of {n} rows")
+        self.cu_seq, self.prefix_len, self.page_table = cu_seq, prefix_len, page_table
+        self.device, self.index = cu_seq.device, cu_seq.get_device()
+        self.c = moe_kv_prefix_t(n, max_group_tokens, max_prefix_len, page_table.shape[1], cu_seq.data_ptr(),
+                                 prefix_len.data_ptr(), page_table.data_ptr())
+
+
 class KVCache:
     """The 8-bit paged cache (moe_kv_*): wraps codes [pages, kv heads, page_size, head_dim] (torch.float8_e4m3fn
     or uint8) and scales [pages, kv heads] fp32 of keys and values; ``KVCache.empty`` allocates them."""
@@ -363,6 +392,7 @@ class KVCache:
         self.device = k_codes.device
         self._index = k_codes.get_device()
         self._row = {}  # checked layouts of the calls' tensors: (name, shape, stride) -> elements between tokens
+        self._shared = {}  # workspace bytes of calls with a prefix, by their bounds
         self.default_scale = D ** -0.5
         cfg = moe_kv_config_t(n_q_heads, H, D, S, P, max_seqs, max_tokens, max_kv_len)
         store = moe_kv_store_t(*(t.data_ptr() for t in (k_codes, v_codes, k_scale, v_scale)))
@@ -437,11 +467,12 @@ class KVCache:
         self._check(_lib.moe_kv_copy(self.h, moves.data_ptr(), moves.shape[0], _stream(stream, self._index)))
 
     def attend(self, q, batch: SeqBatch, out=None, lse=None, scale: float | None = None, causal: bool = True,
-               window: int = 0, sinks: int = 0, stream=None):
+               window: int = 0, sinks: int = 0, stream=None, prefix: SharedPrefix | None = None):
         """Attention of the batch's new tokens q [tokens, q heads, head_dim] bf16 over their sequences' cached
         tokens (write the new ones first).  window > 0: a token sees the last ``window`` tokens, itself
         included, and the first ``sinks`` ones.  Returns out [tokens, q heads, head_dim] bf16; lse, when given,
-        is filled with the natural logarithms of the softmax denominators [tokens, q heads] fp32."""
+        is filled with the natural logarithms of the softmax denominators [tokens, q heads] fp32.  prefix: tokens that
+        sequences share, read once for all of them (not with a window)."""
         dev, H = self.device, self.n_q_heads
         qs = self._tokens(q, "q", H, batch)
         bf16 = torch.bfloat16
@@ -458,9 +489,29 @@ class KVCache:
                                 or lse.device != dev):
             raise ValueError(f"lse must be a contiguous fp32 tensor {shape[:2]} on {dev}")
         mask = moe_kv_mask_t(self.default_scale if scale is None else scale, 1 if causal else 0, window, sinks)
+        if prefix is not None:
+            return self._attend_shared(q, qs, out, lse, mask, batch, prefix, stream)
         self._check(_lib.moe_kv_attend(self.h, q.data_ptr(), qs, out.data_ptr(),
                                        lse.data_ptr() if lse is not None else None, mask, batch.c,
                                        _stream(stream, self._index)))
+        return out
+
+    def _attend_shared(self, q, qs, out, lse, mask, batch, prefix, stream):
+        if prefix.index != self._index:
+            raise ValueError(f"the prefix must be on {self.device}, got {prefix.device}")
+        b, p = batch.c, prefix.c
+        key = (b.n_seqs, b.n_tokens, b.max_q_len, b.max_kv_len, p.n_groups, p.max_group_tokens, p.max_prefix_len)
+        size = self._shared.get(key)
+        if size is None:
+            size = _lib.moe_kv_shared_workspace_bytes(self.h, b, p)
+            if len(self._shared) >= 64:
+                self._shared.clear()
+            self._shared[key] = size
+        # the call's own memory, of its stream: nothing else uses it while the call runs, nor in a graph
+        room = _results((max(size, 16),), torch.uint8, self.device, stream)
+        self._check(_lib.moe_kv_attend_shared(self.h, q.data_ptr(), qs, out.data_ptr(),
+                                              lse.data_ptr() if lse is not None else None, mask, b, p, room.data_ptr(),
+                                              size, _stream(stream, self._index)))
         return out
 
     def device_status(self) -> int:

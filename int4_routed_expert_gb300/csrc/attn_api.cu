@@ -349,49 +349,10 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
     fail(nullptr, "the cache handle is NULL");
     return MOE_ERR_INVALID_ARG;
   }
-  if (!mask) {
-    fail(h, "mask is NULL");
-    return MOE_ERR_INVALID_ARG;
-  }
-  const float scale_log2 = mask->scale * 1.4426950408889634f;
-  if (!isfinite(scale_log2)) {
-    fail(h, "scale must be finite, in base 2 too");
-    return MOE_ERR_INVALID_ARG;
-  }
-  if (mask->window < 0 || mask->sinks < 0) {
-    fail(h, "window and sinks must not be negative (got %d, %d)", mask->window, mask->sinks);
-    return MOE_ERR_INVALID_ARG;
-  }
-  if (!mask->causal && (mask->window || mask->sinks)) {
-    fail(h, "window and sinks need causal != 0");
-    return MOE_ERR_INVALID_ARG;
-  }
-  moe::KvView c{};
-  moe_status_t st = view(h, batch, &c);
+  KvView c{};
+  AttnArgs a{};
+  const moe_status_t st = attend_args(h, q, q_stride, out, lse, mask, batch, &c, &a);
   if (st != MOE_OK || c.n_seqs == 0) return st;
-  if (static_cast<int64_t>(c.n_tokens) * h->cfg.n_q_heads > INT_MAX) {  // the kernels number rows in 32 bits
-    fail(h, "%d tokens of %d query heads are more rows than one call takes", c.n_tokens, h->cfg.n_q_heads);
-    return MOE_ERR_UNSUPPORTED;
-  }
-  const int64_t row = static_cast<int64_t>(h->cfg.n_q_heads) * h->cfg.head_dim;
-  if ((st = check_stride(h, "q_stride", q_stride, row, 2)) != MOE_OK) return st;
-  const void *o = out, *z = lse;
-  if ((st = tensor(h, &h->device, "q", &q)) != MOE_OK) return st;
-  if ((st = tensor(h, &h->device, "out", &o)) != MOE_OK) return st;
-  if (lse && (st = tensor(h, &h->device, "lse", &z)) != MOE_OK) return st;
-  moe::AttnArgs a{};
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.q_stride = q_stride;
-  a.out = static_cast<__nv_bfloat16*>(const_cast<void*>(o));
-  a.lse = static_cast<float*>(const_cast<void*>(z));
-  a.scale_log2 = scale_log2;
-  a.causal = mask->causal != 0;
-  // a window that reaches every cached token is none
-  a.window = mask->window >= c.max_kv ? 0 : mask->window;
-  a.sinks = a.window ? mask->sinks : 0;
-  a.hq = h->cfg.n_q_heads;
-  a.G = h->cfg.n_q_heads / h->cfg.n_kv_heads;
-  a.inv_g = 1.f / static_cast<float>(a.G);
   // Rows of a kv head, up to 32: keys as the products' M dimension; more: rows as
   // M.  At 32 rows the first kernel takes 90 us and the second 101 us (16 x 16384
   // keys, 4 kv heads), at 16 rows 103 and 175 us (8 kv heads), at 8 rows 208 and

@@ -56,10 +56,10 @@ struct RowSees {
     return n >= 32 ? 0xffffffffu : (1u << max(n, 0)) - 1u;
   }
 };
-__device__ __forceinline__ RowSees row_sees(const AttnArgs& a, int L, int p, bool live) {
+__device__ __forceinline__ RowSees row_sees(const AttnArgs& a, int L, int p, bool live, int begin = 0) {
   RowSees r;
   r.hi = !live ? -1 : a.causal ? p : L - 1;
-  r.lo = live && a.window ? p - a.window + 1 : 0;
+  r.lo = live && a.window ? p - a.window + 1 : begin;
   r.sinks = a.sinks;
   return r;
 }

@@ -60,7 +60,7 @@ constexpr int max_splits(int n) { return 4096 / n; }
 template <int D, int N>
 struct Lay {
   static constexpr int kStages = N == 16 ? 3 : 2;  // of key codes and of value codes
-  static constexpr int kCtas = 2;                        // a SM
+  static constexpr int kCtas = 2;                        // a SM (as attn_few_plan counts)
   using Io = TileIo<D, kStages, kStages, 0>;
   static constexpr int kGroups = N / 16;  // softmax groups of 128 threads
   static constexpr int kThreads = 128 * kGroups + 64;
@@ -183,9 +183,9 @@ __device__ __forceinline__ bool mbar_wait2(uint32_t b0, uint32_t p0, uint32_t b1
   return ok != 0 || (mbar_wait(b0, p0, err) && mbar_wait(b1, p1, err));
 }
 
-template <int D, int N>
+template <int D, int N, Part PART>
 __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
-    attn_few_kernel(const KvView c, const AttnArgs a, const AttnWs ws, const Plan pl,
+    attn_few_kernel(const KvView c, const AttnArgs a, const AttnWs ws, const Plan pl, const Share sh,
                     const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
   using L_ = Lay<D, N>;
   using Io = typename L_::Io;
@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
   const uint32_t base_u = smem_u32(smem);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
+  if constexpr (PART != Part::kAll) pdl_launch_dependents();
   int idx = blockIdx.x;
   const int hk = idx % c.hkv;
   idx /= c.hkv;
@@ -203,9 +204,12 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
   idx /= pl.row_tiles;
   const int b = idx % c.n_seqs, split = idx / c.n_seqs;
   Work w;
-  if (!work_of<N>(c, a, pl, b, hk, rt, w) || split >= w.n_split) return;
-  const int t_begin = split * pl.tiles_per_split;
-  const int n = min(w.k.n_t, t_begin + pl.tiles_per_split) - t_begin;  // 0 when the rows see nothing
+  if (!work_of<PART>(c, a, pl, sh, N, b, hk, rt, w) || split >= w.n_split) {
+    end_of_part<PART>();
+    return;
+  }
+  const int t_begin = split * w.tiles_per_split;
+  const int n = min(w.k.n_t, t_begin + w.tiles_per_split) - t_begin;  // 0 when the rows see nothing
 
   auto bar = [&](int i) { return base_u + L_::kBar + 8 * i; };
   if (threadIdx.x == 0) {
@@ -315,7 +319,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
         *reinterpret_cast<uint2*>(dst + k_off<D>(N + r, byte >> 4)) = make_uint2(t1[0], t1[1]);
       }
       if (part == 0) {
-        const RowSees s = row_sees(a, w.q.L, w.base_p + tok, live);
+        const RowSees s = row_sees(a, w.q.L, w.base_p + tok, live, PART == Part::kOwn ? w.k.lo : 0);
         rows.lscale[r] = fmaxf(a.scale_log2 / f, kTiny);
         rows.nref[r] = 0.f;
         rows.m[r] = -INFINITY;
@@ -345,7 +349,8 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
       const float ks = fmaxf(cn.x, kTiny);
       const int tok = w.k.base(t_begin + j) + t, key0 = tok - t;
       const bool whole = (a.causal ? key0 + kKeys <= p_lo + 1 : key0 + kKeys <= w.q.L) &&
-                         (a.window == 0 || key0 > p_hi - a.window || key0 + kKeys <= a.sinks);
+                         (a.window == 0 || key0 > p_hi - a.window || key0 + kKeys <= a.sinks) &&
+                         (PART != Part::kOwn || key0 >= w.k.lo);
       // exponents relative to the rows' references
       float top = -INFINITY;
       tmem_wait_ld16f(z);
@@ -490,14 +495,16 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
     }
     named_sync(1 + grp, 128);
     const int live = w.r1 - w.r0;
-    const size_t prow = (((static_cast<size_t>(b) * c.hkv + hk) * pl.row_tiles + rt) * pl.splits + split) * N;
+    const size_t prow = PART == Part::kAll
+                            ? (((static_cast<size_t>(b) * c.hkv + hk) * pl.row_tiles + rt) * pl.splits + split) * N
+                            : part_row(c, a, w, split);
     if (t < NG && g0 + t < live) {
       const int row = g0 + t;
       const float ll = (red[row] + red[N + row]) + (red[2 * N + row] + red[3 * N + row]);
       const float mm = rows.m[row] + (kLift - kFewLift);  // as the other kernel counts
       const bool any = ll > 0.f || ll != ll;
       rows.f[row] = any ? 1.f / ll : 0.f;
-      if (w.n_split > 1)
+      if (PART != Part::kAll || w.n_split > 1)
         ws.ml[prow + row] = make_float2(mm, ll);
       else if (a.lse)
         a.lse[rows.out[row]] = any ? (mm - kLift + log2f(ll)) * 0.693147180559945f : -INFINITY;
@@ -507,18 +514,22 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
     for (int r = 0; r < NG; ++r) {
       const int row = g0 + r;
       if (row < live && t < D) {
-        if (w.n_split == 1)
+        if (PART == Part::kAll && w.n_split == 1)
           a.out[static_cast<size_t>(rows.out[row]) * D + t] = __float2bfloat16_rn(o[r] * rows.f[row]);
         else
           ws.o[(prow + row) * D + t] = o[r];
       }
     }
-    if (w.n_split > 1) __threadfence();
+    if (PART == Part::kAll && w.n_split > 1) __threadfence();
   }
   __syncwarp();
   fence_before_sync();
   __syncthreads();
   if (warp == kMma) tmem_dealloc(tmem, L_::kTmem);
+  if constexpr (PART != Part::kAll) {
+    end_of_part<PART>();
+    return;
+  }
   if (w.n_split == 1) return;
 
   // the last CTA of the tile to arrive joins the splits, in their order
@@ -614,27 +625,22 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
       finish_row<D>(a, rows.out[of[k]], el[k] % (D / 4), v[k], rows.m[of[k]], rows.f[of[k]]);
 }
 
+template <int D, int N, Part PART>
+cudaError_t launch_part(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,
+                        const KvMaps& maps, cudaStream_t s) {
+  static std::atomic<size_t> done[kMaxDevices];
+  const void* fn = reinterpret_cast<const void*>(attn_few_kernel<D, N, PART>);
+  if (const cudaError_t e = opt_in_smem(fn, done, Lay<D, N>::kSmem); e != cudaSuccess) return e;
+  const int64_t grid = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs * pl.splits;
+  if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+  return launch_kernel(attn_few_kernel<D, N, PART>, grid, Lay<D, N>::kThreads, Lay<D, N>::kSmem, s, PART == Part::kOwn,
+                       c, a, ws, pl, sh, maps.k_tile, maps.v_tile);
+}
+
 template <int D, int N>
 cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const KvMaps& maps, int n_sm, cudaStream_t s) {
-  static std::atomic<size_t> done[kMaxDevices];
-  const void* fn = reinterpret_cast<const void*>(attn_few_kernel<D, N>);
-  if (const cudaError_t e = opt_in_smem(fn, done, Lay<D, N>::kSmem); e != cudaSuccess) return e;
-  Plan pl;
-  const int64_t rows = static_cast<int64_t>(c.max_q) * a.G;
-  pl.row_tiles = static_cast<int>((rows + N - 1) / N);
-  const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
-  const int64_t tiles = max_key_tiles(c, a, N, kKeys);
-  // (32 rows of 8000 keys and 8 kv heads of 128, splits of 8, 4 and 2 tiles:
-  // 27.3, 23.3 and 27.2 us)
-  const int64_t most = std::min<int64_t>(static_cast<int64_t>(ws.cap_rows) / (base * N), max_splits(N));
-  const int64_t splits = best_splits(base, n_sm, tiles, most, c.n_seqs > 1, {Lay<D, N>::kCtas, 3., 0.25});
-  pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
-  pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
-  const int64_t grid = base * pl.splits;
-  if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  attn_few_kernel<D, N><<<static_cast<unsigned>(grid), Lay<D, N>::kThreads, Lay<D, N>::kSmem, s>>>(c, a, ws, pl,
-                                                                                                     maps.k_tile, maps.v_tile);
-  return cudaGetLastError();
+  const Plan pl = attn_few_plan(c, a.G, max_key_tiles(c, a, N, kKeys), static_cast<int64_t>(ws.cap_rows), 0, n_sm);
+  return launch_part<D, N, Part::kAll>(c, a, ws, pl, Share{}, maps, s);
 }
 
 }  // namespace
@@ -647,6 +653,35 @@ cudaError_t attn_few_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws
   if (c.D == 128)
     return (rows <= 16 ? launch<128, 16> : launch<128, 32>)(c, a, ws, maps, n_sm, s);
   return (rows <= 16 ? launch<64, 16> : launch<64, 32>)(c, a, ws, maps, n_sm, s);
+}
+
+Plan attn_few_plan(const KvView& c, int G, int64_t tiles, int64_t cap_rows, int64_t split_rows, int n_sm) {
+  const int64_t rows = static_cast<int64_t>(c.max_q) * G;
+  const int n = rows <= 16 ? 16 : 32;
+  Plan pl;
+  pl.row_tiles = static_cast<int>((rows + n - 1) / n);
+  const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
+  // (32 rows of 8000 keys and 8 kv heads of 128, splits of 8, 4 and 2 tiles:
+  // 27.3, 23.3 and 27.2 us)
+  const int64_t splits =
+      best_splits(base, n_sm, tiles, std::min<int64_t>(cap_rows / (split_rows ? split_rows : base * n), max_splits(n)),
+                  c.n_seqs > 1, {2, 3., 0.25});
+  pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
+  pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
+  return pl;
+}
+
+cudaError_t attn_few_part_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,
+                                 bool prefix, const KvMaps& maps, cudaStream_t s) {
+  const bool n16 = static_cast<int64_t>(c.max_q) * a.G <= 16;
+  if (c.D == 128) {
+    if (prefix)
+      return (n16 ? launch_part<128, 16, Part::kPrefix> : launch_part<128, 32, Part::kPrefix>)(c, a, ws, pl, sh, maps, s);
+    return (n16 ? launch_part<128, 16, Part::kOwn> : launch_part<128, 32, Part::kOwn>)(c, a, ws, pl, sh, maps, s);
+  }
+  if (prefix)
+    return (n16 ? launch_part<64, 16, Part::kPrefix> : launch_part<64, 32, Part::kPrefix>)(c, a, ws, pl, sh, maps, s);
+  return (n16 ? launch_part<64, 16, Part::kOwn> : launch_part<64, 32, Part::kOwn>)(c, a, ws, pl, sh, maps, s);
 }
 
 }  // namespace moe

@@ -201,6 +201,56 @@ inline moe_status_t rope_args(const moe_rope_t* r, const moe_rope_tensor_t* q, c
   return MOE_OK;
 }
 
+// Checks attention's arguments; fills the kernels' view of the batch (n_seqs is 0 where
+// there is nothing to do) and their arguments.
+inline moe_status_t attend_args(moe_kv_t* h, const void* q, int64_t q_stride, void* out, float* lse,
+                                const moe_kv_mask_t* mask, const moe_kv_batch_t* batch, KvView* view_out, AttnArgs* args) {
+  if (!mask) {
+    fail(h, "mask is NULL");
+    return MOE_ERR_INVALID_ARG;
+  }
+  const float scale_log2 = mask->scale * 1.4426950408889634f;
+  if (!isfinite(scale_log2)) {
+    fail(h, "scale must be finite, in base 2 too");
+    return MOE_ERR_INVALID_ARG;
+  }
+  if (mask->window < 0 || mask->sinks < 0) {
+    fail(h, "window and sinks must not be negative (got %d, %d)", mask->window, mask->sinks);
+    return MOE_ERR_INVALID_ARG;
+  }
+  if (!mask->causal && (mask->window || mask->sinks)) {
+    fail(h, "window and sinks need causal != 0");
+    return MOE_ERR_INVALID_ARG;
+  }
+  moe_status_t st = view(h, batch, view_out);
+  const KvView& c = *view_out;
+  if (st != MOE_OK || c.n_seqs == 0) return st;
+  if (static_cast<int64_t>(c.n_tokens) * h->cfg.n_q_heads > INT_MAX) {  // the kernels number rows in 32 bits
+    fail(h, "%d tokens of %d query heads are more rows than one call takes", c.n_tokens, h->cfg.n_q_heads);
+    return MOE_ERR_UNSUPPORTED;
+  }
+  const int64_t row = static_cast<int64_t>(h->cfg.n_q_heads) * h->cfg.head_dim;
+  if ((st = check_stride(h, "q_stride", q_stride, row, 2)) != MOE_OK) return st;
+  const void *o = out, *z = lse;
+  if ((st = tensor(h, &h->device, "q", &q)) != MOE_OK) return st;
+  if ((st = tensor(h, &h->device, "out", &o)) != MOE_OK) return st;
+  if (lse && (st = tensor(h, &h->device, "lse", &z)) != MOE_OK) return st;
+  AttnArgs& a = *args;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.q_stride = q_stride;
+  a.out = static_cast<__nv_bfloat16*>(const_cast<void*>(o));
+  a.lse = static_cast<float*>(const_cast<void*>(z));
+  a.scale_log2 = scale_log2;
+  a.causal = mask->causal != 0;
+  // a window that reaches every cached token is none
+  a.window = mask->window >= c.max_kv ? 0 : mask->window;
+  a.sinks = a.window ? mask->sinks : 0;
+  a.hq = h->cfg.n_q_heads;
+  a.G = h->cfg.n_q_heads / h->cfg.n_kv_heads;
+  a.inv_g = 1.f / static_cast<float>(a.G);
+  return MOE_OK;
+}
+
 // Makes a device current while a call works on it, and the caller's again.  A
 // launch (and the stream NULL) goes to the current device, which need not be the
 // one whose memory the call was given.

@@ -82,6 +82,15 @@ struct AttnArgs {
   float inv_g;    // 1 / G
 };
 
+// Groups of a batch's sequences that share a prefix (moe_kv_prefix_t).
+struct Share {
+  const int32_t* cu_seq;
+  const int32_t* prefix_len;
+  const int32_t* table;
+  int table_stride, n_groups, max_tokens, max_len;
+  int n_seqs;  // of the batch
+};
+
 cudaError_t rope_launch(const uint64_t* inc, int rot_dim, float amplitude, bool interleaved,
                         const moe_rope_tensor_t* q, const moe_rope_tensor_t* k, int head_dim,
                         moe_dtype_t dt, const int32_t* pos, int T, cudaStream_t s);
@@ -99,6 +108,11 @@ struct KvMaps {
 bool kv_create_maps(const moe_kv_config_t& cfg, const moe_kv_store_t& st, KvMaps* m);
 cudaError_t attn_few_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const KvMaps& maps,
                             int n_sm, cudaStream_t s);
+// Attention of a batch whose sequences share prefixes; the workspace holds the partial
+// results of rows over their prefix and over their own tokens.
+size_t attn_shared_workspace(const KvView& c, const Share& sh, int G, int n_sm);
+cudaError_t attn_shared_launch(const KvView& c, const AttnArgs& a, const Share& sh, void* workspace, const KvMaps& maps,
+                               int n_sm, cudaStream_t s);
 cudaError_t attn_tiles_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const KvMaps& maps,
                               int n_sm, cudaStream_t s);
 

@@ -1,0 +1,165 @@
+// Attention of sequences that share a prefix (moe_kv_attend_shared).
+//
+// With O_p, W_p the softmax's sums over the prefix's tokens and O_o, W_o those over a row's
+// own ones, both relative to one reference, out = (O_p + O_o) / (W_p + W_o).  A group's rows
+// see all of its prefix, whichever sequence they are of, so for the prefix the group is one
+// sequence without a causal mask: its keys are read once for all of its rows, and the
+// products have them all as one dimension.  The rows' own tokens are the ordinary batch, from
+// the prefix's end on.  Both are launches of the two attention kernels, by their rows, that
+// leave unnormalised sums in fp32, a reference and a weight sum for each split of the keys;
+// a last kernel joins them, own splits first, in their order.
+// The three launches overlap: the second does not need the first and begins as its
+// CTAs leave SMs, the third is in place when they end.
+#include "attn_tc.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kJoinThreads = 256;
+
+// One of the two launches: which kernel, its plan and its partial results.
+struct Side {
+  Plan pl;
+  bool few;
+  int rows;    // of a row tile
+  int parts;   // results of a split: two where both M tiles have the same rows
+  size_t cap;  // rows of results
+};
+
+Side side_of(const KvView& c, int G, int64_t tiles, int n_sm) {
+  const int64_t rows = static_cast<int64_t>(c.max_q) * G;
+  const int64_t split = static_cast<int64_t>(c.n_tokens) * c.hkv * G;
+  // as many rows as the handle's own workspace: more splits would only add to the join
+  constexpr int64_t kMost = 1 << 18;
+  Side x;
+  x.few = rows <= 32;  // as moe_kv_attend chooses
+  x.parts = !x.few && rows <= 128 ? 2 : 1;
+  x.pl = (x.few ? attn_few_plan : attn_tiles_plan)(c, G, std::max<int64_t>(tiles, 1), kMost, x.parts * split, n_sm);
+  x.rows = x.few ? (rows <= 16 ? 16 : 32) : 256;
+  x.cap = static_cast<size_t>(x.parts) * x.pl.splits * split;
+  return x;
+}
+
+// The prefixes as a batch: a group is a sequence.
+KvView prefix_view(const KvView& c, const Share& sh) {
+  KvView p = c;
+  p.n_seqs = sh.n_groups;
+  p.max_q = sh.max_tokens;
+  p.max_kv = sh.max_len;
+  p.table = sh.table;
+  p.table_stride = sh.table_stride;
+  return p;
+}
+
+struct Sides {
+  KvView prefix;
+  Side own, shared;
+};
+Sides sides_of(const KvView& c, const Share& sh, int G, int n_sm) {
+  Sides s;
+  s.prefix = prefix_view(c, sh);
+  // the host knows no bound of a sequence's own tokens; where prefixes are alike it is this
+  s.own = side_of(c, G, (std::max(c.max_kv - sh.max_len, 1) + kKeys - 1) / kKeys, n_sm);
+  s.shared = side_of(s.prefix, G, (sh.max_len + kKeys - 1) / kKeys, n_sm);
+  return s;
+}
+
+size_t align(size_t x) { return (x + 255) / 256 * 256; }
+size_t side_bytes(const Side& x, int D) { return align(x.cap * D * 4) + align(x.cap * 8); }
+
+AttnWs side_ws(const Side& x, int D, char* base) {
+  return AttnWs{reinterpret_cast<float*>(base), reinterpret_cast<float2*>(base + align(x.cap * D * 4)), nullptr, x.cap};
+}
+
+// A CTA joins a slice of the heads of one token, D / 4 threads a row.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads)
+    join_kernel(const KvView c, const AttnArgs a, const Share sh, const Side own, const Side shared, const AttnWs own_ws,
+                const AttnWs shared_ws, int slices) {
+  constexpr int kPer = kJoinThreads / (D / 4), kBatch = 8;
+  const int t = blockIdx.x / slices, slice = blockIdx.x % slices;
+  const int b = last_not_above(c.cu_q, c.n_seqs, t);
+  Seq q, g{0, 0, 0};
+  const bool covered = load_seq(c, b, q) && t >= q.q0 && t < q.q0 + q.n;
+  int group = -1, begin = 0;
+  if (covered) begin = own_begin(sh, b, q, group);
+  if (group >= 0 && !load_group(c, sh, group, g)) group = -1;
+  int n_shared = 0, per;
+  if (group >= 0) {
+    split_tiles(shared.pl, (g.L + kKeys - 1) / kKeys, n_shared, per);
+    n_shared *= shared.parts;
+  }
+  pdl_wait();
+  if (!covered) return;
+  const int d4 = threadIdx.x % (D / 4);
+  const int h1 = static_cast<int>((slice + static_cast<int64_t>(1)) * a.hq / slices);
+  for (int h = static_cast<int>(static_cast<int64_t>(slice) * a.hq / slices) + threadIdx.x / (D / 4); h < h1; h += kPer) {
+    const int hk = h / a.G, r = (t - q.q0) * a.G + h - hk * a.G;  // row of the sequence
+    const int64_t tile_end = (static_cast<int64_t>(r) / own.rows + 1) * own.rows;
+    const int last = static_cast<int>(min(static_cast<int64_t>(q.n) * a.G, tile_end) - 1) / a.G;
+    int n_own;
+    split_tiles(own.pl, own_tiles(a, q.L, begin, q.L - q.n + last), n_own, per);
+    n_own *= own.parts;
+    const size_t step = static_cast<size_t>(c.hkv) * c.n_tokens * a.G;
+    const size_t first = (static_cast<size_t>(hk) * c.n_tokens + t) * a.G + h - hk * a.G;
+    float mm = -INFINITY, ll = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < n_own + n_shared; s0 += kBatch) {
+      float2 x[kBatch];
+      float4 y[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int s = min(s0 + i, n_own + n_shared - 1);
+        const AttnWs& ws = s < n_own ? own_ws : shared_ws;
+        const size_t at = first + (s < n_own ? s : s - n_own) * step;
+        x[i] = __ldcg(&ws.ml[at]);
+        y[i] = __ldcg(reinterpret_cast<const float4*>(ws.o + at * D + 4 * d4));
+      }
+      float top = mm;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) top = fmaxf(top, x[i].x);
+      const float ref = top == -INFINITY ? 0.f : top;
+      const float back = ex2(mm - ref);
+      mm = top;
+      ll *= back;
+      v.x *= back, v.y *= back, v.z *= back, v.w *= back;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (s0 + i >= n_own + n_shared) break;
+        const float f = ex2(x[i].x - ref);
+        ll = fmaf(x[i].y, f, ll);
+        v.x = fmaf(y[i].x, f, v.x), v.y = fmaf(y[i].y, f, v.y);
+        v.z = fmaf(y[i].z, f, v.z), v.w = fmaf(y[i].w, f, v.w);
+      }
+    }
+    finish_row<D>(a, static_cast<size_t>(t) * a.hq + h, d4, v, mm, ll);
+  }
+}
+
+}  // namespace
+
+size_t attn_shared_workspace(const KvView& c, const Share& sh, int G, int n_sm) {
+  const Sides x = sides_of(c, sh, G, n_sm);
+  return side_bytes(x.own, c.D) + side_bytes(x.shared, c.D);
+}
+
+cudaError_t attn_shared_launch(const KvView& c, const AttnArgs& a, const Share& sh, void* workspace, const KvMaps& maps,
+                               int n_sm, cudaStream_t s) {
+  const Sides x = sides_of(c, sh, a.G, n_sm);
+  char* base = static_cast<char*>(workspace);
+  const AttnWs own = side_ws(x.own, c.D, base), shared = side_ws(x.shared, c.D, base + side_bytes(x.own, c.D));
+  AttnArgs all = a;
+  all.causal = 0;
+  cudaError_t e = (x.shared.few ? attn_few_part_launch : attn_tiles_part_launch)(x.prefix, all, shared, x.shared.pl, sh,
+                                                                                 true, maps, s);
+  if (e != cudaSuccess) return e;
+  e = (x.own.few ? attn_few_part_launch : attn_tiles_part_launch)(c, a, own, x.own.pl, sh, false, maps, s);
+  if (e != cudaSuccess) return e;
+  // a CTA for a pass of its threads over heads, while that is not more than the SMs hold at once
+  const int64_t per = kJoinThreads / (c.D / 4), passes = (a.hq + per - 1) / per;
+  const int64_t slices = std::max<int64_t>(1, std::min<int64_t>(passes, 8LL * n_sm / c.n_tokens));
+  return launch_kernel(c.D == 128 ? join_kernel<128> : join_kernel<64>, c.n_tokens * slices, kJoinThreads, 0, s, true, c,
+                       a, sh, x.own, x.shared, own, shared, static_cast<int>(slices));
+}
+
+}  // namespace moe

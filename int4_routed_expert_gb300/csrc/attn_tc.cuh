@@ -357,6 +357,11 @@ struct Plan {
   int row_tiles, splits, tiles_per_split;
 };
 
+// Which of a row's keys a launch is about: all; those behind its sequence's prefix; those
+// of the prefix, where a group of sequences takes the place of one.  The last two leave
+// partial results alone.
+enum class Part { kAll, kOwn, kPrefix };
+
 // What a kernel's CTAs cost, in the time that a CTA with an SM of its own takes
 // for a tile of keys.
 struct Costs {
@@ -390,10 +395,11 @@ inline int64_t best_splits(int64_t base, int64_t n_sm, int64_t tiles, int64_t mo
 struct Work {
   Seq q;
   int b, hk, r0, r1, base_p;
+  int group;       // of the sequence, where it has a prefix
   int tok0, rem0;  // token and head (of the kv head's) of row r0
   int p_lo, p_hi;  // positions of the first and the last row
   KeyTiles k;
-  int n_split;
+  int n_split, tiles_per_split;
 
   // token and head of row r0 + i: (rem0 + i) / G by its reciprocal, exact as the
   // dividend is below 2^13 and half away from the next whole number
@@ -404,17 +410,87 @@ struct Work {
   }
 };
 
-template <int ROWS>
-__device__ __forceinline__ bool work_of(const KvView& c, const AttnArgs& a, const Plan& pl, int b, int hk, int rt,
-                                        Work& w) {
-  if (!load_seq(c, b, w.q)) return false;
+// The batch's group g as one sequence whose tokens are the prefix and whose new ones are
+// the group's.  False where its arrays break their bounds.
+__device__ __forceinline__ bool load_group(const KvView& c, const Share& sh, int g, Seq& s) {
+  const int s0 = __ldg(sh.cu_seq + g), s1 = __ldg(sh.cu_seq + g + 1), L = __ldg(sh.prefix_len + g);
+  bool ok = s0 >= 0 && s1 >= s0 && s1 <= sh.n_seqs;
+  const int q0 = ok ? __ldg(c.cu_q + s0) : 0, q1 = ok ? __ldg(c.cu_q + s1) : 0;
+  s.q0 = q0;
+  s.n = q1 - q0;
+  s.L = L;
+  ok = ok && q0 >= 0 && q1 >= q0 && q1 <= c.n_tokens && s.n <= sh.max_tokens && L >= 0 && L <= sh.max_len &&
+       ((L + c.page - 1) >> c.page_log2) <= sh.table_stride;
+  if (!ok) atomicOr(c.err, kErrBadBatch);
+  return ok;
+}
+
+// The last of n ascending numbers that is not above x, looked for by the whole warp, 32
+// places at once; 0 where all are above it.
+__device__ __forceinline__ int last_not_above(const int32_t* v, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  for (int step = n; step > 1;) {
+    step = (n + 31) / 32;
+    const int at = lane * step;
+    const int k = max(__popc(__ballot_sync(0xffffffffu, at < n && __ldg(v + lo + at) <= x)), 1);
+    lo += (k - 1) * step;
+    n = min(step, n - (k - 1) * step);
+  }
+  return lo;
+}
+
+// The group of sequence b, or -1.
+__device__ __forceinline__ int group_of(const Share& sh, int b) {
+  const int g = last_not_above(sh.cu_seq, sh.n_groups, b);
+  return __ldg(sh.cu_seq + g) <= b && b < __ldg(sh.cu_seq + g + 1) ? g : -1;
+}
+
+// The first of a sequence's own keys: its prefix's length when all of its new tokens lie
+// behind it (then group >= 0), else 0.
+__device__ __forceinline__ int own_begin(const Share& sh, int b, const Seq& q, int& group) {
+  group = group_of(sh, b);
+  const int p = group >= 0 ? __ldg(sh.prefix_len + group) : 0;
+  if (p <= 0 || p > sh.max_len || q.L - q.n < p) group = -1;
+  return group >= 0 ? p : 0;
+}
+
+// How many CTAs share n_t tiles of keys: where a part of the keys is unlike what the plan
+// was made for, more or fewer tiles each.
+__device__ __forceinline__ void split_tiles(const Plan& pl, int n_t, int& n_split, int& tiles_per_split) {
+  n_split = min(max((n_t + pl.tiles_per_split - 1) / pl.tiles_per_split, 1), pl.splits);
+  tiles_per_split = max((n_t + n_split - 1) / n_split, 1);
+  n_split = max((n_t + tiles_per_split - 1) / tiles_per_split, 1);
+}
+
+// Tiles of a sequence's own keys, from `begin` on, for rows up to position p1.
+__device__ __forceinline__ int own_tiles(const AttnArgs& a, int L, int begin, int p1) {
+  const int hi = a.causal ? max(p1 + 1, 0) : L;
+  return max((hi + kKeys - 1) / kKeys - begin / kKeys, 0);
+}
+
+// Where the partial results of a launch over a part of the keys stand: [part][kv head][row],
+// a row for each token of the call and query head of the kv head.
+__device__ __forceinline__ size_t part_row(const KvView& c, const AttnArgs& a, const Work& w, int part) {
+  return (static_cast<size_t>(part) * c.hkv + w.hk) * (static_cast<size_t>(c.n_tokens) * a.G) +
+         static_cast<size_t>(w.q.q0) * a.G + w.r0;
+}
+
+template <Part PART = Part::kAll>
+__device__ __forceinline__ bool work_of(const KvView& c, const AttnArgs& a, const Plan& pl, const Share& sh, int rows,
+                                        int b, int hk, int rt, Work& w) {
+  if constexpr (PART == Part::kPrefix) {
+    if (!load_group(c, sh, b, w.q)) return false;
+  } else {
+    if (!load_seq(c, b, w.q)) return false;
+  }
   const int64_t R = static_cast<int64_t>(w.q.n) * a.G;
-  const int64_t r0 = static_cast<int64_t>(rt) * ROWS;
+  const int64_t r0 = static_cast<int64_t>(rt) * rows;
   if (r0 >= R) return false;
   w.b = b;
   w.hk = hk;
   w.r0 = static_cast<int>(r0);
-  w.r1 = static_cast<int>(min(R, r0 + ROWS));
+  w.r1 = static_cast<int>(min(R, r0 + rows));
   w.base_p = w.q.L - w.q.n;
   w.tok0 = w.r0 / a.G;
   w.rem0 = w.r0 - w.tok0 * a.G;
@@ -423,8 +499,54 @@ __device__ __forceinline__ bool work_of(const KvView& c, const AttnArgs& a, cons
   w.p_lo = w.base_p + w.tok0;
   w.p_hi = w.base_p + last;
   w.k = key_tiles<kKeys>(a, w.q.L, w.p_lo, w.p_hi);
-  w.n_split = max((w.k.n_t + pl.tiles_per_split - 1) / pl.tiles_per_split, 1);
+  if constexpr (PART == Part::kOwn) {
+    w.k.lo = own_begin(sh, b, w.q, w.group);
+    w.k.t_b = w.k.lo / kKeys;
+    w.k.n_t = own_tiles(a, w.q.L, w.k.lo, w.p_hi);
+  }
+  if constexpr (PART == Part::kAll) {
+    w.tiles_per_split = pl.tiles_per_split;
+    w.n_split = max((w.k.n_t + pl.tiles_per_split - 1) / pl.tiles_per_split, 1);
+  } else {
+    split_tiles(pl, w.k.n_t, w.n_split, w.tiles_per_split);
+  }
   return true;
 }
+
+// A launch over the rows' own keys may begin while the one over the prefixes runs, and does
+// not wait for it; the join behind both waits for this one alone.  So its last CTA ends
+// with the other launch.
+template <Part PART>
+__device__ __forceinline__ void end_of_part() {
+  if constexpr (PART == Part::kOwn)
+    if (blockIdx.x == gridDim.x - 1) pdl_wait();
+}
+
+// `early`: while the launch before still runs, once all of its CTAs said so.
+template <typename... Params, typename... Args>
+cudaError_t launch_kernel(void (*kernel)(Params...), int64_t grid, int threads, size_t smem, cudaStream_t s, bool early,
+                          const Args&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The two kernels' plans for `tiles` tiles of keys and room for `cap_rows` rows of partial
+// results, of which a split takes split_rows (0: whole row tiles), and their launches over
+// parts of the keys (attn_shared.cu).
+Plan attn_few_plan(const KvView& c, int G, int64_t tiles, int64_t cap_rows, int64_t split_rows, int n_sm);
+Plan attn_tiles_plan(const KvView& c, int G, int64_t tiles, int64_t cap_rows, int64_t split_rows, int n_sm);
+cudaError_t attn_few_part_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,
+                                 bool prefix, const KvMaps& maps, cudaStream_t s);
+cudaError_t attn_tiles_part_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,
+                                   bool prefix, const KvMaps& maps, cudaStream_t s);
 
 }  // namespace moe

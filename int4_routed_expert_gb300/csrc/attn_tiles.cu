@@ -92,9 +92,9 @@ enum Bar {
 // its own, which the join takes for two splits: one's softmax still runs under
 // the other's products.  48 rows a kv head (four sequences of up to 131072
 // keys, 4 kv heads): 142 us, and 198 us as one M tile.
-template <int D, bool DUAL>
+template <int D, bool DUAL, Part PART>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_tiles_kernel(const KvView c, const AttnArgs a, const AttnWs ws, const Plan pl,
+    attn_tiles_kernel(const KvView c, const AttnArgs a, const AttnWs ws, const Plan pl, const Share sh,
                       const __grid_constant__ CUtensorMap k_map) {
   using L_ = Lay<D>;
   extern __shared__ char smem_raw[];
@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base_u = smem_u32(smem);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), wg = warp >> 2, lane = threadIdx.x & 31;
 
+  if constexpr (PART != Part::kAll) pdl_launch_dependents();
   // long tiles first: the last rows of a causal prompt see the most keys
   int idx = blockIdx.x;
   const int hk = idx % c.hkv;
@@ -112,9 +113,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int split = idx % pl.splits;
   const int rt = pl.row_tiles - 1 - idx / pl.splits;
   Work w;
-  if (!work_of<kRows>(c, a, pl, b, hk, rt, w) || split >= w.n_split) return;
-  const int t_begin = split * pl.tiles_per_split;
-  const int t_end = min(w.k.n_t, t_begin + pl.tiles_per_split);
+  if (!work_of<PART>(c, a, pl, sh, kRows, b, hk, rt, w) || split >= w.n_split) {
+    end_of_part<PART>();
+    return;
+  }
+  const int t_begin = split * w.tiles_per_split;
+  const int t_end = min(w.k.n_t, t_begin + w.tiles_per_split);
   const int n = t_end - t_begin;  // 0 when the rows see nothing
   const int n_mt = DUAL || w.r1 - w.r0 > kM ? 2 : 1;
 
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tok = 0, head = 0;
     if (live) w.row(a, r - w.r0, tok, head);
     head += hk * a.G;
-    const RowSees sees = row_sees(a, w.q.L, w.base_p + tok, live);
+    const RowSees sees = row_sees(a, w.q.L, w.base_p + tok, live, PART == Part::kOwn ? w.k.lo : 0);
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 * (warp % 4)
     const uint32_t ts = tmem + i * 128 + lanes + half * 64, to = tmem + 256 + i * 128 + lanes + half * (D / 2);
     // What the row's two threads tell each other, two buffers in turn.  A warp
@@ -315,7 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float4* cn = io.scales(j) + 4 * half;
       const int base = w.k.base(t_begin + j) + 64 * half;
       const bool whole = (a.causal ? base + 64 <= p_lo + 1 : base + 64 <= w.q.L) &&
-                         (a.window == 0 || base > p_hi - a.window || base + 64 <= a.sinks);
+                         (a.window == 0 || base > p_hi - a.window || base + 64 <= a.sinks) &&
+                         (PART != Part::kOwn || base >= w.k.lo);
       // S is read in halves of 32 keys, the first of them twice: for the row's
       // largest logit (within 16 keys of one scale the largest product gives
       // it), then for the weights
@@ -402,7 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_after_sync();
       const size_t orow = (static_cast<size_t>(w.q.q0) + tok) * a.hq + head;
       const size_t prow =
-          (((static_cast<size_t>(b) * c.hkv + hk) * pl.row_tiles + rt) * pl.splits + split) * kRows + i * kM + row;
+          PART == Part::kAll
+              ? (((static_cast<size_t>(b) * c.hkv + hk) * pl.row_tiles + rt) * pl.splits + split) * kRows + i * kM + row
+              : part_row(c, a, w, DUAL ? 2 * split + i : split) + (DUAL ? 0 : i * kM) + row;
       // A thread's half row goes through shared memory (the queries' room: the
       // last S of either M tile came before this O), D bytes a row, so that the
       // warp's stores are whole lines: D / 2 bf16 elements in one go, or fp32
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float f = any ? 1.f / l : 0.f;
       char* stage = smem + L_::kQ + warp * (32 * D);
       const uint32_t olo = static_cast<uint32_t>(orow);
-      const bool parts = DUAL || w.n_split > 1;
+      const bool parts = PART != Part::kAll || DUAL || w.n_split > 1;
       constexpr int kCols = D / 4;  // columns a round
 #pragma unroll 1
       for (int y = 0; y < 2; ++y) {
@@ -473,6 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before_sync();
   __syncthreads();
   if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  end_of_part<PART>();
 }
 
 // Joins the splits (and the M tiles of DUAL) of every row that has more than one.
@@ -488,7 +496,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int64_t s = tile_id / pl.row_tiles;
   const int hk = static_cast<int>(s % c.hkv), b = static_cast<int>(s / c.hkv);
   Work w;
-  if (b >= c.n_seqs || !work_of<kRows>(c, a, pl, b, hk, rt, w) || (!DUAL && w.n_split == 1) || w.r0 + row >= w.r1) return;
+  if (b >= c.n_seqs || !work_of(c, a, pl, Share{}, kRows, b, hk, rt, w) || (!DUAL && w.n_split == 1) || w.r0 + row >= w.r1) return;
   int tok, head;
   w.row(a, row, tok, head);
   const size_t orow = (static_cast<size_t>(w.q.q0) + tok) * a.hq + hk * a.G + head;
@@ -496,26 +504,24 @@ __global__ void __launch_bounds__(kJoinThreads)
               DUAL ? 2 * w.n_split : w.n_split, orow, threadIdx.x % (D / 4));
 }
 
+template <int D, bool DUAL, Part PART>
+cudaError_t launch_part(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,
+                        const CUtensorMap& k_map, cudaStream_t s) {
+  static std::atomic<size_t> done[kMaxDevices];
+  const void* fn = reinterpret_cast<const void*>(attn_tiles_kernel<D, DUAL, PART>);
+  if (const cudaError_t e = opt_in_smem(fn, done, Lay<D>::kSmem); e != cudaSuccess) return e;
+  const int64_t grid = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs * pl.splits;
+  if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
+  return launch_kernel(attn_tiles_kernel<D, DUAL, PART>, grid, kThreads, Lay<D>::kSmem, s, PART == Part::kOwn, c, a, ws,
+                       pl, sh, k_map);
+}
+
 template <int D, bool DUAL>
 cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const CUtensorMap& k_map, int n_sm,
                    cudaStream_t s) {
-  static std::atomic<size_t> done[kMaxDevices];
-  const void* fn = reinterpret_cast<const void*>(attn_tiles_kernel<D, DUAL>);
-  if (const cudaError_t e = opt_in_smem(fn, done, Lay<D>::kSmem); e != cudaSuccess) return e;
-  Plan pl;
-  const int64_t rows = static_cast<int64_t>(c.max_q) * a.G;
-  pl.row_tiles = static_cast<int>((rows + kRows - 1) / kRows);
+  const Plan pl = attn_tiles_plan(c, a.G, max_key_tiles(c, a, kRows, kKeys), static_cast<int64_t>(ws.cap_rows), 0, n_sm);
   const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
-  const int64_t tiles = max_key_tiles(c, a, kRows, kKeys);
-  // one CTA a SM: split the keys when the row tiles do not fill the SMs evenly
-  const int64_t most = static_cast<int64_t>(ws.cap_rows) / (base * kRows);
-  const int64_t splits = best_splits(base, n_sm, tiles, most, c.n_seqs > 1, {1, 6., 1. / 32});
-  pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
-  pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
-  const int64_t grid = base * pl.splits;
-  if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
-  attn_tiles_kernel<D, DUAL><<<static_cast<unsigned>(grid), kThreads, Lay<D>::kSmem, s>>>(c, a, ws, pl, k_map);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_part<D, DUAL, Part::kAll>(c, a, ws, pl, Share{}, k_map, s);
   if (e != cudaSuccess || (!DUAL && pl.splits == 1)) return e;
   const int64_t items = base * kRows, per = kJoinThreads / (D / 4);
   attn_join_kernel<D, DUAL><<<static_cast<unsigned>((items + per - 1) / per), kJoinThreads, 0, s>>>(c, a, ws, pl);
@@ -531,6 +537,33 @@ cudaError_t attn_tiles_launch(const KvView& c, const AttnArgs& a, const AttnWs& 
                     static_cast<size_t>(c.n_seqs) * c.hkv * kRows <= ws.cap_rows;
   if (c.D == 128) return (dual ? launch<128, true> : launch<128, false>)(c, a, ws, maps.k_tile, n_sm, s);
   return (dual ? launch<64, true> : launch<64, false>)(c, a, ws, maps.k_tile, n_sm, s);
+}
+
+Plan attn_tiles_plan(const KvView& c, int G, int64_t tiles, int64_t cap_rows, int64_t split_rows, int n_sm) {
+  Plan pl;
+  const int64_t rows = static_cast<int64_t>(c.max_q) * G;
+  pl.row_tiles = static_cast<int>((rows + kRows - 1) / kRows);
+  const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
+  // one CTA a SM: split the keys when the row tiles do not fill the SMs evenly
+  const int64_t splits = best_splits(base, n_sm, tiles, cap_rows / (split_rows ? split_rows : base * kRows),
+                                     c.n_seqs > 1, {1, 6., 1. / 32});
+  pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
+  pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
+  return pl;
+}
+
+cudaError_t attn_tiles_part_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,
+                                   bool prefix, const KvMaps& maps, cudaStream_t s) {
+  const bool dual = static_cast<int64_t>(c.max_q) * a.G <= kM;
+  const CUtensorMap& k = maps.k_tile;
+  if (c.D == 128) {
+    if (prefix)
+      return (dual ? launch_part<128, true, Part::kPrefix> : launch_part<128, false, Part::kPrefix>)(c, a, ws, pl, sh, k, s);
+    return (dual ? launch_part<128, true, Part::kOwn> : launch_part<128, false, Part::kOwn>)(c, a, ws, pl, sh, k, s);
+  }
+  if (prefix)
+    return (dual ? launch_part<64, true, Part::kPrefix> : launch_part<64, false, Part::kPrefix>)(c, a, ws, pl, sh, k, s);
+  return (dual ? launch_part<64, true, Part::kOwn> : launch_part<64, false, Part::kOwn>)(c, a, ws, pl, sh, k, s);
 }
 
 }  // namespace moe
