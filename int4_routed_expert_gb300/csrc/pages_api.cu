@@ -9,6 +9,7 @@
 struct moe_pages : moe::HandleBase {
   moe_pages_config_t cfg;
   moe::PagesView v;
+  int n_sm;
   void* base;  // workspace
 };
 
@@ -89,6 +90,7 @@ moe_status_t moe_pages_create(const moe_pages_config_t* cfg, const moe_pages_sto
   }
   h->cfg = *cfg;
   cudaError_t e = cudaGetDevice(&h->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->n_sm, cudaDevAttrMultiProcessorCount, h->device);
   if (e != cudaSuccess) {
     fail(nullptr, "no usable CUDA device: %s", cudaGetErrorString(e));
     delete h;
@@ -114,6 +116,7 @@ moe_status_t moe_pages_create(const moe_pages_config_t* cfg, const moe_pages_sto
   while ((1 << log2) < cfg->page_size) ++log2;
   h->v = PagesView{store->table, store->kv_len, store->ref, store->cu_q, store->free_pages, cfg->n_pages, cfg->n_slots,
                    cfg->table_stride, cfg->page_size, log2, reinterpret_cast<int*>(base + L.err),
+                   reinterpret_cast<int*>(base + L.err + 128),
                    reinterpret_cast<int4*>(base + L.slot), reinterpret_cast<int4*>(base + L.place),
                    reinterpret_cast<int32_t*>(base + L.rows), reinterpret_cast<int32_t*>(base + L.ids),
                    reinterpret_cast<int32_t*>(base + L.writers), reinterpret_cast<int32_t*>(base + L.first)};
@@ -157,7 +160,7 @@ moe_status_t moe_pages_fork(moe_pages_t* h, const int32_t* parent, const int32_t
   return launched(h,
                   pages_fork_launch(h->v, static_cast<const int32_t*>(pa), static_cast<const int32_t*>(ad),
                                     static_cast<const int32_t*>(ke),
-                                    static_cast<moe_page_move_t*>(const_cast<void*>(mo)),
+                                    static_cast<moe_page_move_t*>(const_cast<void*>(mo)), h->n_sm,
                                     static_cast<cudaStream_t>(stream)),
                   "moe_pages_fork");
 }
@@ -173,7 +176,7 @@ moe_status_t moe_pages_compact(moe_pages_t* h, moe_page_move_t* moves, void* str
   const OnDevice on(h->device);
   if (on.error != cudaSuccess) return launched(h, on.error, "moe_pages_compact");
   return launched(h,
-                  pages_compact_launch(h->v, static_cast<moe_page_move_t*>(const_cast<void*>(mo)),
+                  pages_compact_launch(h->v, static_cast<moe_page_move_t*>(const_cast<void*>(mo)), h->n_sm,
                                        static_cast<cudaStream_t>(stream)),
                   "moe_pages_compact");
 }

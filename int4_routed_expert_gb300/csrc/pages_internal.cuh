@@ -19,6 +19,7 @@ struct PagesView {
   int n_pages, n_slots, stride, page, page_log2;
   int* err;
   // workspace
+  int* state;          // [3] between the launches of a call: broken bounds (0 between calls), and sizes
   int4* slot;          // [n_slots] parent, kept tokens, pages that it had, added tokens
   int4* place;         // [n_slots] first of its new pages, rank of its copy, page that it copies or -1
   int32_t* rows;       // [n_slots][stride] kept pages of slots whose parent is another
@@ -28,8 +29,8 @@ struct PagesView {
 };
 
 cudaError_t pages_fork_launch(const PagesView& p, const int32_t* parent, const int32_t* added, const int32_t* keep,
-                              moe_page_move_t* moves, cudaStream_t s);
-cudaError_t pages_compact_launch(const PagesView& p, moe_page_move_t* moves, cudaStream_t s);
+                              moe_page_move_t* moves, int n_sm, cudaStream_t s);
+cudaError_t pages_compact_launch(const PagesView& p, moe_page_move_t* moves, int n_sm, cudaStream_t s);
 cudaError_t kv_copy_launch(const KvView& c, const moe_page_move_t* moves, int n, int n_sm, cudaStream_t s);
 
 }  // namespace moe

@@ -29,10 +29,10 @@ extern "C" const char* fake_pages_log() {
 namespace moe {
 struct PagesView;
 struct KvView;
-cudaError_t pages_fork_launch(const PagesView&, const int32_t*, const int32_t*, const int32_t*, moe_page_move_t*,
+cudaError_t pages_fork_launch(const PagesView&, const int32_t*, const int32_t*, const int32_t*, moe_page_move_t*, int,
                               cudaStream_t) {
   return note("fork");
 }
-cudaError_t pages_compact_launch(const PagesView&, moe_page_move_t*, cudaStream_t) { return note("compact"); }
+cudaError_t pages_compact_launch(const PagesView&, moe_page_move_t*, int, cudaStream_t) { return note("compact"); }
 cudaError_t kv_copy_launch(const KvView&, const moe_page_move_t*, int, int, cudaStream_t) { return note("copy"); }
 }  // namespace moe
