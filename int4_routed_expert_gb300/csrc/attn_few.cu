@@ -60,7 +60,7 @@ constexpr int max_splits(int n) { return 4096 / n; }
 template <int D, int N>
 struct Lay {
   static constexpr int kStages = N == 16 ? 3 : 2;  // of key codes and of value codes
-  static constexpr int kCtas = 2;                        // a SM (as attn_few_plan counts)
+  static constexpr int kCtas = 2;                        // a SM
   using Io = TileIo<D, kStages, kStages, 0>;
   static constexpr int kGroups = N / 16;  // softmax groups of 128 threads
   static constexpr int kThreads = 128 * kGroups + 64;
@@ -639,7 +639,17 @@ cudaError_t launch_part(const KvView& c, const AttnArgs& a, const AttnWs& ws, co
 
 template <int D, int N>
 cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const KvMaps& maps, int n_sm, cudaStream_t s) {
-  const Plan pl = attn_few_plan(c, a.G, max_key_tiles(c, a, N, kKeys), static_cast<int64_t>(ws.cap_rows), 0, n_sm);
+  Plan pl;
+  const int64_t rows = static_cast<int64_t>(c.max_q) * a.G;
+  pl.row_tiles = static_cast<int>((rows + N - 1) / N);
+  const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
+  const int64_t tiles = max_key_tiles(c, a, N, kKeys);
+  // (32 rows of 8000 keys and 8 kv heads of 128, splits of 8, 4 and 2 tiles:
+  // 27.3, 23.3 and 27.2 us)
+  const int64_t most = std::min<int64_t>(static_cast<int64_t>(ws.cap_rows) / (base * N), max_splits(N));
+  const int64_t splits = best_splits(base, n_sm, tiles, most, c.n_seqs > 1, {Lay<D, N>::kCtas, 3., 0.25});
+  pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
+  pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
   return launch_part<D, N, Part::kAll>(c, a, ws, pl, Share{}, maps, s);
 }
 
@@ -653,22 +663,6 @@ cudaError_t attn_few_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws
   if (c.D == 128)
     return (rows <= 16 ? launch<128, 16> : launch<128, 32>)(c, a, ws, maps, n_sm, s);
   return (rows <= 16 ? launch<64, 16> : launch<64, 32>)(c, a, ws, maps, n_sm, s);
-}
-
-Plan attn_few_plan(const KvView& c, int G, int64_t tiles, int64_t cap_rows, int64_t split_rows, int n_sm) {
-  const int64_t rows = static_cast<int64_t>(c.max_q) * G;
-  const int n = rows <= 16 ? 16 : 32;
-  Plan pl;
-  pl.row_tiles = static_cast<int>((rows + n - 1) / n);
-  const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
-  // (32 rows of 8000 keys and 8 kv heads of 128, splits of 8, 4 and 2 tiles:
-  // 27.3, 23.3 and 27.2 us)
-  const int64_t splits =
-      best_splits(base, n_sm, tiles, std::min<int64_t>(cap_rows / (split_rows ? split_rows : base * n), max_splits(n)),
-                  c.n_seqs > 1, {2, 3., 0.25});
-  pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
-  pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
-  return pl;
 }
 
 cudaError_t attn_few_part_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,

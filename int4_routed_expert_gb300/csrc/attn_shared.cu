@@ -26,18 +26,37 @@ struct Side {
   size_t cap;  // rows of results
 };
 
-Side side_of(const KvView& c, int G, int64_t tiles, int n_sm) {
-  const int64_t rows = static_cast<int64_t>(c.max_q) * G;
-  const int64_t split = static_cast<int64_t>(c.n_tokens) * c.hkv * G;
-  // as many rows as the handle's own workspace: more splits would only add to the join
-  constexpr int64_t kMost = 1 << 18;
+// What a CTA of either kernel costs on a busy SM, in microseconds: a tile of keys, and its
+// beginning and end; and how many share the SM.
+struct CtaCost {
+  double tile, start;
+  int per_sm;
+};
+CtaCost cost_of(int64_t rows) {
+  if (rows <= 16) return {1.9, 5., 2};
+  if (rows <= 32) return {3.3, 6., 2};
+  return {1.75, 10., 1};
+}
+
+// The kernel for a side's rows, and its row tiles: `live` of them are sure to have rows, of
+// all CTAs' ones that a launch has to count on.
+Side side_of(const KvView& c, int G, double& live) {
+  const int64_t rows = static_cast<int64_t>(c.max_q) * G, all = static_cast<int64_t>(c.n_tokens) * G;
   Side x;
   x.few = rows <= 32;  // as moe_kv_attend chooses
-  x.parts = !x.few && rows <= 128 ? 2 : 1;
-  x.pl = (x.few ? attn_few_plan : attn_tiles_plan)(c, G, std::max<int64_t>(tiles, 1), kMost, x.parts * split, n_sm);
   x.rows = x.few ? (rows <= 16 ? 16 : 32) : 256;
-  x.cap = static_cast<size_t>(x.parts) * x.pl.splits * split;
+  x.parts = !x.few && rows <= 128 ? 2 : 1;
+  x.pl.row_tiles = static_cast<int>((rows + x.rows - 1) / x.rows);
+  // the sequences' rows add up to the call's, and half a tile of each is empty
+  live = std::min(static_cast<double>(x.pl.row_tiles) * c.n_seqs, static_cast<double>(all) / x.rows + 0.5 * c.n_seqs + 0.5) *
+         c.hkv;
   return x;
+}
+
+void set_splits(Side& x, const KvView& c, int G, int64_t tiles, int64_t splits) {
+  x.pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
+  x.pl.splits = static_cast<int>((tiles + x.pl.tiles_per_split - 1) / x.pl.tiles_per_split);
+  x.cap = static_cast<size_t>(x.parts) * x.pl.splits * c.n_tokens * c.hkv * G;
 }
 
 // The prefixes as a batch: a group is a sequence.
@@ -55,12 +74,45 @@ struct Sides {
   KvView prefix;
   Side own, shared;
 };
+// The splits of the keys.  A launch over own tokens fills the SMs that the one over the
+// prefixes leaves, so that one's splits go by the time of both: that of its longest CTAs,
+// or all CTAs' time over the SMs, whichever is longer, and what a split more costs the join.
+// (64 tokens on a prefix of 16384, 64 / 8 heads: 78 us at 4 to 6 splits, 87 us at 9, where
+// the prefix alone is fastest; 37 x 4 tokens on three of up to 66001, 48 / 4 heads: 265 us at
+// 4 splits, 338 us at 6, whose second round of CTAs is a quarter full.)
 Sides sides_of(const KvView& c, const Share& sh, int G, int n_sm) {
+  constexpr int64_t kMost = 1 << 20;  // rows of results a side, where one split has fewer
+  const int64_t rows = static_cast<int64_t>(c.n_tokens) * c.hkv * G;
   Sides s;
   s.prefix = prefix_view(c, sh);
+  double own_live, live;
+  s.own = side_of(c, G, own_live);
+  s.shared = side_of(s.prefix, G, live);
   // the host knows no bound of a sequence's own tokens; where prefixes are alike it is this
-  s.own = side_of(c, G, (std::max(c.max_kv - sh.max_len, 1) + kKeys - 1) / kKeys, n_sm);
-  s.shared = side_of(s.prefix, G, (sh.max_len + kKeys - 1) / kKeys, n_sm);
+  const int64_t own_tiles = (std::max(c.max_kv - sh.max_len, 1) + kKeys - 1) / kKeys;
+  const int64_t tiles = (sh.max_len + kKeys - 1) / kKeys;
+  const CtaCost own_cost = cost_of(static_cast<int64_t>(c.max_q) * G), cost = cost_of(static_cast<int64_t>(s.prefix.max_q) * G);
+  auto limit = [&](int64_t n, const Side& x) {
+    return std::max<int64_t>(std::min({n, static_cast<int64_t>(256), kMost / (x.parts * rows)}), 1);
+  };
+  const int64_t own_splits =
+      best_splits(static_cast<int64_t>(own_live + 0.5), n_sm, own_tiles, limit(own_tiles, s.own), c.n_seqs > 1,
+                  s.own.few ? Costs{2, 3., 0.25} : Costs{1, 6., 1. / 32});
+  set_splits(s.own, c, G, own_tiles, own_splits);
+  // (sequences' lengths spread between none and the bound)
+  const double own_time = own_live * (0.6 * static_cast<double>(own_tiles) * own_cost.tile + own_cost.start * s.own.pl.splits) /
+                          own_cost.per_sm;
+  const double join = static_cast<double>(rows) * s.shared.parts * c.D * 8 / 5e6;  // sums written and read, at 5 TB/s
+  double least = 1e300;
+  int64_t best = 1;
+  for (int64_t k = 1, end = limit(tiles, s.shared); k <= end; ++k) {
+    const double cta = cost.tile * static_cast<double>((tiles + k - 1) / k) + cost.start;
+    const double ctas = std::max(live * static_cast<double>(k), 1.);
+    const double rounds = static_cast<double>(static_cast<int64_t>((ctas - 1) / (n_sm * cost.per_sm)) + 1);
+    const double time = std::max(rounds * cta, (ctas * cta / cost.per_sm + own_time) / n_sm) + join * static_cast<double>(k);
+    if (time < least) least = time, best = k;
+  }
+  set_splits(s.shared, c, G, tiles, best);
   return s;
 }
 
@@ -143,9 +195,11 @@ size_t attn_shared_workspace(const KvView& c, const Share& sh, int G, int n_sm) 
   return side_bytes(x.own, c.D) + side_bytes(x.shared, c.D);
 }
 
-cudaError_t attn_shared_launch(const KvView& c, const AttnArgs& a, const Share& sh, void* workspace, const KvMaps& maps,
-                               int n_sm, cudaStream_t s) {
+cudaError_t attn_shared_launch(const KvView& c, const AttnArgs& a, const Share& sh, void* workspace, size_t have,
+                               size_t* need, const KvMaps& maps, int n_sm, cudaStream_t s) {
   const Sides x = sides_of(c, sh, a.G, n_sm);
+  *need = side_bytes(x.own, c.D) + side_bytes(x.shared, c.D);
+  if (have < *need) return cudaErrorInvalidValue;
   char* base = static_cast<char*>(workspace);
   const AttnWs own = side_ws(x.own, c.D, base), shared = side_ws(x.shared, c.D, base + side_bytes(x.own, c.D));
   AttnArgs all = a;

@@ -539,11 +539,7 @@ cudaError_t launch_kernel(void (*kernel)(Params...), int64_t grid, int threads, 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// The two kernels' plans for `tiles` tiles of keys and room for `cap_rows` rows of partial
-// results, of which a split takes split_rows (0: whole row tiles), and their launches over
-// parts of the keys (attn_shared.cu).
-Plan attn_few_plan(const KvView& c, int G, int64_t tiles, int64_t cap_rows, int64_t split_rows, int n_sm);
-Plan attn_tiles_plan(const KvView& c, int G, int64_t tiles, int64_t cap_rows, int64_t split_rows, int n_sm);
+// The two kernels' launches over parts of the keys (attn_shared.cu).
 cudaError_t attn_few_part_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,
                                  bool prefix, const KvMaps& maps, cudaStream_t s);
 cudaError_t attn_tiles_part_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,

@@ -519,8 +519,16 @@ cudaError_t launch_part(const KvView& c, const AttnArgs& a, const AttnWs& ws, co
 template <int D, bool DUAL>
 cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const CUtensorMap& k_map, int n_sm,
                    cudaStream_t s) {
-  const Plan pl = attn_tiles_plan(c, a.G, max_key_tiles(c, a, kRows, kKeys), static_cast<int64_t>(ws.cap_rows), 0, n_sm);
+  Plan pl;
+  const int64_t rows = static_cast<int64_t>(c.max_q) * a.G;
+  pl.row_tiles = static_cast<int>((rows + kRows - 1) / kRows);
   const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
+  const int64_t tiles = max_key_tiles(c, a, kRows, kKeys);
+  // one CTA a SM: split the keys when the row tiles do not fill the SMs evenly
+  const int64_t most = static_cast<int64_t>(ws.cap_rows) / (base * kRows);
+  const int64_t splits = best_splits(base, n_sm, tiles, most, c.n_seqs > 1, {1, 6., 1. / 32});
+  pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
+  pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
   const cudaError_t e = launch_part<D, DUAL, Part::kAll>(c, a, ws, pl, Share{}, k_map, s);
   if (e != cudaSuccess || (!DUAL && pl.splits == 1)) return e;
   const int64_t items = base * kRows, per = kJoinThreads / (D / 4);
@@ -537,19 +545,6 @@ cudaError_t attn_tiles_launch(const KvView& c, const AttnArgs& a, const AttnWs& 
                     static_cast<size_t>(c.n_seqs) * c.hkv * kRows <= ws.cap_rows;
   if (c.D == 128) return (dual ? launch<128, true> : launch<128, false>)(c, a, ws, maps.k_tile, n_sm, s);
   return (dual ? launch<64, true> : launch<64, false>)(c, a, ws, maps.k_tile, n_sm, s);
-}
-
-Plan attn_tiles_plan(const KvView& c, int G, int64_t tiles, int64_t cap_rows, int64_t split_rows, int n_sm) {
-  Plan pl;
-  const int64_t rows = static_cast<int64_t>(c.max_q) * G;
-  pl.row_tiles = static_cast<int>((rows + kRows - 1) / kRows);
-  const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
-  // one CTA a SM: split the keys when the row tiles do not fill the SMs evenly
-  const int64_t splits = best_splits(base, n_sm, tiles, cap_rows / (split_rows ? split_rows : base * kRows),
-                                     c.n_seqs > 1, {1, 6., 1. / 32});
-  pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
-  pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
-  return pl;
 }
 
 cudaError_t attn_tiles_part_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,

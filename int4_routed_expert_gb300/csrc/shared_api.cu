@@ -66,15 +66,16 @@ moe_status_t moe_kv_attend_shared(moe_kv_t* h, const void* q, int64_t q_stride, 
   sh.cu_seq = static_cast<const int32_t*>(p[0]);
   sh.prefix_len = static_cast<const int32_t*>(p[1]);
   sh.table = static_cast<const int32_t*>(p[2]);
-  const size_t need = attn_shared_workspace(c, sh, a.G, h->n_sm);
+  const OnDevice on(h->device);
+  if (on.error != cudaSuccess) return launched(h, on.error, "moe_kv_attend_shared");
+  size_t need = 0;
+  const cudaError_t e = attn_shared_launch(c, a, sh, const_cast<void*>(p[3]), workspace_bytes, &need, h->maps, h->n_sm,
+                                           static_cast<cudaStream_t>(stream));
   if (workspace_bytes < need) {
     fail(h, "the workspace has %zu bytes, the call needs %zu", workspace_bytes, need);
     return MOE_ERR_CAPACITY;
   }
-  const OnDevice on(h->device);
-  if (on.error != cudaSuccess) return launched(h, on.error, "moe_kv_attend_shared");
-  return launched(h, attn_shared_launch(c, a, sh, const_cast<void*>(p[3]), h->maps, h->n_sm, static_cast<cudaStream_t>(stream)),
-                  "moe_kv_attend_shared");
+  return launched(h, e, "moe_kv_attend_shared");
 }
 
 }  // extern "C"

@@ -30,8 +30,10 @@ struct AttnArgs;
 struct Share;
 struct KvMaps;
 size_t attn_shared_workspace(const KvView&, const Share&, int, int) { return 4096; }
-cudaError_t attn_shared_launch(const KvView&, const AttnArgs&, const Share&, void*, const KvMaps&, int, cudaStream_t) {
-  return note("shared");
+cudaError_t attn_shared_launch(const KvView&, const AttnArgs&, const Share&, void*, size_t have, size_t* need, const KvMaps&,
+                               int, cudaStream_t) {
+  *need = 4096;
+  return have < *need ? cudaErrorInvalidValue : note("shared");
 }
 cudaError_t rope_axes_launch(const uint64_t*, const uint8_t*, int, float, bool, const moe_rope_tensor_t*,
                              const moe_rope_tensor_t*, int, moe_dtype_t, const int32_t*, int64_t, int, cudaStream_t) {
