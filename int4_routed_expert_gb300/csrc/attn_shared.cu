@@ -132,12 +132,11 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int t = blockIdx.x / slices, slice = blockIdx.x % slices;
   const int b = last_not_above(c.cu_q, c.n_seqs, t);
   Seq q, g{0, 0, 0};
+  InGroup in = group_of(sh, b);
   const bool covered = load_seq(c, b, q) && t >= q.q0 && t < q.q0 + q.n;
-  int group = -1, begin = 0;
-  if (covered) begin = own_begin(sh, b, q, group);
-  if (group >= 0 && !load_group(c, sh, group, g)) group = -1;
+  const int begin = covered ? own_begin(sh, q, in) : 0;
   int n_shared = 0, per;
-  if (group >= 0) {
+  if (covered && in.g >= 0 && load_group(c, sh, in.g, g)) {
     split_tiles(shared.pl, (g.L + kKeys - 1) / kKeys, n_shared, per);
     n_shared *= shared.parts;
   }

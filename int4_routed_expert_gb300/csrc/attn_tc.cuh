@@ -395,7 +395,6 @@ inline int64_t best_splits(int64_t base, int64_t n_sm, int64_t tiles, int64_t mo
 struct Work {
   Seq q;
   int b, hk, r0, r1, base_p;
-  int group;       // of the sequence, where it has a prefix
   int tok0, rem0;  // token and head (of the kv head's) of row r0
   int p_lo, p_hi;  // positions of the first and the last row
   KeyTiles k;
@@ -440,19 +439,29 @@ __device__ __forceinline__ int last_not_above(const int32_t* v, int n, int x) {
   return lo;
 }
 
-// The group of sequence b, or -1.
-__device__ __forceinline__ int group_of(const Share& sh, int b) {
+// A sequence's group and its prefix's length; g is -1 where no group holds it.  Up to 32
+// groups are looked at in one go: a CTA's first loads are a chain that it waits for.
+struct InGroup {
+  int g, prefix;
+};
+__device__ __forceinline__ InGroup group_of(const Share& sh, int b) {
+  if (sh.n_groups <= 32) {
+    const int lane = threadIdx.x & 31, g = min(lane, sh.n_groups - 1);
+    const int s0 = __ldg(sh.cu_seq + g), s1 = __ldg(sh.cu_seq + g + 1), p = __ldg(sh.prefix_len + g);
+    const uint32_t in = __ballot_sync(0xffffffffu, lane < sh.n_groups && s0 <= b && b < s1);
+    const int at = in ? 31 - __clz(in) : 0;
+    return {in ? at : -1, __shfl_sync(0xffffffffu, p, at)};
+  }
   const int g = last_not_above(sh.cu_seq, sh.n_groups, b);
-  return __ldg(sh.cu_seq + g) <= b && b < __ldg(sh.cu_seq + g + 1) ? g : -1;
+  const int s0 = __ldg(sh.cu_seq + g), s1 = __ldg(sh.cu_seq + g + 1), p = __ldg(sh.prefix_len + g);
+  return {s0 <= b && b < s1 ? g : -1, p};
 }
 
 // The first of a sequence's own keys: its prefix's length when all of its new tokens lie
-// behind it (then group >= 0), else 0.
-__device__ __forceinline__ int own_begin(const Share& sh, int b, const Seq& q, int& group) {
-  group = group_of(sh, b);
-  const int p = group >= 0 ? __ldg(sh.prefix_len + group) : 0;
-  if (p <= 0 || p > sh.max_len || q.L - q.n < p) group = -1;
-  return group >= 0 ? p : 0;
+// behind it, else 0 and no group.
+__device__ __forceinline__ int own_begin(const Share& sh, const Seq& q, InGroup& in) {
+  if (in.prefix <= 0 || in.prefix > sh.max_len || q.L - q.n < in.prefix) in.g = -1;
+  return in.g >= 0 ? in.prefix : 0;
 }
 
 // How many CTAs share n_t tiles of keys: where a part of the keys is unlike what the plan
@@ -479,6 +488,8 @@ __device__ __forceinline__ size_t part_row(const KvView& c, const AttnArgs& a, c
 template <Part PART = Part::kAll>
 __device__ __forceinline__ bool work_of(const KvView& c, const AttnArgs& a, const Plan& pl, const Share& sh, int rows,
                                         int b, int hk, int rt, Work& w) {
+  InGroup in{-1, 0};
+  if constexpr (PART == Part::kOwn) in = group_of(sh, b);
   if constexpr (PART == Part::kPrefix) {
     if (!load_group(c, sh, b, w.q)) return false;
   } else {
@@ -500,7 +511,7 @@ __device__ __forceinline__ bool work_of(const KvView& c, const AttnArgs& a, cons
   w.p_hi = w.base_p + last;
   w.k = key_tiles<kKeys>(a, w.q.L, w.p_lo, w.p_hi);
   if constexpr (PART == Part::kOwn) {
-    w.k.lo = own_begin(sh, b, w.q, w.group);
+    w.k.lo = own_begin(sh, w.q, in);
     w.k.t_b = w.k.lo / kKeys;
     w.k.n_t = own_tiles(a, w.q.L, w.k.lo, w.p_hi);
   }
