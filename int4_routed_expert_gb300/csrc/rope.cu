@@ -8,16 +8,21 @@
 // quarter turn is taken off in integers, and what fp32 cannot hold of the rest's
 // 30 bits turns the sine and cosine by their derivatives: the angle that goes in
 // is exact to 2^-33 turns, where the phase as one fp32 number would be off by up
-// to 2^-26.  Bound by memory: x is read once and y written once (8192 tokens of 56 heads of 128,
-// bf16: 43.0 us, 5.5 TB/s).
+// to 2^-26.  Several axes are a position for each pair, picked where its phase is worked out.
+//
+// Bound by memory: x is read once and y written once.  A thread's next heads are on their
+// way while it turns the ones at hand, the first ones under the angles, and small CTAs,
+// seven of them a SM in bf16, are in different phases (8192 tokens of 56 heads of 128, bf16:
+// 36.8 us, 6.4 TB/s; CTAs of 256 threads and four tokens 40.8 us, without the loads ahead
+// 42.8 us; fp32, whose registers allow four of the CTAs, 70.2 us, 6.7 TB/s).
 #include "attn_internal.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kItems = 2;   // heads of a thread under way
-constexpr int kTokens = 4;  // most tokens of a CTA
+constexpr int kThreads = 128;
+constexpr int kItems = 2;   // heads of a thread under way, twice
+constexpr int kTokens = 2;  // most tokens of a CTA
 
 struct RopeParams {
   uint64_t inc[128];  // fraction of a turn per position, 64-bit fixed point
@@ -80,10 +85,34 @@ struct Raw {
 };
 
 template <typename T, bool INTERLEAVED, bool AXES>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams P) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 7 : 1) rope_kernel(const __grid_constant__ RopeParams P) {
   __shared__ float2 cs[kTokens][128];  // cosine, sine
   const int half = P.rot >> 1;
   const int t0 = blockIdx.x * P.tokens, tn = min(P.tokens, P.T - t0);
+  // a thread's place c in a head is fixed: elements ia .. ia + 7 and ib .. ib + 7
+  const int per_head = P.head_dim >> 4;
+  const int h0 = threadIdx.x / per_head, c = threadIdx.x - h0 * per_head;
+  const int hstep = blockDim.x / per_head, heads = P.heads[0] + P.heads[1];
+  const bool turned = c < (P.rot >> 4);
+  int ia = 16 * c, ib = 16 * c + 8;
+  if (!INTERLEAVED && turned) ia = 8 * c, ib = 8 * c + half;
+  auto at = [&](const void* const (&base)[2], const int64_t (&stride)[2], int t, int h) {
+    const int w = h >= P.heads[0];
+    return static_cast<const T*>(base[w]) + (t0 + t) * stride[w] + (h - (w ? P.heads[0] : 0)) * P.head_dim;
+  };
+  Raw<T> a[kItems], b[kItems], a1[kItems], b1[kItems];
+  auto load = [&](Raw<T>(&x)[kItems], Raw<T>(&y)[kItems], int t, int h) {
+#pragma unroll
+    for (int n = 0; n < kItems; ++n) {
+      if (t < tn && h + n * hstep < heads) {
+        const T* p = at(P.x, P.xs, t, h + n * hstep);
+        x[n].load(p + ia);
+        y[n].load(p + ib);
+      }
+    }
+  };
+  // the first heads are on their way while the angles are worked out
+  load(a, b, 0, h0);
   for (int i = threadIdx.x; i < tn * half; i += blockDim.x) {
     const int tk = i / half, pair = i - tk * half;
     const int32_t* pos = P.pos + t0 + tk;
@@ -102,17 +131,6 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     c = (quarter + 1) & 2 ? -c : c;
     cs[tk][pair] = make_float2(c * P.amplitude, s * P.amplitude);
   }
-  // a thread's place c in a head is fixed: elements ia .. ia + 7 and ib .. ib + 7
-  const int per_head = P.head_dim >> 4;
-  const int h0 = threadIdx.x / per_head, c = threadIdx.x - h0 * per_head;
-  const int hstep = blockDim.x / per_head, heads = P.heads[0] + P.heads[1];
-  const bool turned = c < (P.rot >> 4);
-  int ia = 16 * c, ib = 16 * c + 8;
-  if (!INTERLEAVED && turned) ia = 8 * c, ib = 8 * c + half;
-  auto at = [&](const void* const (&base)[2], const int64_t (&stride)[2], int t, int h) {
-    const int w = h >= P.heads[0];
-    return static_cast<const T*>(base[w]) + (t0 + t) * stride[w] + (h - (w ? P.heads[0] : 0)) * P.head_dim;
-  };
   __syncthreads();
   for (int t = 0; t < tn; ++t) {
     float2 r[8];
@@ -121,15 +139,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
       for (int i = 0; i < 8; ++i) r[i] = cs[t][8 * c + i];
     }
     for (int h = h0; h < heads; h += kItems * hstep) {
-      Raw<T> a[kItems], b[kItems];
-#pragma unroll
-      for (int n = 0; n < kItems; ++n) {
-        if (h + n * hstep < heads) {
-          const T* x = at(P.x, P.xs, t, h + n * hstep);
-          a[n].load(x + ia);
-          b[n].load(x + ib);
-        }
-      }
+      // the next heads, this token's or the next one's
+      const bool more = h + kItems * hstep < heads;
+      load(a1, b1, more ? t : t + 1, more ? h + kItems * hstep : h0);
 #pragma unroll
       for (int n = 0; n < kItems; ++n) {
         if (h + n * hstep >= heads) break;
@@ -152,6 +164,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         a[n].store(y + ia);
         b[n].store(y + ib);
       }
+#pragma unroll
+      for (int n = 0; n < kItems; ++n) a[n] = a1[n], b[n] = b1[n];
     }
   }
 }
@@ -179,8 +193,8 @@ cudaError_t launch(const uint64_t* inc, const uint8_t* axis, int rot_dim, float 
   P.rot = rot_dim;
   P.head_dim = head_dim;
   P.T = T;
-  // one token a CTA while that fills the device once; four share the angles' phase then
-  // (8192 tokens: 42.9 us, and 45.1 us with one)
+  // one token a CTA while that fills the device once; two share the angles' phase then
+  // (8192 tokens of 32 + 2 heads of 64: 15.2 us, and 17.8 us with one)
   P.tokens = T >= 2048 ? kTokens : 1;
   const int per_head = head_dim / 16, threads = kThreads / per_head * per_head;
   const int grid = (T + P.tokens - 1) / P.tokens;
