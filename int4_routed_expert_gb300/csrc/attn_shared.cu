@@ -73,6 +73,7 @@ KvView prefix_view(const KvView& c, const Share& sh) {
 struct Sides {
   KvView prefix;
   Side own, shared;
+  bool wide;  // few rows: the join has a CTA for each
 };
 // The splits of the keys.  A launch over own tokens fills the SMs that the one over the
 // prefixes leaves, so that one's splits go by the time of both: that of its longest CTAs,
@@ -102,7 +103,9 @@ Sides sides_of(const KvView& c, const Share& sh, int G, int n_sm) {
   // (sequences' lengths spread between none and the bound)
   const double own_time = own_live * (0.6 * static_cast<double>(own_tiles) * own_cost.tile + own_cost.start * s.own.pl.splits) /
                           own_cost.per_sm;
-  const double join = static_cast<double>(rows) * s.shared.parts * c.D * 8 / 5e6;  // sums written and read, at 5 TB/s
+  // a split's sums written and read, at 5 TB/s, and read eight at a time, by one or all of a CTA's rows
+  s.wide = rows <= 16 * n_sm;
+  const double join = static_cast<double>(rows) * s.shared.parts * c.D * 8 / 5e6 + s.shared.parts * (s.wide ? 0.8 / 64 : 0.1);
   double least = 1e300;
   int64_t best = 1;
   for (int64_t k = 1, end = limit(tiles, s.shared); k <= end; ++k) {
@@ -123,8 +126,36 @@ AttnWs side_ws(const Side& x, int D, char* base) {
   return AttnWs{reinterpret_cast<float*>(base), reinterpret_cast<float2*>(base + align(x.cap * D * 4)), nullptr, x.cap};
 }
 
-// A CTA joins a slice of the heads of one token, D / 4 threads a row.
-template <int D>
+// What a row's partial results add up to, so far.
+struct RowSum {
+  float m, l;  // reference, sum of weights
+  float4 v;
+  // Takes on kBatch results at once, in their order; those from n on are none.
+  template <int N>
+  __device__ __forceinline__ void add(const float2 (&x)[N], const float4 (&y)[N], int n) {
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = fmaxf(top, x[i].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    const float back = ex2(m - ref);
+    m = top;
+    l *= back;
+    v.x *= back, v.y *= back, v.z *= back, v.w *= back;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i >= n) break;
+      const float f = ex2(x[i].x - ref);
+      l = fmaf(x[i].y, f, l);
+      v.x = fmaf(y[i].x, f, v.x), v.y = fmaf(y[i].y, f, v.y);
+      v.z = fmaf(y[i].z, f, v.z), v.w = fmaf(y[i].w, f, v.w);
+    }
+  }
+};
+
+// A CTA joins a slice of the heads of one token, D / 4 threads a row.  WIDE: the whole CTA
+// a row, D / 4 threads every eighth (heads of 64: sixteenth) of its results, whose sums are
+// joined once more: for calls of few rows, whose keys are cut into many splits.
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(kJoinThreads)
     join_kernel(const KvView c, const AttnArgs a, const Share sh, const Side own, const Side shared, const AttnWs own_ws,
                 const AttnWs shared_ws, int slices) {
@@ -142,9 +173,10 @@ __global__ void __launch_bounds__(kJoinThreads)
   }
   pdl_wait();
   if (!covered) return;
-  const int d4 = threadIdx.x % (D / 4);
+  const int d4 = threadIdx.x % (D / 4), grp = threadIdx.x / (D / 4);
+  const int h0 = static_cast<int>(static_cast<int64_t>(slice) * a.hq / slices);
   const int h1 = static_cast<int>((slice + static_cast<int64_t>(1)) * a.hq / slices);
-  for (int h = static_cast<int>(static_cast<int64_t>(slice) * a.hq / slices) + threadIdx.x / (D / 4); h < h1; h += kPer) {
+  for (int h = h0 + (WIDE ? 0 : grp); h < h1; h += WIDE ? 1 : kPer) {
     const int hk = h / a.G, r = (t - q.q0) * a.G + h - hk * a.G;  // row of the sequence
     const int64_t tile_end = (static_cast<int64_t>(r) / own.rows + 1) * own.rows;
     const int last = static_cast<int>(min(static_cast<int64_t>(q.n) * a.G, tile_end) - 1) / a.G;
@@ -153,37 +185,37 @@ __global__ void __launch_bounds__(kJoinThreads)
     n_own *= own.parts;
     const size_t step = static_cast<size_t>(c.hkv) * c.n_tokens * a.G;
     const size_t first = (static_cast<size_t>(hk) * c.n_tokens + t) * a.G + h - hk * a.G;
-    float mm = -INFINITY, ll = 0.f;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < n_own + n_shared; s0 += kBatch) {
+    const int all = n_own + n_shared, mine = WIDE ? max((all - grp + kPer - 1) / kPer, 0) : all;
+    RowSum sum{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int s0 = 0; s0 < mine; s0 += kBatch) {
       float2 x[kBatch];
       float4 y[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int s = min(s0 + i, n_own + n_shared - 1);
+        const int k = min(s0 + i, mine - 1), s = WIDE ? k * kPer + grp : k;
         const AttnWs& ws = s < n_own ? own_ws : shared_ws;
         const size_t at = first + (s < n_own ? s : s - n_own) * step;
         x[i] = __ldcg(&ws.ml[at]);
         y[i] = __ldcg(reinterpret_cast<const float4*>(ws.o + at * D + 4 * d4));
       }
-      float top = mm;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) top = fmaxf(top, x[i].x);
-      const float ref = top == -INFINITY ? 0.f : top;
-      const float back = ex2(mm - ref);
-      mm = top;
-      ll *= back;
-      v.x *= back, v.y *= back, v.z *= back, v.w *= back;
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        if (s0 + i >= n_own + n_shared) break;
-        const float f = ex2(x[i].x - ref);
-        ll = fmaf(x[i].y, f, ll);
-        v.x = fmaf(y[i].x, f, v.x), v.y = fmaf(y[i].y, f, v.y);
-        v.z = fmaf(y[i].z, f, v.z), v.w = fmaf(y[i].w, f, v.w);
-      }
+      sum.add(x, y, mine - s0);
     }
-    finish_row<D>(a, static_cast<size_t>(t) * a.hq + h, d4, v, mm, ll);
+    if constexpr (WIDE) {
+      __shared__ float2 ml[kPer];
+      __shared__ float4 part[kPer][D / 4];
+      __syncthreads();  // (of the row before)
+      if (d4 == 0) ml[grp] = make_float2(sum.m, sum.l);
+      part[grp][d4] = sum.v;
+      __syncthreads();
+      if (grp > 0) continue;
+      float2 x[kPer];
+      float4 y[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) x[i] = ml[i], y[i] = part[i][d4];
+      sum = RowSum{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      sum.add(x, y, kPer);
+    }
+    finish_row<D>(a, static_cast<size_t>(t) * a.hq + h, d4, sum.v, sum.m, sum.l);
   }
 }
 
@@ -209,10 +241,12 @@ cudaError_t attn_shared_launch(const KvView& c, const AttnArgs& a, const Share& 
   e = (x.own.few ? attn_few_part_launch : attn_tiles_part_launch)(c, a, own, x.own.pl, sh, false, maps, s);
   if (e != cudaSuccess) return e;
   // a CTA for a pass of its threads over heads, while that is not more than the SMs hold at once
-  const int64_t per = kJoinThreads / (c.D / 4), passes = (a.hq + per - 1) / per;
-  const int64_t slices = std::max<int64_t>(1, std::min<int64_t>(passes, 8LL * n_sm / c.n_tokens));
-  return launch_kernel(c.D == 128 ? join_kernel<128> : join_kernel<64>, c.n_tokens * slices, kJoinThreads, 0, s, true, c,
-                       a, sh, x.own, x.shared, own, shared, static_cast<int>(slices));
+  const int64_t per = x.wide ? 1 : kJoinThreads / (c.D / 4), passes = (a.hq + per - 1) / per;
+  const int64_t slices = x.wide ? passes : std::max<int64_t>(1, std::min<int64_t>(passes, 8LL * n_sm / c.n_tokens));
+  auto join = c.D == 128 ? (x.wide ? join_kernel<128, true> : join_kernel<128, false>)
+                         : (x.wide ? join_kernel<64, true> : join_kernel<64, false>);
+  return launch_kernel(join, c.n_tokens * slices, kJoinThreads, 0, s, true, c, a, sh, x.own, x.shared, own, shared,
+                       static_cast<int>(slices));
 }
 
 }  // namespace moe
