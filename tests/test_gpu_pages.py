@@ -92,6 +92,50 @@ def test_fork_of_one_page_by_all(m):
     assert pool.free.item() == 64 and (pool.table == -1).all()
 
 
+@pytest.mark.parametrize("slots,width", [(5, 6), (2000, 40)])
+def test_keep_may_be_the_lengths_themselves(m, slots, width):
+    """keep=pool.kv_len (a slot keeps at most as many tokens as it had): the lengths are read before they change."""
+    r = random.Random(slots)
+    pool, ref = empty(m, slots * width, 16, slots, width)
+    assert fork(m, pool, ref, [-1] * slots, [r.randint(0, 40) for _ in range(slots)]) == 0
+    for _ in range(3):
+        parent, added = [r.randrange(slots) for _ in range(slots)], [r.randint(0, 3) for _ in range(slots)]
+        assert ref.fork(parent, added, list(ref.lens))[0] == 0
+        pool.fork(t(parent), t(added), keep=pool.kv_len)
+        same(pool, ref)
+    assert pool.device_status() == 0
+
+
+def test_a_captured_fork_follows_its_arrays(m):
+    pool, ref = empty(m, 3000, 16, 300, 40)
+    parent, added, keep = (torch.zeros(300, **I32) for _ in range(3))
+    parent.fill_(-1)
+    pool.fork(parent, added, keep=keep)
+    assert ref.fork([-1] * 300, [0] * 300)[0] == 0
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        moves = pool.fork(parent, added, keep=keep)
+        compacted = pool.compact()
+    r = random.Random(1)
+    for step in range(12):
+        p = [r.choice((i, r.randrange(300), -1)) if step else -1 for i in range(300)]
+        a = [r.randint(0, 60 if step % 4 == 0 else 2) for _ in range(300)]
+        if step == 7:
+            a[200] = -1  # refused: the graph's compaction runs all the same
+        k = [r.randint(0, 640 - x) for x in a]
+        parent.copy_(t(p)), added.copy_(t(a)), keep.copy_(t(k))
+        g.replay()
+        want, wanted, cu = ref.fork(p, a, k)
+        assert (want == 0) == (step != 7)
+        assert moves.tolist() == [list(x) for x in wanted] and pool.cu_q.tolist() == cu
+        assert compacted.tolist() == [list(x) for x in ref.compact()]
+        same(pool, ref)
+        if want:
+            with pytest.raises(m.MoeError):
+                pool.device_status()
+    assert pool.device_status() == 0
+
+
 def test_kept_pages(m):
     """A page that the caller counts once more stays when its sequence ends, and is copied by its only writer."""
     pool, ref = empty(m, 32, 16, 2, 4)
@@ -217,6 +261,25 @@ def test_copy(m, heads, page, dim, n):
     c.copy(t([(-1, -1, -1)] * 1000))
     c.copy(t([(ids[0], ids[0], page)]))  # onto itself
     assert all(torch.equal(x, y) for x, y in zip(want, (c.k_codes, c.v_codes, c.k_scale, c.v_scale)))
+    assert c.device_status() == 0
+
+
+def test_copy_far_pages(m):
+    """Offsets beyond 2^31 bytes, either way."""
+    pages, page = 40001, 128
+    codes = [torch.empty(pages, 8, page, 128, dtype=torch.uint8, device=DEV) for _ in range(2)]  # 5 GB each
+    scales = [torch.empty(pages, 8, device=DEV) for _ in range(2)]
+    c = m.KVCache(*codes, *scales, n_q_heads=8, max_seqs=1, max_tokens=1, max_kv_len=1)
+    ends = [0, 1, 16384, pages - 2, pages - 1]
+    for x in codes + scales:
+        for i in ends:
+            x[i] = torch.randint(0, 256, x.shape[1:], device=DEV).to(x.dtype)
+    want = [[x[i].clone() for i in ends] for x in codes + scales]
+    c.copy(t([(pages - 1, 1, page), (0, pages - 2, page), (16384, 20000, 5)]))
+    for x, (a, _, mid, _, z) in zip(codes + scales, want):
+        assert torch.equal(x[1], z) and torch.equal(x[pages - 2], a) and torch.equal(x[pages - 1], z) and torch.equal(x[0], a)
+        part = slice(None) if x.dim() == 2 else (slice(None), slice(0, 5))
+        assert torch.equal(x[20000][part], mid[part])
     assert c.device_status() == 0
 
 

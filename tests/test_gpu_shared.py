@@ -188,6 +188,34 @@ def test_wild_scales(m, monkeypatch):
 
 
 @pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_a_query_that_is_not_finite_stays_in_its_row(m, new, bad):
+    k = Case(m, [(300, [(new, new), (new + 50, new), (new, new)])], 64, 2, 8, 16, seed=11)
+    want = k.c.attend(k.q, k.bt.b, prefix=k.share)
+    k.q[new, 3, 17] = bad
+    out = k.c.attend(k.q, k.bt.b, prefix=k.share)
+    assert out[new, 3].isnan().all()
+    out[new, 3] = want[new, 3]
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dim,new", [(64, 1), (128, 1), (64, 9), (128, 30)])
+def test_far_pages(m, monkeypatch, dim, new):
+    """Pages whose codes lie beyond 2^31 bytes, of the prefix and of the sequences."""
+    k = Case(m, [(200, [(new + 3, new), (new, new), (new + 140, new)])], dim, 8, 8, 128, seed=13, junk=False)
+    far = (1 << 32) // (8 * 128 * dim) + 17  # pages behind 4 GB
+    codes = [torch.zeros(far + k.bt.n_pages, 8, 128, dim, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    scales = [torch.ones(far + k.bt.n_pages, 8, device=DEV) for _ in range(2)]
+    for big, small in zip(codes + scales, (k.c.k_codes, k.c.v_codes, k.c.k_scale, k.c.v_scale)):
+        big[far:] = small
+    want = k.c.attend(k.q, k.bt.b, prefix=k.share)
+    c = m.KVCache(*codes, *scales, n_q_heads=8, max_seqs=3, max_tokens=k.bt.cu[-1], max_kv_len=512)
+    for table in (k.bt.b.page_table, k.share.page_table):
+        table += far
+    assert torch.equal(c.attend(k.q, k.bt.b, prefix=k.share), want) and c.device_status() == 0
+
+
+@pytest.mark.parametrize("new", [1, 40])
 def test_strided_queries_and_given_results(m, new):
     k = Case(m, [(300, [(new, new), (new + 50, new)])], 64, 2, 8, 16, seed=4)
     want = k.c.attend(k.q, k.bt.b, prefix=k.share)
