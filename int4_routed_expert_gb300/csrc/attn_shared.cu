@@ -10,6 +10,8 @@
 // a last kernel joins them, own splits first, in their order.
 // The three launches overlap: the second does not need the first and begins as its
 // CTAs leave SMs, the third is in place when they end.
+#include <cmath>
+
 #include "attn_tc.cuh"
 
 namespace moe {
@@ -23,6 +25,7 @@ struct Side {
   bool few;
   int rows;    // of a row tile
   int parts;   // results of a split: two where both M tiles have the same rows
+  int ctas;    // not 0: the prefixes' work is dealt out to so many CTAs, pl.splits parts a row tile at most
   size_t cap;  // rows of results
 };
 
@@ -46,6 +49,7 @@ Side side_of(const KvView& c, int G, double& live) {
   x.few = rows <= 32;  // as moe_kv_attend chooses
   x.rows = x.few ? (rows <= 16 ? 16 : 32) : 256;
   x.parts = !x.few && rows <= 128 ? 2 : 1;
+  x.ctas = 0;
   x.pl.row_tiles = static_cast<int>((rows + x.rows - 1) / x.rows);
   // the sequences' rows add up to the call's, and half a tile of each is empty
   live = std::min(static_cast<double>(x.pl.row_tiles) * c.n_seqs, static_cast<double>(all) / x.rows + 0.5 * c.n_seqs + 0.5) *
@@ -75,12 +79,13 @@ struct Sides {
   Side own, shared;
   bool wide;  // few rows: the join has a CTA for each
 };
-// The splits of the keys.  A launch over own tokens fills the SMs that the one over the
-// prefixes leaves, so that one's splits go by the time of both: that of its longest CTAs,
-// or all CTAs' time over the SMs, whichever is longer, and what a split more costs the join.
-// (64 tokens on a prefix of 16384, 64 / 8 heads: 78 us at 4 to 6 splits, 87 us at 9, where
-// the prefix alone is fastest; 37 x 4 tokens on three of up to 66001, 48 / 4 heads: 265 us at
-// 4 splits, 338 us at 6, whose second round of CTAs is a quarter full.)
+// How the keys are cut.  The launch over own tokens fills the SMs that the one over the
+// prefixes leaves, so that one's CTAs go by the time of both: that of the longest ones, or
+// all CTAs' time over the SMs, whichever is longer, and what a split more costs the join.
+// The splits are alike, or (more than 128 rows, up to 32 groups) the row tiles' keys are
+// dealt out evenly to CTAs that go from one to the next, which costs some at each change.  (37 x 4 tokens on three prefixes of up to 66001, 48 / 4 heads, in splits: 265 us at
+// 4, 338 us at 6, whose second round of CTAs is a quarter full; dealt out 224 us.
+// 5085 tokens of 12 questions on 24001, 32 / 2 heads of 64: 1546 us in 2 splits, 1437 us dealt out.)
 Sides sides_of(const KvView& c, const Share& sh, int G, int n_sm) {
   constexpr int64_t kMost = 1 << 20;  // rows of results a side, where one split has fewer
   const int64_t rows = static_cast<int64_t>(c.n_tokens) * c.hkv * G;
@@ -116,6 +121,28 @@ Sides sides_of(const KvView& c, const Share& sh, int G, int n_sm) {
     if (time < least) least = time, best = k;
   }
   set_splits(s.shared, c, G, tiles, best);
+  if (s.shared.few || s.shared.parts > 1 || sh.n_groups > 32 ||
+      (live + sh.n_groups * c.hkv) * static_cast<double>(tiles) > 1e9)  // (units are counted in 32 bits)
+    return s;
+  const double units = live * static_cast<double>(tiles);
+  int64_t ctas = 0;
+  // (splits that are alike are so of groups that are not)
+  if (sh.n_groups > 1) least += 0.15 * cost.tile * static_cast<double>(s.shared.pl.tiles_per_split);
+  for (int64_t k = 1; k <= n_sm; ++k) {
+    const double per = static_cast<double>(static_cast<int64_t>(units / static_cast<double>(k)) + 1);
+    // (the deal itself, and half a beginning and end for each row tile but the first)
+    const double cta = cost.tile * per + cost.start + 1.5 + 0.5 * cost.start * (1 + std::floor(per / static_cast<double>(tiles)));
+    const double time = std::max(cta, (cta * static_cast<double>(k) + own_time) / n_sm) + join * (static_cast<double>(k) / live + 1);
+    if (time < least) least = time, ctas = k;
+  }
+  if (ctas) {
+    s.shared.ctas = static_cast<int>(ctas);
+    // parts of a row tile: its keys over a CTA's, and one more where it begins within a CTA's;
+    // half as much again, as the rows and lengths may be fewer than the host knows
+    const int64_t parts = static_cast<int64_t>(1.5 * static_cast<double>(ctas) / live) + 3;
+    s.shared.pl.splits = static_cast<int>(std::max<int64_t>(std::min(parts, kMost / rows), 2));
+    s.shared.cap = static_cast<size_t>(s.shared.pl.splits) * rows;
+  }
   return s;
 }
 
@@ -154,8 +181,9 @@ struct RowSum {
 
 // A CTA joins a slice of the heads of one token, D / 4 threads a row.  WIDE: the whole CTA
 // a row, D / 4 threads every eighth (heads of 64: sixteenth) of its results, whose sums are
-// joined once more: for calls of few rows, whose keys are cut into many splits.
-template <int D, bool WIDE>
+// joined once more: for calls of few rows, whose keys are cut into many splits.  DEALT: the
+// prefixes' results are of dealt out work.
+template <int D, bool WIDE, bool DEALT>
 __global__ void __launch_bounds__(kJoinThreads)
     join_kernel(const KvView c, const AttnArgs a, const Share sh, const Side own, const Side shared, const AttnWs own_ws,
                 const AttnWs shared_ws, int slices) {
@@ -166,8 +194,16 @@ __global__ void __launch_bounds__(kJoinThreads)
   InGroup in = group_of(sh, b);
   const bool covered = load_seq(c, b, q) && t >= q.q0 && t < q.q0 + q.n;
   const int begin = covered ? own_begin(sh, q, in) : 0;
-  int n_shared = 0, per;
-  if (covered && in.g >= 0 && load_group(c, sh, in.g, g)) {
+  int n_shared = 0, per, before = 0, g_tiles = 0, g_per = 1;
+  if constexpr (DEALT) {
+    const Dealt d = deal_out(c, a, sh, shared.ctas, shared.pl.splits);
+    const int lane_of = max(in.g, 0);
+    before = __shfl_sync(0xffffffffu, d.before, lane_of);
+    g_tiles = __shfl_sync(0xffffffffu, d.n_t, lane_of);
+    g.q0 = __shfl_sync(0xffffffffu, d.q.q0, lane_of);
+    g_per = d.per;
+    if (!covered || in.g < 0) g_tiles = 0;
+  } else if (covered && in.g >= 0 && load_group(c, sh, in.g, g)) {
     split_tiles(shared.pl, (g.L + kKeys - 1) / kKeys, n_shared, per);
     n_shared *= shared.parts;
   }
@@ -183,6 +219,10 @@ __global__ void __launch_bounds__(kJoinThreads)
     int n_own;
     split_tiles(own.pl, own_tiles(a, q.L, begin, q.L - q.n + last), n_own, per);
     n_own *= own.parts;
+    if (DEALT && g_tiles > 0) {  // the CTAs that its row tile's units went to
+      const int unit = before + (((t - g.q0) * a.G + h - hk * a.G) / 256 * c.hkv + hk) * g_tiles;
+      n_shared = (unit + g_tiles - 1) / g_per - unit / g_per + 1;
+    }
     const size_t step = static_cast<size_t>(c.hkv) * c.n_tokens * a.G;
     const size_t first = (static_cast<size_t>(hk) * c.n_tokens + t) * a.G + h - hk * a.G;
     const int all = n_own + n_shared, mine = WIDE ? max((all - grp + kPer - 1) / kPer, 0) : all;
@@ -235,16 +275,21 @@ cudaError_t attn_shared_launch(const KvView& c, const AttnArgs& a, const Share& 
   const AttnWs own = side_ws(x.own, c.D, base), shared = side_ws(x.shared, c.D, base + side_bytes(x.own, c.D));
   AttnArgs all = a;
   all.causal = 0;
-  cudaError_t e = (x.shared.few ? attn_few_part_launch : attn_tiles_part_launch)(x.prefix, all, shared, x.shared.pl, sh,
-                                                                                 true, maps, s);
+  cudaError_t e = x.shared.few
+                      ? attn_few_part_launch(x.prefix, all, shared, x.shared.pl, sh, true, maps, s)
+                      : attn_tiles_part_launch(x.prefix, all, shared, x.shared.pl, sh, true, x.shared.ctas, maps, s);
   if (e != cudaSuccess) return e;
-  e = (x.own.few ? attn_few_part_launch : attn_tiles_part_launch)(c, a, own, x.own.pl, sh, false, maps, s);
+  e = x.own.few ? attn_few_part_launch(c, a, own, x.own.pl, sh, false, maps, s)
+                : attn_tiles_part_launch(c, a, own, x.own.pl, sh, false, 0, maps, s);
   if (e != cudaSuccess) return e;
   // a CTA for a pass of its threads over heads, while that is not more than the SMs hold at once
   const int64_t per = x.wide ? 1 : kJoinThreads / (c.D / 4), passes = (a.hq + per - 1) / per;
   const int64_t slices = x.wide ? passes : std::max<int64_t>(1, std::min<int64_t>(passes, 8LL * n_sm / c.n_tokens));
-  auto join = c.D == 128 ? (x.wide ? join_kernel<128, true> : join_kernel<128, false>)
-                         : (x.wide ? join_kernel<64, true> : join_kernel<64, false>);
+  const bool dealt = x.shared.ctas != 0;
+  auto join = c.D == 128 ? (x.wide ? (dealt ? join_kernel<128, true, true> : join_kernel<128, true, false>)
+                                   : (dealt ? join_kernel<128, false, true> : join_kernel<128, false, false>))
+                         : (x.wide ? (dealt ? join_kernel<64, true, true> : join_kernel<64, true, false>)
+                                   : (dealt ? join_kernel<64, false, true> : join_kernel<64, false, false>));
   return launch_kernel(join, c.n_tokens * slices, kJoinThreads, 0, s, true, c, a, sh, x.own, x.shared, own, shared,
                        static_cast<int>(slices));
 }

@@ -225,11 +225,12 @@ struct TileIo {
   // tiles ahead and its scales one tile ahead.  k_empty[s] is passed on by
   // the softmax, which then also is through with the scales of the tile
   // kConstRing - KS before.
-  __device__ __forceinline__ void load(const KvView& c, const AttnArgs& a, const KeyTiles& kt, int b, int hk,
+  // j0: tiles that the CTA has had before (of other rows).  False when a wait gave up.
+  __device__ __forceinline__ bool load(const KvView& c, const AttnArgs& a, const KeyTiles& kt, int b, int hk,
                                        int t_begin, int n, const CUtensorMap* k_map, const CUtensorMap* v_map,
-                                       int lane) const {
+                                       int lane, int j0 = 0) const {
     static_assert(kConstRing > KS, "the ring outlives the key stages");
-    const int t_end = t_begin + n;
+    const int t_end = t_begin + n, j_end = j0 + n;
     bool ok = true, bad = false, odd = false;
     const int per = c.page >> 4;  // groups of a page
     const uint32_t bytes = static_cast<uint32_t>(c.page) * D;
@@ -251,12 +252,12 @@ struct TileIo {
     };
     float kscale, vscale;
     int page = take(entry(t_begin), kscale, vscale), raw1 = entry(t_begin + 1);
-    int k_sent = 0, r_sent = 0;  // tiles whose copies are on their way
-    for (int j = 0; j < n; ++j) {
+    int k_sent = j0, r_sent = j0;  // tiles whose copies are on their way
+    for (int j = j0; j < j_end; ++j) {
       const int ks = j % KS, rs = j % RS;
       float kscale1, vscale1;
       const int page1 = take(raw1, kscale1, vscale1);
-      raw1 = entry(t_begin + j + 2);
+      raw1 = entry(t_begin + j - j0 + 2);
       const bool copies = page >= 0 && (lane & (per - 1)) == 0;
       const uint32_t total = __popc(__ballot_sync(0xffu, copies)) * bytes;
       ok = j < KS || mbar_wait(k_empty + 8 * ks, (j / KS - 1) & 1, c.err);
@@ -293,14 +294,15 @@ struct TileIo {
     }
     if (bad) atomicOr(c.err, kErrBadBatch);
     if (odd) atomicOr(c.err, kErrNonFinite);
+    return ok;
   }
 
   // CT threads: value codes to f16.  Thread t takes 16-byte chunk t % (D / 16)
   // of keys t / (D / 16) + 0, kPer, ...; a chunk becomes two of the operand's.
   // free(j) waits until the product that read the stage of tile j - VS is done.
   template <typename Free>
-  __device__ __forceinline__ void convert(const KvView& c, const AttnArgs& a, const KeyTiles& kt, int t_begin, int n,
-                                          int tid, Free free) const {
+  __device__ __forceinline__ bool convert(const KvView& c, const AttnArgs& a, const KeyTiles& kt, int t_begin, int n,
+                                          int tid, Free free, int j0 = 0) const {
     constexpr int kChunks = D / 16, kPer = CT / kChunks;
     const int ch = tid % kChunks, row0 = tid / kChunks;
     // the two halves' lanes store their two chunks in opposite order: no bank conflicts
@@ -308,10 +310,10 @@ struct TileIo {
     const uint32_t out = (ch >> 2) * kHalf + row0 * 128;
     const uint32_t o0 = out + ((c0 ^ (row0 & 7)) << 4), o1 = out + (((c0 ^ 1) ^ (row0 & 7)) << 4);
     const bool swap = (ch >> 2) != 0;
-    for (int j = 0; j < n; ++j) {
+    for (int j = j0, j_end = j0 + n; j < j_end; ++j) {
       const int rs = j % RS, vs = j % VS;
-      if (!mbar_wait(r_full + 8 * rs, (j / RS) & 1, c.err) || (j >= VS && !free(j))) break;
-      const int base_key = kt.base(t_begin + j);
+      if (!mbar_wait(r_full + 8 * rs, (j / RS) & 1, c.err) || (j >= VS && !free(j))) return false;
+      const int base_key = kt.base(t_begin + j - j0);
       const bool whole = base_key + kKeys <= kt.hi && (base_key >= kt.lo || base_key + kKeys <= a.sinks);
       const char* src = smem + (raw - base) + rs * kMat8 + tid * 16;
       const char* src0 = src + (swap ? 8 : 0);
@@ -339,6 +341,7 @@ struct TileIo {
       mbar_arrive(v_full + 8 * vs);
       mbar_arrive(r_empty + 8 * rs);
     }
+    return true;
   }
 };
 
@@ -358,9 +361,9 @@ struct Plan {
 };
 
 // Which of a row's keys a launch is about: all; those behind its sequence's prefix; those
-// of the prefix, where a group of sequences takes the place of one.  The last two leave
-// partial results alone.
-enum class Part { kAll, kOwn, kPrefix };
+// of the prefix, where a group of sequences takes the place of one; the same, dealt out
+// evenly (Dealt).  The last three leave partial results alone.
+enum class Part { kAll, kOwn, kPrefix, kDealt };
 
 // What a kernel's CTAs cost, in the time that a CTA with an SM of its own takes
 // for a tile of keys.
@@ -524,6 +527,39 @@ __device__ __forceinline__ bool work_of(const KvView& c, const AttnArgs& a, cons
   return true;
 }
 
+// The prefixes' work dealt out evenly.  A group's row tiles (256 rows) and kv heads have
+// n_t tiles of keys each, one behind the other: rt * hkv + hk has the units
+//   before + (rt * hkv + hk) * n_t ...,
+// and CTA x takes the units from x * per on, whichever rows they are of: what a row tile
+// gets from one CTA is a part of its results.
+struct Dealt {
+  int before, n_t;  // of the lane's group
+  Seq q;
+  int per, total;   // of all
+};
+// `most`: the most parts of a row tile.
+__device__ __forceinline__ Dealt deal_out(const KvView& c, const AttnArgs& a, const Share& sh, int ctas, int most) {
+  const int lane = threadIdx.x & 31;
+  Dealt d{0, 0, {0, 0, 0}, 0, 0};
+  int units = 0;
+  if (lane < sh.n_groups && load_group(c, sh, lane, d.q)) {
+    d.n_t = (d.q.L + kKeys - 1) / kKeys;
+    units = (d.q.n * a.G + 255) / 256 * c.hkv * d.n_t;
+  }
+  int up = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, up, o);
+    if (lane >= o) up += y;
+  }
+  d.before = up - units;
+  d.total = __shfl_sync(0xffffffffu, up, 31);
+  const int longest = __reduce_max_sync(0xffffffffu, units ? d.n_t : 0);
+  d.per = max(max((d.total + ctas - 1) / ctas, (longest + most - 2) / (most - 1)), 1);
+  if (!units) d.n_t = 0;
+  return d;
+}
+
 // A launch over the rows' own keys may begin while the one over the prefixes runs, and does
 // not wait for it; the join behind both waits for this one alone.  So its last CTA ends
 // with the other launch.
@@ -553,7 +589,8 @@ cudaError_t launch_kernel(void (*kernel)(Params...), int64_t grid, int threads, 
 // The two kernels' launches over parts of the keys (attn_shared.cu).
 cudaError_t attn_few_part_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,
                                  bool prefix, const KvMaps& maps, cudaStream_t s);
+// (ctas: prefixes of more than 128 rows a kv head dealt out to so many CTAs, at most pl.splits parts a row tile)
 cudaError_t attn_tiles_part_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,
-                                   bool prefix, const KvMaps& maps, cudaStream_t s);
+                                   bool prefix, int ctas, const KvMaps& maps, cudaStream_t s);
 
 }  // namespace moe

@@ -92,6 +92,8 @@ enum Bar {
 // its own, which the join takes for two splits: one's softmax still runs under
 // the other's products.  48 rows a kv head (four sequences of up to 131072
 // keys, 4 kv heads): 142 us, and 198 us as one M tile.
+// Part::kDealt: a CTA goes from one piece of the dealt out work to the next; the load warp
+// brings the next piece's keys while the last one's results are written.
 template <int D, bool DUAL, Part PART>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tiles_kernel(const KvView c, const AttnArgs a, const AttnWs ws, const Plan pl, const Share sh,
@@ -104,23 +106,63 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), wg = warp >> 2, lane = threadIdx.x & 31;
 
   if constexpr (PART != Part::kAll) pdl_launch_dependents();
-  // long tiles first: the last rows of a causal prompt see the most keys
-  int idx = blockIdx.x;
-  const int hk = idx % c.hkv;
-  idx /= c.hkv;
-  const int b = idx % c.n_seqs;
-  idx /= c.n_seqs;
-  const int split = idx % pl.splits;
-  const int rt = pl.row_tiles - 1 - idx / pl.splits;
+  constexpr bool kDealt = PART == Part::kDealt;  // the CTA takes its piece of all groups' work
+  __shared__ int4 s_group[kDealt ? 32 : 1];      // first token, tokens, length, units before
+  __shared__ int s_per;
   Work w;
-  if (!work_of<PART>(c, a, pl, sh, kRows, b, hk, rt, w) || split >= w.n_split) {
-    end_of_part<PART>();
-    return;
+  int hk, b, rt, split, t_begin, n;  // n: tiles, 0 when the rows see nothing
+  int unit = 0, unit_end = 0;        // of the dealt work
+  // The next row tile and its keys, of those that are the CTA's.
+  auto next = [&]() {
+    if (unit >= unit_end) return false;
+    const int4 mine = s_group[lane];
+    // (groups without work begin where the next one does: the last one that begins here has some)
+    const uint32_t begun = __ballot_sync(0xffffffffu, mine.z > 0 && mine.w <= unit);
+    b = 31 - __clz(begun);
+    const int4 g = s_group[b];
+    w.q = Seq{g.x, g.y, g.z};
+    w.k = key_tiles<kKeys>(a, g.z, 0, 0);
+    const int tile = (unit - g.w) / w.k.n_t;
+    rt = tile / c.hkv;
+    hk = tile - rt * c.hkv;
+    w.b = b, w.hk = hk;
+    w.r0 = rt * kRows;
+    w.r1 = min(w.q.n * a.G, w.r0 + kRows);
+    w.base_p = w.p_lo = w.p_hi = 0;  // (without the causal mask)
+    w.tok0 = w.r0 / a.G;
+    w.rem0 = w.r0 - w.tok0 * a.G;
+    const int first = g.w + tile * w.k.n_t;
+    t_begin = unit - first;
+    n = min(w.k.n_t - t_begin, unit_end - unit);
+    split = blockIdx.x - first / s_per;
+    unit += n;
+    return true;
+  };
+  if constexpr (kDealt) {
+    const Dealt d = deal_out(c, a, sh, gridDim.x, pl.splits);
+    if (warp == 0) s_group[lane] = make_int4(d.q.q0, d.q.n, d.n_t > 0 ? d.q.L : 0, d.before);
+    if (threadIdx.x == 0) s_per = d.per;
+    unit = min(static_cast<int64_t>(blockIdx.x) * d.per, static_cast<int64_t>(d.total));
+    unit_end = min(unit + d.per, d.total);
+    __syncthreads();
+    if (!next()) return;
+  } else {
+    // long tiles first: the last rows of a causal prompt see the most keys
+    int idx = blockIdx.x;
+    hk = idx % c.hkv;
+    idx /= c.hkv;
+    b = idx % c.n_seqs;
+    idx /= c.n_seqs;
+    split = idx % pl.splits;
+    rt = pl.row_tiles - 1 - idx / pl.splits;
+    if (!work_of<PART>(c, a, pl, sh, kRows, b, hk, rt, w) || split >= w.n_split) {
+      end_of_part<PART>();
+      return;
+    }
+    t_begin = split * w.tiles_per_split;
+    n = min(w.k.n_t, t_begin + w.tiles_per_split) - t_begin;
   }
-  const int t_begin = split * w.tiles_per_split;
-  const int t_end = min(w.k.n_t, t_begin + w.tiles_per_split);
-  const int n = t_end - t_begin;  // 0 when the rows see nothing
-  const int n_mt = DUAL || w.r1 - w.r0 > kM ? 2 : 1;
+  const int n_mt = kDealt || DUAL || w.r1 - w.r0 > kM ? 2 : 1;
 
   // The softmax warps' queries are on their way while all else is set up, each
   // row to where its two terms will stand.  (This loop and the next two that run
@@ -130,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int sub = lane / kLanes, part = lane % kLanes, wrow = (warp & 7) * 16;
   const uint32_t q_tile = L_::kQ + (DUAL ? 0 : warp >> 3) * 2 * L_::kMat8;
   const uint32_t q_raw = q_tile + part / (D / 16) * L_::kMat8;
-  if (n > 0 && warp < (DUAL ? 8 : 8 * n_mt)) {
+  auto load_queries = [&]() {
 #pragma unroll 2
     for (int x = 0; x < kIts; ++x) {
       const int r = wrow + x * kPer + sub, i = (DUAL ? 0 : (warp >> 3) * kM) + r;  // row of the M tile, of the CTA
@@ -142,7 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                      8 * part,
                  in ? 16 : 0);
     }
-  }
+  };
+  if (n > 0 && warp < (DUAL ? 8 : 8 * n_mt)) load_queries();
 
   auto bar = [&](int i) { return base_u + L_::kBar + 8 * i; };
   if (threadIdx.x == 0) {
@@ -163,317 +206,340 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const Io<D> io{base_u + L_::kK, base_u + L_::kRaw, base_u + L_::kV, smem, base_u, base_u + L_::kConst,
                  bar(kKFull), bar(kKEmpty), bar(kRFull), bar(kREmpty), bar(kVFull), bar(kCFull)};
+  // Each role goes through the CTA's pieces by itself (dealt work; else there is one): j0
+  // tiles have been before, so that stages and barriers go on as in one long walk over keys.
+  int j0 = 0, piece = 0;
+  auto go_on = [&](bool ok) {
+    if (!kDealt || !ok) return false;
+    j0 += n, ++piece;
+    return next();
+  };
   if (warp == kMmaWarp + 1) {
-    if (lane < 8 && n > 0) io.load(c, a, w.k, b, hk, t_begin, n, &k_map, nullptr, lane);
+    bool ok = true;
+    do {
+      if (lane < 8 && n > 0) ok = io.load(c, a, w.k, b, hk, t_begin, n, &k_map, nullptr, lane, j0);
+    } while (go_on(kDealt && __all_sync(0xffffffffu, ok)));
   } else if (warp == kMmaWarp) {
-    if (lane == 0 && n > 0) {
-      constexpr uint32_t id_s = idesc_f16(kM, kKeys);           // e4m3 is format 0 of its kind, too
-      constexpr uint32_t id_o = idesc_f16(kM, D) | (1u << 16);  // V is MN-major
-      const uint64_t q_desc = sdesc_k<D>(base_u + L_::kQ), k_desc = sdesc_k<D>(base_u + L_::kK);
-      const uint64_t v_desc = sdesc_sw128_mn(base_u + L_::kV, Io<D>::kHalf);
-      auto issue_s = [&](int i, int stage) {
-        mma_s<D>(tmem + i * 128, q_desc + (DUAL ? 0 : i) * (2 * L_::kMat8 >> 4),
-                 k_desc + stage * (L_::kMat8 >> 4), id_s);
-        mma_commit(bar(kSFull + i));
-      };
-      auto k_wait = [&](int j) { return mbar_wait(bar(kKFull + j % kKStages), (j / kKStages) & 1, c.err); };
-      auto issue_o = [&](int i, int j, bool first) {
-        const uint32_t ot = tmem + 256 + i * 128, pt = tmem + i * 128 + kPAt;
-        const uint64_t vd = v_desc + (j & 1) * (L_::kMat >> 4);
-        mma_o(ot, pt, vd, id_o, first);
-        mma_o(ot, pt + 64, vd + (64 * 128 >> 4), id_o, 0);  // P's halves stand as far apart as S's
-      };
-      bool ok = mbar_wait(bar(kQFull), 0, c.err) && k_wait(0);
-      if (ok) {
-        fence_after_sync();
-        issue_s(0, 0);
-        if (!DUAL && n_mt == 2) issue_s(1, 0);
-        mma_commit(bar(kKEmpty));
-      }
-      if (DUAL && ok && n > 1 && (ok = k_wait(1))) {
-        fence_after_sync();
-        issue_s(1, 1);
-        mma_commit(bar(kKEmpty + 1));
-      }
-      // S of tile j + 1 goes straight behind O += P V of tile j, whose P it
-      // overwrites: one thread's products run on the tensor pipe in the order of
-      // their issue.  (Waiting for the product before issuing S costs a commit's
-      // and a wait's latency, about 1000 clocks a tile: prompt of 8192, 822 us
-      // to 1009 us; with a thread that looks in turn which M tile can go on,
-      // 695 us to 884 us.)
-      for (int j = 0; DUAL && ok && j < n; ++j) {
-        const int i = j & 1, next = j + 2;
-        ok = mbar_wait(bar(kPFull + i), (j >> 1) & 1, c.err) && mbar_wait(bar(kVFull + i), (j >> 1) & 1, c.err);
-        if (!ok) break;
-        fence_after_sync();
-        issue_o(i, j, j < 2);
-        mma_commit(bar(kVEmpty + i));
-        if (next >= n) {
-          mma_commit(bar(kOFull + i));
-        } else if ((ok = k_wait(next))) {
+    bool ok = true;
+    do {
+      if (lane == 0 && n > 0) {
+        constexpr uint32_t id_s = idesc_f16(kM, kKeys);           // e4m3 is format 0 of its kind, too
+        constexpr uint32_t id_o = idesc_f16(kM, D) | (1u << 16);  // V is MN-major
+        const uint64_t q_desc = sdesc_k<D>(base_u + L_::kQ), k_desc = sdesc_k<D>(base_u + L_::kK);
+        const uint64_t v_desc = sdesc_sw128_mn(base_u + L_::kV, Io<D>::kHalf);
+        auto issue_s = [&](int i, int stage) {
+          mma_s<D>(tmem + i * 128, q_desc + (DUAL ? 0 : i) * (2 * L_::kMat8 >> 4),
+                   k_desc + stage * (L_::kMat8 >> 4), id_s);
+          mma_commit(bar(kSFull + i));
+        };
+        auto k_wait = [&](int j) { return mbar_wait(bar(kKFull + j % kKStages), (j / kKStages) & 1, c.err); };
+        auto issue_o = [&](int i, int j, bool first) {
+          const uint32_t ot = tmem + 256 + i * 128, pt = tmem + i * 128 + kPAt;
+          const uint64_t vd = v_desc + (j & 1) * (L_::kMat >> 4);
+          mma_o(ot, pt, vd, id_o, first);
+          mma_o(ot, pt + 64, vd + (64 * 128 >> 4), id_o, 0);  // P's halves stand as far apart as S's
+        };
+        ok = mbar_wait(bar(kQFull), piece & 1, c.err) && k_wait(j0);
+        if (ok) {
           fence_after_sync();
-          issue_s(i, next % kKStages);
-          mma_commit(bar(kKEmpty + next % kKStages));
+          issue_s(0, j0 % kKStages);
+          if (!DUAL && n_mt == 2) issue_s(1, j0 % kKStages);
+          mma_commit(bar(kKEmpty + j0 % kKStages));
         }
-      }
-      for (int j = 0; !DUAL && ok && j < n; ++j) {
-        for (int i = 0; ok && i < n_mt; ++i) {
-          ok = mbar_wait(bar(kPFull + i), j & 1, c.err) &&
-               (i > 0 || mbar_wait(bar(kVFull + (j & 1)), (j >> 1) & 1, c.err));
+        if (DUAL && ok && n > 1 && (ok = k_wait(1))) {
+          fence_after_sync();
+          issue_s(1, 1);
+          mma_commit(bar(kKEmpty + 1));
+        }
+        // S of tile j + 1 goes straight behind O += P V of tile j, whose P it
+        // overwrites: one thread's products run on the tensor pipe in the order of
+        // their issue.  (Waiting for the product before issuing S costs a commit's
+        // and a wait's latency, about 1000 clocks a tile: prompt of 8192, 822 us
+        // to 1009 us; with a thread that looks in turn which M tile can go on,
+        // 695 us to 884 us.)
+        for (int j = 0; DUAL && ok && j < n; ++j) {
+          const int i = j & 1, next = j + 2;
+          ok = mbar_wait(bar(kPFull + i), (j >> 1) & 1, c.err) && mbar_wait(bar(kVFull + i), (j >> 1) & 1, c.err);
           if (!ok) break;
           fence_after_sync();
-          issue_o(i, j, j == 0);
-          if (i == n_mt - 1) mma_commit(bar(kVEmpty + (j & 1)));
-          if (j == n - 1) {
+          issue_o(i, j, j < 2);
+          mma_commit(bar(kVEmpty + i));
+          if (next >= n) {
             mma_commit(bar(kOFull + i));
-          } else if ((ok = i > 0 || k_wait(j + 1))) {
+          } else if ((ok = k_wait(next))) {
             fence_after_sync();
-            issue_s(i, (j + 1) % kKStages);
-            if (i == n_mt - 1) mma_commit(bar(kKEmpty + (j + 1) % kKStages));
+            issue_s(i, next % kKStages);
+            mma_commit(bar(kKEmpty + next % kKStages));
           }
         }
+        for (int j = j0, j_end = j0 + n; !DUAL && ok && j < j_end; ++j) {
+          for (int i = 0; ok && i < n_mt; ++i) {
+            ok = mbar_wait(bar(kPFull + i), j & 1, c.err) &&
+                 (i > 0 || mbar_wait(bar(kVFull + (j & 1)), (j >> 1) & 1, c.err));
+            if (!ok) break;
+            fence_after_sync();
+            issue_o(i, j, j == j0);
+            if (i == n_mt - 1) mma_commit(bar(kVEmpty + (j & 1)));
+            if (j == j_end - 1) {
+              mma_commit(bar(kOFull + i));
+            } else if ((ok = i > 0 || k_wait(j + 1))) {
+              fence_after_sync();
+              issue_s(i, (j + 1) % kKStages);
+              if (i == n_mt - 1) mma_commit(bar(kKEmpty + (j + 1) % kKStages));
+            }
+          }
+        }
+        if (!ok) {
+          // what was issued ends by itself; wait for it before the tensor memory goes back
+          mma_commit(bar(kDrain));
+          mbar_wait(bar(kDrain), 0, c.err);
+        }
       }
-      if (!ok) {
-        // what was issued ends by itself; wait for it before the tensor memory goes back
-        mma_commit(bar(kDrain));
-        mbar_wait(bar(kDrain), 0, c.err);
-      }
-    }
+    } while (go_on(kDealt && __shfl_sync(0xffffffffu, ok, 0)));
   } else if (wg == 4) {
-    io.convert(c, a, w.k, t_begin, n, threadIdx.x - kSoftmax,
-               [&](int j) { return mbar_wait(bar(kVEmpty + (j & 1)), ((j >> 1) & 1) ^ 1, c.err); });
+    bool ok = true;
+    do {
+      ok = io.convert(c, a, w.k, t_begin, n, threadIdx.x - kSoftmax,
+                      [&](int j) { return mbar_wait(bar(kVEmpty + (j & 1)), ((j >> 1) & 1) ^ 1, c.err); }, j0);
+    } while (go_on(kDealt && __all_sync(0xffffffffu, ok)));
   } else if ((wg >> 1) < n_mt) {
     const int i = wg >> 1, half = wg & 1, row = threadIdx.x & 127;  // M tile, half of the keys
-    const int row0 = w.r0 + (DUAL ? 0 : i * kM);  // of the M tile
-    const int r = row0 + row;
-    const bool live = r < w.r1;
-    int tok = 0, head = 0;
-    if (live) w.row(a, r - w.r0, tok, head);
-    head += hk * a.G;
-    const RowSees sees = row_sees(a, w.q.L, w.base_p + tok, live, PART == Part::kOwn ? w.k.lo : 0);
-    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 * (warp % 4)
-    const uint32_t ts = tmem + i * 128 + lanes + half * 64, to = tmem + 256 + i * 128 + lanes + half * (D / 2);
-    // What the row's two threads tell each other, two buffers in turn.  A warp
-    // whose wait gave up waits no more but still comes to every barrier, and the
-    // loop ends for all.
     bool ok = true;
-    float* pair = reinterpret_cast<float*>(smem + L_::kPair) + i * 512;
-    const int mine = DUAL ? (n + 1 - i) >> 1 : n;  // tiles of this M tile
-    auto other = [&](int buf, float mine) {
-      pair[buf * 256 + half * 128 + row] = mine;
-      ok = !named_vote(1 + i, 256, !ok);
-      return pair[buf * 256 + (half ^ 1) * 128 + row];
-    };
-    float m = -INFINITY, l = 0.f, lscale = 0.f;  // lscale >= 0: a negative scale turns the query's sign
-    if (n > 0 && (!DUAL || i == 0)) {
-      // The rows' queries, each brought to [2^7, 2^8) by a power of two, as two
-      // e4m3 terms: a warp takes 16 of the M tile's rows, D / 8 lanes a row.
-      char* dst = smem + q_tile;
-      asm volatile("cp.async.wait_all;" ::: "memory");
+    for (;;) {
+      const int row0 = w.r0 + (DUAL ? 0 : i * kM);  // of the M tile
+      const int r = row0 + row;
+      const bool live = r < w.r1;
+      int tok = 0, head = 0;
+      if (live) w.row(a, r - w.r0, tok, head);
+      head += hk * a.G;
+      const RowSees sees = row_sees(a, w.q.L, w.base_p + tok, live, PART == Part::kOwn ? w.k.lo : 0);
+      const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 * (warp % 4)
+      const uint32_t ts = tmem + i * 128 + lanes + half * 64, to = tmem + 256 + i * 128 + lanes + half * (D / 2);
+      // What the row's two threads tell each other, two buffers in turn.  A warp
+      // whose wait gave up waits no more but still comes to every barrier, and the
+      // loop ends for all.
+      float* pair = reinterpret_cast<float*>(smem + L_::kPair) + i * 512;
+      const int mine = DUAL ? (n + 1 - i) >> 1 : n;  // tiles of this M tile
+      auto other = [&](int buf, float mine) {
+        pair[buf * 256 + half * 128 + row] = mine;
+        ok = !named_vote(1 + i, 256, !ok);
+        return pair[buf * 256 + (half ^ 1) * 128 + row];
+      };
+      float m = -INFINITY, l = 0.f, lscale = 0.f;  // lscale >= 0: a negative scale turns the query's sign
+      if (n > 0 && (!DUAL || i == 0)) {
+        // The rows' queries, each brought to [2^7, 2^8) by a power of two, as two
+        // e4m3 terms: a warp takes 16 of the M tile's rows, D / 8 lanes a row.
+        char* dst = smem + q_tile;
+        asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 2
-      for (int x = 0; x < kIts; ++x) {
-        const int qrow = wrow + x * kPer + sub;
-        const uint4 raw = *reinterpret_cast<const uint4*>(smem + q_raw + k_off<D>(qrow, part % (D / 16)));
-        const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-        // the row's largest magnitude: as bf16 bits magnitudes order like integers (NaN above all)
-        uint32_t top = __vmaxu2(__vmaxu2(u[0] & 0x7fff7fffu, u[1] & 0x7fff7fffu),
-                                __vmaxu2(u[2] & 0x7fff7fffu, u[3] & 0x7fff7fffu));
+        for (int x = 0; x < kIts; ++x) {
+          const int qrow = wrow + x * kPer + sub;
+          const uint4 raw = *reinterpret_cast<const uint4*>(smem + q_raw + k_off<D>(qrow, part % (D / 16)));
+          const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+          // the row's largest magnitude: as bf16 bits magnitudes order like integers (NaN above all)
+          uint32_t top = __vmaxu2(__vmaxu2(u[0] & 0x7fff7fffu, u[1] & 0x7fff7fffu),
+                                  __vmaxu2(u[2] & 0x7fff7fffu, u[3] & 0x7fff7fffu));
 #pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float amax = __uint_as_float(max(top << 16, top & 0xffff0000u));
-        const float f = copysignf(row_factor<7>(amax), a.scale_log2);
-        const bool inf = !(amax < INFINITY);  // (codes saturate: such a row is NaN instead)
-        uint32_t t0[2], t1[2];
+          for (int o = kLanes / 2; o > 0; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const float amax = __uint_as_float(max(top << 16, top & 0xffff0000u));
+          const float f = copysignf(row_factor<7>(amax), a.scale_log2);
+          const bool inf = !(amax < INFINITY);  // (codes saturate: such a row is NaN instead)
+          uint32_t t0[2], t1[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t a1, a2, b1, b2;
-          split_query(u[2 * k], f, a1, a2);
-          split_query(u[2 * k + 1], f, b1, b2);
-          t0[k] = inf ? 0x7f7f7f7fu : a1 | (b1 << 16);
-          t1[k] = a2 | (b2 << 16);
+          for (int k = 0; k < 2; ++k) {
+            uint32_t a1, a2, b1, b2;
+            split_query(u[2 * k], f, a1, a2);
+            split_query(u[2 * k + 1], f, b1, b2);
+            t0[k] = inf ? 0x7f7f7f7fu : a1 | (b1 << 16);
+            t1[k] = a2 | (b2 << 16);
+          }
+          __syncwarp();  // the row's lanes have read it
+          const uint32_t off = k_off<D>(qrow, part >> 1) + 8 * (part & 1);
+          *reinterpret_cast<uint2*>(dst + off) = make_uint2(t0[0], t0[1]);
+          *reinterpret_cast<uint2*>(dst + L_::kMat8 + off) = make_uint2(t1[0], t1[1]);
+          if (part == 0) pair[256 + qrow] = fabsf(a.scale_log2) * inverse(fabsf(f));
         }
-        __syncwarp();  // the row's lanes have read it
-        const uint32_t off = k_off<D>(qrow, part >> 1) + 8 * (part & 1);
-        *reinterpret_cast<uint2*>(dst + off) = make_uint2(t0[0], t0[1]);
-        *reinterpret_cast<uint2*>(dst + L_::kMat8 + off) = make_uint2(t1[0], t1[1]);
-        if (part == 0) pair[256 + qrow] = fabsf(a.scale_log2) * inverse(fabsf(f));
+        fence_proxy_async_smem();
+        mbar_arrive(bar(kQFull));
       }
-      fence_proxy_async_smem();
-      mbar_arrive(bar(kQFull));
-    }
-    // (both barriers of one count: the second comes before the pair buffers' first use)
-    auto all_sync = [&]() { DUAL ? named_sync(3, 512) : named_sync(1 + i, 256); };
-    if (n > 0) {
-      all_sync();
-      lscale = reinterpret_cast<const float*>(smem + L_::kPair)[(DUAL ? 0 : i * 512) + 256 + row];
-      all_sync();
-    }
-    // the range that all rows of the CTA see whole
-    const int p_lo = w.p_lo, p_hi = w.p_hi;
-    for (int t = 0; t < mine; ++t) {
-      const int j = DUAL ? 2 * t + i : t;
-      // (S of this tile says that O += P V of the tile before is done, too)
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(kCFull + j % kConstRing), (j / kConstRing) & 1, c.err) &&
-                                       mbar_wait(bar(kSFull + i), t & 1, c.err));
-      fence_after_sync();
-      const float4* cn = io.scales(j) + 4 * half;
-      const int base = w.k.base(t_begin + j) + 64 * half;
-      const bool whole = (a.causal ? base + 64 <= p_lo + 1 : base + 64 <= w.q.L) &&
-                         (a.window == 0 || base > p_hi - a.window || base + 64 <= a.sinks) &&
-                         (PART != Part::kOwn || base >= w.k.lo);
-      // S is read in halves of 32 keys, the first of them twice: for the row's
-      // largest logit (within 16 keys of one scale the largest product gives
-      // it), then for the weights
-      float s[32];
-      float mt = -INFINITY;
-      auto hide = [&](int x) {
-        const uint32_t seen = sees.bits(base + 32 * x);
+      // (both barriers of one count: the second comes before the pair buffers' first use)
+      auto all_sync = [&]() { DUAL ? named_sync(3, 512) : named_sync(1 + i, 256); };
+      if (n > 0) {
+        all_sync();
+        lscale = reinterpret_cast<const float*>(smem + L_::kPair)[(DUAL ? 0 : i * 512) + 256 + row];
+        all_sync();
+      }
+      // the range that all rows of the CTA see whole
+      const int p_lo = w.p_lo, p_hi = w.p_hi;
+      for (int t = 0; t < mine; ++t) {
+        const int j = j0 + (DUAL ? 2 * t + i : t);
+        // (S of this tile says that O += P V of the tile before is done, too)
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(kCFull + j % kConstRing), (j / kConstRing) & 1, c.err) &&
+                                         mbar_wait(bar(kSFull + i), (j0 + t) & 1, c.err));
+        fence_after_sync();
+        const float4* cn = io.scales(j) + 4 * half;
+        const int base = w.k.base(t_begin + j - j0) + 64 * half;
+        const bool whole = (a.causal ? base + 64 <= p_lo + 1 : base + 64 <= w.q.L) &&
+                           (a.window == 0 || base > p_hi - a.window || base + 64 <= a.sinks) &&
+                           (PART != Part::kOwn || base >= w.k.lo);
+        // S is read in halves of 32 keys, the first of them twice: for the row's
+        // largest logit (within 16 keys of one scale the largest product gives
+        // it), then for the weights
+        float s[32];
+        float mt = -INFINITY;
+        auto hide = [&](int x) {
+          const uint32_t seen = sees.bits(base + 32 * x);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) s[k] = seen & (1u << k) ? s[k] : -INFINITY;
-      };
+          for (int k = 0; k < 32; ++k) s[k] = seen & (1u << k) ? s[k] : -INFINITY;
+        };
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        tmem_ld32(ts + 32 * x, s);
+        for (int x = 0; x < 2; ++x) {
+          tmem_ld32(ts + 32 * x, s);
+          tmem_wait_ld32(s);
+          if (!whole) hide(x);
+#pragma unroll
+          for (int gg = 0; gg < 2; ++gg) {
+            const float4 z = cn[2 * x + gg];
+            const float* v = s + 16 * gg;
+            float t0 = max3(v[0], v[1], v[2]), t1 = max3(v[3], v[4], v[5]);
+            t0 = max3(t0, v[6], v[7]), t1 = max3(t1, v[8], v[9]);
+            t0 = max3(t0, v[10], v[11]), t1 = max3(t1, v[12], v[13]);
+            t0 = max3(t0, v[14], v[15]);
+            mt = fmaxf(mt, fmaf(fmaxf(t0, t1), fmaxf(lscale * z.x, kTiny), z.y));
+          }
+        }
+        mt = fmaxf(mt, other(t & 1, mt));
+        if (!ok) break;
+        if (__any_sync(0xffffffffu, mt > m + kRescale)) {
+          const float nm = fmaxf(m, mt);
+          const float f = nm == m ? 1.f : ex2(m - nm);
+          m = nm;
+          l *= f;
+          if (t > 0) {
+            // half of the output's columns a thread
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) {
+              uint32_t u[16];
+              tmem_ld16(to + 16 * x, u);
+              tmem_wait_ld16(u);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * f);
+              tmem_st16(to + 16 * x, u);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m - kLift;
+        auto weigh = [&](int x) {
+          uint32_t u[16];
+#pragma unroll
+          for (int gg = 0; gg < 2; ++gg) {
+            const float4 z = cn[2 * x + gg];
+            const float sc = fmaxf(lscale * z.x, kTiny), off = z.y - ref;
+            const float* v = s + 16 * gg;
+            float sum0 = 0.f, sum1 = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              float w0, w1;
+              fma2(w0, w1, v[k], v[k + 1], sc, off);
+              w0 = ex2(w0), w1 = ex2(w1);
+              add2(sum0, sum1, w0, w1);
+              // (f16's 11 bits for the product: an output's error stays below its own rounding to
+              // bf16's 8; the sum takes the weights as they are)
+              u[8 * gg + k / 2] = half2_bits(w0, w1);
+            }
+            l = fmaf(sum0 + sum1, z.z, l);
+          }
+          // P takes the second half of this thread's S columns, those of keys 32 .. 63: they are in
+          // registers or used up, while the load of the first half is still under way
+          if (x == 1) tmem_ld32(ts, s);
+          tmem_st16(ts + kPAt + 16 * x, u);
+        };
+        weigh(1);
         tmem_wait_ld32(s);
-        if (!whole) hide(x);
-#pragma unroll
-        for (int gg = 0; gg < 2; ++gg) {
-          const float4 z = cn[2 * x + gg];
-          const float* v = s + 16 * gg;
-          float t0 = max3(v[0], v[1], v[2]), t1 = max3(v[3], v[4], v[5]);
-          t0 = max3(t0, v[6], v[7]), t1 = max3(t1, v[8], v[9]);
-          t0 = max3(t0, v[10], v[11]), t1 = max3(t1, v[12], v[13]);
-          t0 = max3(t0, v[14], v[15]);
-          mt = fmaxf(mt, fmaf(fmaxf(t0, t1), fmaxf(lscale * z.x, kTiny), z.y));
-        }
+        if (!whole) hide(0);
+        weigh(0);
+        tmem_wait_st();
+        fence_before_sync();
+        mbar_arrive(bar(kPFull + i));
       }
-      mt = fmaxf(mt, other(t & 1, mt));
-      if (!ok) break;
-      if (__any_sync(0xffffffffu, mt > m + kRescale)) {
-        const float nm = fmaxf(m, mt);
-        const float f = nm == m ? 1.f : ex2(m - nm);
-        m = nm;
-        l *= f;
-        if (t > 0) {
-          // half of the output's columns a thread
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
-            uint32_t u[16];
-            tmem_ld16(to + 16 * x, u);
-            tmem_wait_ld16(u);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(__uint_as_float(u[k]) * f);
-            tmem_st16(to + 16 * x, u);
-          }
-        }
-      }
-      const float ref = m == -INFINITY ? 0.f : m - kLift;
-      auto weigh = [&](int x) {
-        uint32_t u[16];
-#pragma unroll
-        for (int gg = 0; gg < 2; ++gg) {
-          const float4 z = cn[2 * x + gg];
-          const float sc = fmaxf(lscale * z.x, kTiny), off = z.y - ref;
-          const float* v = s + 16 * gg;
-          float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            float w0, w1;
-            fma2(w0, w1, v[k], v[k + 1], sc, off);
-            w0 = ex2(w0), w1 = ex2(w1);
-            add2(sum0, sum1, w0, w1);
-            // (f16's 11 bits for the product: an output's error stays below its own rounding to
-            // bf16's 8; the sum takes the weights as they are)
-            u[8 * gg + k / 2] = half2_bits(w0, w1);
-          }
-          l = fmaf(sum0 + sum1, z.z, l);
-        }
-        // P takes the second half of this thread's S columns, those of keys 32 .. 63: they are in
-        // registers or used up, while the load of the first half is still under way
-        if (x == 1) tmem_ld32(ts, s);
-        tmem_st16(ts + kPAt + 16 * x, u);
-      };
-      weigh(1);
-      tmem_wait_ld32(s);
-      if (!whole) hide(0);
-      weigh(0);
-      tmem_wait_st();
-      fence_before_sync();
-      mbar_arrive(bar(kPFull + i));
-    }
-    if (ok && mine > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(kOFull + i), 0, c.err));
-    if (mine > 0) l += other(mine & 1, l);
-    if (ok) {
-      fence_after_sync();
-      const size_t orow = (static_cast<size_t>(w.q.q0) + tok) * a.hq + head;
-      const size_t prow =
-          PART == Part::kAll
-              ? (((static_cast<size_t>(b) * c.hkv + hk) * pl.row_tiles + rt) * pl.splits + split) * kRows + i * kM + row
-              : part_row(c, a, w, DUAL ? 2 * split + i : split) + (DUAL ? 0 : i * kM) + row;
-      // A thread's half row goes through shared memory (the queries' room: the
-      // last S of either M tile came before this O), D bytes a row, so that the
-      // warp's stores are whole lines: D / 2 bf16 elements in one go, or fp32
-      // partial sums in two.
-      const bool any = l > 0.f || l != l;
-      const float f = any ? 1.f / l : 0.f;
-      char* stage = smem + L_::kQ + warp * (32 * D);
-      const uint32_t olo = static_cast<uint32_t>(orow);
-      const bool parts = PART != Part::kAll || DUAL || w.n_split > 1;
-      constexpr int kCols = D / 4;  // columns a round
+      if (ok && mine > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(kOFull + i), piece & 1, c.err));
+      if (mine > 0) l += other(mine & 1, l);
+      if (ok) {
+        fence_after_sync();
+        const size_t orow = (static_cast<size_t>(w.q.q0) + tok) * a.hq + head;
+        const size_t prow =
+            PART == Part::kAll
+                ? (((static_cast<size_t>(b) * c.hkv + hk) * pl.row_tiles + rt) * pl.splits + split) * kRows + i * kM + row
+                : part_row(c, a, w, DUAL ? 2 * split + i : split) + (DUAL ? 0 : i * kM) + row;
+        // A thread's half row goes through shared memory (the queries' room: the
+        // last S of either M tile came before this O), D bytes a row, so that the
+        // warp's stores are whole lines: D / 2 bf16 elements in one go, or fp32
+        // partial sums in two.
+        const bool any = l > 0.f || l != l;
+        const float f = any ? 1.f / l : 0.f;
+        char* stage = smem + L_::kQ + warp * (32 * D);
+        const uint32_t olo = static_cast<uint32_t>(orow);
+        const bool parts = PART != Part::kAll || DUAL || w.n_split > 1;
+        constexpr int kCols = D / 4;  // columns a round
 #pragma unroll 1
-      for (int y = 0; y < 2; ++y) {
-        float o[kCols];
+        for (int y = 0; y < 2; ++y) {
+          float o[kCols];
 #pragma unroll
-        for (int k = 0; k < kCols; ++k) o[k] = 0.f;
-        if (mine > 0) {
-          if constexpr (D == 128) {
-            tmem_ld32(to + kCols * y, o);
-            tmem_wait_ld32(o);
+          for (int k = 0; k < kCols; ++k) o[k] = 0.f;
+          if (mine > 0) {
+            if constexpr (D == 128) {
+              tmem_ld32(to + kCols * y, o);
+              tmem_wait_ld32(o);
+            } else {
+              tmem_ld16f(to + kCols * y, o);
+              tmem_wait_ld16f(o);
+            }
+          }
+          if (parts) {
+#pragma unroll
+            for (int k = 0; k < kCols / 4; ++k)
+              *reinterpret_cast<uint4*>(stage + k_off<D>(lane, k)) =
+                  make_uint4(__float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]),
+                             __float_as_uint(o[4 * k + 3]));
           } else {
-            tmem_ld16f(to + kCols * y, o);
-            tmem_wait_ld16f(o);
-          }
-        }
-        if (parts) {
 #pragma unroll
-          for (int k = 0; k < kCols / 4; ++k)
-            *reinterpret_cast<uint4*>(stage + k_off<D>(lane, k)) =
-                make_uint4(__float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]), __float_as_uint(o[4 * k + 2]),
-                           __float_as_uint(o[4 * k + 3]));
-        } else {
+            for (int k = 0; k < kCols / 8; ++k) {
+              uint32_t h[4];
 #pragma unroll
-          for (int k = 0; k < kCols / 8; ++k) {
-            uint32_t h[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 x = __floats2bfloat162_rn(o[8 * k + 2 * e] * f, o[8 * k + 2 * e + 1] * f);
-              h[e] = *reinterpret_cast<const uint32_t*>(&x);
-            }
-            *reinterpret_cast<uint4*>(stage + k_off<D>(lane, y * (kCols / 8) + k)) = make_uint4(h[0], h[1], h[2], h[3]);
-          }
-        }
-        if (parts || y == 1) {
-          __syncwarp();
-          constexpr int kChunks = D / 16;  // 16-byte chunks of a row
-          const int cc = lane % kChunks;
-#pragma unroll
-          for (int e = 0; e < kChunks; ++e) {
-            const int rr = e * (32 / kChunks) + lane / kChunks;
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + k_off<D>(rr, cc));
-            const uint32_t to_row = __shfl_sync(0xffffffffu, olo, rr);
-            if (__shfl_sync(0xffffffffu, static_cast<int>(live), rr)) {
-              if (parts)
-                *reinterpret_cast<uint4*>(ws.o + (prow - lane + rr) * D + half * (D / 2) + kCols * y + 4 * cc) = v;
-              else
-                *reinterpret_cast<uint4*>(a.out + static_cast<size_t>(to_row) * D + half * (D / 2) + 8 * cc) = v;
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 x = __floats2bfloat162_rn(o[8 * k + 2 * e] * f, o[8 * k + 2 * e + 1] * f);
+                h[e] = *reinterpret_cast<const uint32_t*>(&x);
+              }
+              *reinterpret_cast<uint4*>(stage + k_off<D>(lane, y * (kCols / 8) + k)) = make_uint4(h[0], h[1], h[2], h[3]);
             }
           }
-          __syncwarp();
+          if (parts || y == 1) {
+            __syncwarp();
+            constexpr int kChunks = D / 16;  // 16-byte chunks of a row
+            const int cc = lane % kChunks;
+#pragma unroll
+            for (int e = 0; e < kChunks; ++e) {
+              const int rr = e * (32 / kChunks) + lane / kChunks;
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + k_off<D>(rr, cc));
+              const uint32_t to_row = __shfl_sync(0xffffffffu, olo, rr);
+              if (__shfl_sync(0xffffffffu, static_cast<int>(live), rr)) {
+                if (parts)
+                  *reinterpret_cast<uint4*>(ws.o + (prow - lane + rr) * D + half * (D / 2) + kCols * y + 4 * cc) = v;
+                else
+                  *reinterpret_cast<uint4*>(a.out + static_cast<size_t>(to_row) * D + half * (D / 2) + 8 * cc) = v;
+              }
+            }
+            __syncwarp();
+          }
         }
+        if (live && half == 0 && !parts && a.lse)
+          a.lse[orow] = any ? (m - kLift + log2f(l)) * 0.693147180559945f : -INFINITY;
+        if (live && half == 0 && parts) ws.ml[prow] = make_float2(m, l);
       }
-      if (live && half == 0 && !parts && a.lse)
-        a.lse[orow] = any ? (m - kLift + log2f(l)) * 0.693147180559945f : -INFINITY;
-      if (live && half == 0 && parts) ws.ml[prow] = make_float2(m, l);
+      if (!go_on(ok)) break;
+      // (the last results' room and the pairs' are the queries' now; all of the M tile's warps agree on `ok`)
+      named_sync(1 + i, 256);
+      load_queries();
     }
   }
   __syncwarp();
@@ -506,11 +572,11 @@ __global__ void __launch_bounds__(kJoinThreads)
 
 template <int D, bool DUAL, Part PART>
 cudaError_t launch_part(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,
-                        const CUtensorMap& k_map, cudaStream_t s) {
+                        const CUtensorMap& k_map, cudaStream_t s, int ctas = 0) {
   static std::atomic<size_t> done[kMaxDevices];
   const void* fn = reinterpret_cast<const void*>(attn_tiles_kernel<D, DUAL, PART>);
   if (const cudaError_t e = opt_in_smem(fn, done, Lay<D>::kSmem); e != cudaSuccess) return e;
-  const int64_t grid = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs * pl.splits;
+  const int64_t grid = ctas ? ctas : static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs * pl.splits;
   if (grid > INT_MAX) return cudaErrorInvalidConfiguration;
   return launch_kernel(attn_tiles_kernel<D, DUAL, PART>, grid, kThreads, Lay<D>::kSmem, s, PART == Part::kOwn, c, a, ws,
                        pl, sh, k_map);
@@ -548,17 +614,19 @@ cudaError_t attn_tiles_launch(const KvView& c, const AttnArgs& a, const AttnWs& 
 }
 
 cudaError_t attn_tiles_part_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,
-                                   bool prefix, const KvMaps& maps, cudaStream_t s) {
+                                   bool prefix, int ctas, const KvMaps& maps, cudaStream_t s) {
   const bool dual = static_cast<int64_t>(c.max_q) * a.G <= kM;
   const CUtensorMap& k = maps.k_tile;
+  if (ctas)
+    return (c.D == 128 ? launch_part<128, false, Part::kDealt> : launch_part<64, false, Part::kDealt>)(c, a, ws, pl, sh, k, s, ctas);
   if (c.D == 128) {
     if (prefix)
-      return (dual ? launch_part<128, true, Part::kPrefix> : launch_part<128, false, Part::kPrefix>)(c, a, ws, pl, sh, k, s);
-    return (dual ? launch_part<128, true, Part::kOwn> : launch_part<128, false, Part::kOwn>)(c, a, ws, pl, sh, k, s);
+      return (dual ? launch_part<128, true, Part::kPrefix> : launch_part<128, false, Part::kPrefix>)(c, a, ws, pl, sh, k, s, 0);
+    return (dual ? launch_part<128, true, Part::kOwn> : launch_part<128, false, Part::kOwn>)(c, a, ws, pl, sh, k, s, 0);
   }
   if (prefix)
-    return (dual ? launch_part<64, true, Part::kPrefix> : launch_part<64, false, Part::kPrefix>)(c, a, ws, pl, sh, k, s);
-  return (dual ? launch_part<64, true, Part::kOwn> : launch_part<64, false, Part::kOwn>)(c, a, ws, pl, sh, k, s);
+    return (dual ? launch_part<64, true, Part::kPrefix> : launch_part<64, false, Part::kPrefix>)(c, a, ws, pl, sh, k, s, 0);
+  return (dual ? launch_part<64, true, Part::kOwn> : launch_part<64, false, Part::kOwn>)(c, a, ws, pl, sh, k, s, 0);
 }
 
 }  // namespace moe

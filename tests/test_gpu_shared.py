@@ -161,6 +161,14 @@ def test_as_many_groups_as_sequences(m, monkeypatch):
     Case(m, groups, 64, 1, 2, 16, seed=1, lone=(3,)).check(monkeypatch)
 
 
+@pytest.mark.parametrize("groups,dim,hq,new", [(33, 64, 8, 20), (32, 64, 8, 20), (40, 128, 6, 25), (5, 128, 8, 70)])
+def test_groups_of_many_rows(m, monkeypatch, groups, dim, hq, new):
+    """Row tiles of several groups, some of them empty or without a prefix, one CTA's work after the other's."""
+    r = random.Random(groups)
+    some = [(r.choice((0, 40, 128, 700, r.randint(1, 400))), ragged(r, r.choice((0, 1, 2, 3)), 50, new)) for _ in range(groups - 2)]
+    Case(m, [(0, []), *some, (300, [(new, new)] * 9)], dim, 1, hq, 16, seed=2).check(monkeypatch)
+
+
 def test_agrees_with_attention_of_each(m):
     """Tables that name the prefix's pages themselves: both calls see the same tokens."""
     r = random.Random(2)
