@@ -345,6 +345,7 @@ class SeqBatch:
             raise ValueError(f"{n} sequences need cu_q of {n + 1} entries and page_table of {n} rows")
         self.cu_q, self.kv_len, self.page_table = cu_q, kv_len, page_table
         self.n_tokens, self.device, self.index = n_tokens, cu_q.device, cu_q.get_device()
+        self.bounds = (n, n_tokens, max_q_len, max_kv_len)
         self.c = moe_kv_batch_t(n, n_tokens, max_q_len, max_kv_len, page_table.shape[1], cu_q.data_ptr(),
                                 kv_len.data_ptr(), page_table.data_ptr())
 
@@ -365,6 +366,7 @@ class SharedPrefix:
             raise ValueError(f"{n} groups need cu_seq of {n + 1} entries and page_table of {n} rows")
         self.cu_seq, self.prefix_len, self.page_table = cu_seq, prefix_len, page_table
         self.device, self.index = cu_seq.device, cu_seq.get_device()
+        self.bounds = (n, max_group_tokens, max_prefix_len)
         self.c = moe_kv_prefix_t(n, max_group_tokens, max_prefix_len, page_table.shape[1], cu_seq.data_ptr(),
                                  prefix_len.data_ptr(), page_table.data_ptr())
 
@@ -500,7 +502,7 @@ class KVCache:
         if prefix.index != self._index:
             raise ValueError(f"the prefix must be on {self.device}, got {prefix.device}")
         b, p = batch.c, prefix.c
-        key = (b.n_seqs, b.n_tokens, b.max_q_len, b.max_kv_len, p.n_groups, p.max_group_tokens, p.max_prefix_len)
+        key = (batch.bounds, prefix.bounds)
         size = self._shared.get(key)
         if size is None:
             size = _lib.moe_kv_shared_workspace_bytes(self.h, b, p)
