@@ -210,12 +210,12 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
  * of new tokens >= prefix_len); another one, and one that no group holds, has all of its
  * tokens by its own table, as in moe_kv_attend.  The arrays live on the device; the host
  * gives bounds: max_group_tokens new tokens of any group (their rows are those from its
- * first sequence's to its last one's), max_prefix_len tokens of any prefix.  A group whose
- * arrays break them (cu_seq not ascending within [0, n_seqs], a length outside
- * [0, max_prefix_len], a needed page id outside [0, n_pages)) sets bit 1 of
- * moe_kv_device_status, and its rows are not valid.  With mask->causal == 0 the rows see
- * all of the prefix and of their own tokens.  window and sinks are not supported: the rows
- * of windowed layers do not see the whole prefix.
+ * first sequence's to its last one's), max_prefix_len tokens of any prefix (at most the
+ * handle's max_kv_len).  A group whose arrays break them (cu_seq not ascending within
+ * [0, n_seqs], a length outside [0, max_prefix_len], a needed page id outside [0, n_pages))
+ * sets bit 1 of moe_kv_device_status, and its rows are not valid.  With mask->causal == 0
+ * the rows see all of the prefix and of their own tokens.  window and sinks are not
+ * supported: the rows of windowed layers do not see the whole prefix.
  * workspace: device memory of at least moe_kv_shared_workspace_bytes (0 when the arguments
  * are not valid), used until the call has run; it needs no preparation and keeps nothing.
  * n_groups: 0 (which makes moe_kv_attend of it) to 65535. */

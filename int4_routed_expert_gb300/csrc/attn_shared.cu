@@ -41,8 +41,8 @@ CtaCost cost_of(int64_t rows) {
   return {1.75, 10., 1};
 }
 
-// The kernel for a side's rows, and its row tiles: `live` of them are sure to have rows, of
-// all CTAs' ones that a launch has to count on.
+// The kernel for a side's rows, and its row tiles: a launch has to count on row_tiles of each
+// sequence, but `live` of all sequences and kv heads have rows, or about so many.
 Side side_of(const KvView& c, int G, double& live) {
   const int64_t rows = static_cast<int64_t>(c.max_q) * G, all = static_cast<int64_t>(c.n_tokens) * G;
   Side x;
@@ -51,7 +51,7 @@ Side side_of(const KvView& c, int G, double& live) {
   x.parts = !x.few && rows <= 128 ? 2 : 1;
   x.ctas = 0;
   x.pl.row_tiles = static_cast<int>((rows + x.rows - 1) / x.rows);
-  // the sequences' rows add up to the call's, and half a tile of each is empty
+  // (the sequences' rows add up to the call's, and half a tile of each is empty)
   live = std::min(static_cast<double>(x.pl.row_tiles) * c.n_seqs, static_cast<double>(all) / x.rows + 0.5 * c.n_seqs + 0.5) *
          c.hkv;
   return x;
@@ -83,9 +83,12 @@ struct Sides {
 // prefixes leaves, so that one's CTAs go by the time of both: that of the longest ones, or
 // all CTAs' time over the SMs, whichever is longer, and what a split more costs the join.
 // The splits are alike, or (more than 128 rows, up to 32 groups) the row tiles' keys are
-// dealt out evenly to CTAs that go from one to the next, which costs some at each change.  (37 x 4 tokens on three prefixes of up to 66001, 48 / 4 heads, in splits: 265 us at
-// 4, 338 us at 6, whose second round of CTAs is a quarter full; dealt out 224 us.
-// 5085 tokens of 12 questions on 24001, 32 / 2 heads of 64: 1546 us in 2 splits, 1437 us dealt out.)
+// dealt out evenly to CTAs that go from one to the next, which costs some at each change.
+// (64 tokens on a prefix of 16384, 64 / 8 heads: 71 us in 5 splits, 87 us in 9, where the
+// prefix alone is fastest, 79 us dealt out.  37 x 4 tokens on three prefixes of up to 66001,
+// 48 / 4 heads: 265 us in 4 splits, 338 us in 6, whose second round of CTAs is a quarter
+// full, 224 us dealt out.  5085 tokens of 12 questions on 24001, 32 / 2 heads of 64: 1546 us
+// in 2 splits, 1437 us dealt out.)
 Sides sides_of(const KvView& c, const Share& sh, int G, int n_sm) {
   constexpr int64_t kMost = 1 << 20;  // rows of results a side, where one split has fewer
   const int64_t rows = static_cast<int64_t>(c.n_tokens) * c.hkv * G;

@@ -1,5 +1,7 @@
 // C ABI of attention over shared prefixes (include/moe_attn.h): argument checks,
 // workspace.
+#include <algorithm>
+
 #include "attn_host.cuh"
 
 namespace {
@@ -7,11 +9,11 @@ namespace {
 using namespace moe;
 
 // NULL, or what is wrong with the bounds of a prefix.
-const char* check_prefix(const moe_kv_config_t& c, const moe_kv_batch_t* b, const moe_kv_prefix_t* p) {
+const char* check_prefix(const moe_kv_config_t& c, const moe_kv_prefix_t* p) {
   if (!p) return "prefix is NULL";
   if (p->n_groups < 0 || p->n_groups > 65535) return "n_groups must be in [0, 65535]";
   if (p->n_groups == 0) return nullptr;
-  if (p->max_group_tokens < 1 || p->max_group_tokens > b->n_tokens) return "max_group_tokens must be in [1, n_tokens]";
+  if (p->max_group_tokens < 1) return "max_group_tokens must be at least 1";
   if (p->max_prefix_len < 1 || p->max_prefix_len > c.max_kv_len)
     return "max_prefix_len must be in [1, max_kv_len of the handle]";
   if (p->table_stride < 1) return "the prefix's table_stride must be at least 1";
@@ -19,8 +21,8 @@ const char* check_prefix(const moe_kv_config_t& c, const moe_kv_batch_t* b, cons
 }
 
 Share share_of(const moe_kv_batch_t* b, const moe_kv_prefix_t* p) {
-  return Share{p->cu_seq, p->prefix_len, p->page_table, p->table_stride, p->n_groups, p->max_group_tokens,
-               p->max_prefix_len, b->n_seqs};
+  return Share{p->cu_seq, p->prefix_len, p->page_table, p->table_stride, p->n_groups,
+               std::min(p->max_group_tokens, b->n_tokens), p->max_prefix_len, b->n_seqs};
 }
 
 }  // namespace
@@ -30,7 +32,7 @@ extern "C" {
 size_t moe_kv_shared_workspace_bytes(const moe_kv_t* h, const moe_kv_batch_t* batch, const moe_kv_prefix_t* prefix) {
   if (!h || !batch || batch->n_seqs < 1 || batch->n_tokens < 1 || batch->max_q_len < 1 || batch->max_kv_len < 0 ||
       batch->n_seqs > h->cfg.max_seqs || batch->n_tokens > h->cfg.max_tokens || batch->max_kv_len > h->cfg.max_kv_len ||
-      batch->max_q_len > batch->n_tokens || check_prefix(h->cfg, batch, prefix) || prefix->n_groups == 0)
+      batch->max_q_len > batch->n_tokens || check_prefix(h->cfg, prefix) || prefix->n_groups == 0)
     return 0;
   KvView c{};
   c.n_seqs = batch->n_seqs, c.n_tokens = batch->n_tokens, c.max_q = batch->max_q_len, c.max_kv = batch->max_kv_len;
@@ -50,7 +52,7 @@ moe_status_t moe_kv_attend_shared(moe_kv_t* h, const void* q, int64_t q_stride, 
   AttnArgs a{};
   moe_status_t st = attend_args(h, q, q_stride, out, lse, mask, batch, &c, &a);
   if (st != MOE_OK || c.n_seqs == 0) return st;
-  if (const char* m = check_prefix(h->cfg, batch, prefix)) {
+  if (const char* m = check_prefix(h->cfg, prefix)) {
     fail(h, "%s", m);
     return MOE_ERR_INVALID_ARG;
   }

@@ -317,7 +317,8 @@ def test_refusals(m):
     def prefix(cu=(0, 2), lens=(300,), table=rows, group=2, most=300):
         return m.SharedPrefix(t(list(cu)), t(list(lens)), table, group, most)
 
-    for bad in (prefix(group=0), prefix(group=3), prefix(most=0), prefix(most=10 ** 6)):
+    assert torch.equal(k.c.attend(k.q, k.bt.b, prefix=prefix(group=99)), k.c.attend(k.q, k.bt.b, prefix=k.share))
+    for bad in (prefix(group=0), prefix(most=0), prefix(most=10 ** 6)):
         with pytest.raises(m.MoeError):
             k.c.attend(k.q, k.bt.b, prefix=bad)
     for args in ((t([0]), t([300]), rows, 2, 300), (t([0, 2]), t([300]).long(), rows, 2, 300), (t([0, 2]), t([300]), rows[0], 2, 300),

@@ -92,7 +92,7 @@ def test_refusals(lib):
             setattr(kv.prefix, field, bad)
             assert kv.call() == INVALID and field.encode() in kv.message()
         setattr(kv.prefix, field, old)
-    for field, bads in (("n_groups", (-1, 65536)), ("max_group_tokens", (0, 4)), ("max_prefix_len", (0, 129)), ("table_stride", (0,))):
+    for field, bads in (("n_groups", (-1, 65536)), ("max_group_tokens", (0, -1)), ("max_prefix_len", (0, 129)), ("table_stride", (0,))):
         old = getattr(kv.prefix, field)
         for bad in bads:
             setattr(kv.prefix, field, bad)
