@@ -394,6 +394,7 @@ class KVCache:
         self.device = k_codes.device
         self._index = k_codes.get_device()
         self._row = {}  # checked layouts of the calls' tensors: (name, shape, stride) -> elements between tokens
+        self._mask = {}  # calls' masks as the library takes them (it only reads them)
         self._shared = {}  # workspace bytes of calls with a prefix, by their bounds
         self.default_scale = D ** -0.5
         cfg = moe_kv_config_t(n_q_heads, H, D, S, P, max_seqs, max_tokens, max_kv_len)
@@ -490,7 +491,13 @@ class KVCache:
         if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()
                                 or lse.device != dev):
             raise ValueError(f"lse must be a contiguous fp32 tensor {shape[:2]} on {dev}")
-        mask = moe_kv_mask_t(self.default_scale if scale is None else scale, 1 if causal else 0, window, sinks)
+        key = (scale, causal, window, sinks)
+        mask = self._mask.get(key)
+        if mask is None:
+            if len(self._mask) >= 64:
+                self._mask.clear()
+            mask = self._mask[key] = moe_kv_mask_t(self.default_scale if scale is None else scale, 1 if causal else 0,
+                                                   window, sinks)
         if prefix is not None:
             return self._attend_shared(q, qs, out, lse, mask, batch, prefix, stream)
         self._check(_lib.moe_kv_attend(self.h, q.data_ptr(), qs, out.data_ptr(),
