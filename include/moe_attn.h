@@ -203,9 +203,10 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
                            const moe_kv_mask_t* mask, const moe_kv_batch_t* batch, void* stream);
 
 /* The same for sequences that share a prefix, whose keys and values are read once for
- * all of them.  Group g holds the batch's sequences cu_seq[g] .. cu_seq[g+1] - 1; their
- * tokens 0 .. prefix_len[g] - 1 are those of row g of the prefix's own page_table (the
- * entries of the batch's table for pages that end within the prefix are not looked at).
+ * all of them (short ones, by the bounds, for each where that takes less time).  Group g
+ * holds the batch's sequences cu_seq[g] .. cu_seq[g+1] - 1; their tokens 0 ..
+ * prefix_len[g] - 1 are those of row g of the prefix's own page_table (the entries of the
+ * batch's table for pages that end within the prefix are not looked at).
  * A sequence takes part when its new tokens all lie behind the prefix (kv_len - number
  * of new tokens >= prefix_len); another one, and one that no group holds, has all of its
  * tokens by its own table, as in moe_kv_attend.  The arrays live on the device; the host

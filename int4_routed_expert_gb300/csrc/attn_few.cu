@@ -196,7 +196,8 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
   const uint32_t base_u = smem_u32(smem);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
-  if constexpr (PART != Part::kAll) pdl_launch_dependents();
+  constexpr bool kWhole = PART == Part::kAll || PART == Part::kBoth;  // (else partial results alone)
+  if constexpr (!kWhole) pdl_launch_dependents();
   int idx = blockIdx.x;
   const int hk = idx % c.hkv;
   idx /= c.hkv;
@@ -205,6 +206,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
   const int b = idx % c.n_seqs, split = idx / c.n_seqs;
   Work w;
   if (!work_of<PART>(c, a, pl, sh, N, b, hk, rt, w) || split >= w.n_split) {
+    if (PART == Part::kBoth && warp == 0) check_groups(c, sh);
     end_of_part<PART>();
     return;
   }
@@ -235,8 +237,11 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
   const Rows<N> rows(smem + L_::kRow);
 
   if (warp == kMma + 1) {
-    if (lane < 8 && n > 0) io.load(c, a, w.k, b, hk, t_begin, n, &k_map, &v_map, lane);
+    if (lane < 8 && n > 0)
+      io.template load<PART == Part::kBoth>(c, a, w.k, b, hk, t_begin, n, &k_map, &v_map, lane, 0,
+                                            sh.table + static_cast<size_t>(max(w.k.group, 0)) * sh.table_stride);
   } else if (warp == kMma) {
+    if constexpr (PART == Part::kBoth) check_groups(c, sh);  // (while the first keys are on their way)
     if (lane == 0 && n > 0) {
       constexpr uint32_t id_s = idesc_f16(kKeys, 2 * N);                      // e4m3 is format 0 of its kind, too
       constexpr uint32_t id_o = idesc_f16(128, 4 * N) | (1u << 15) | (1u << 16);  // both MN-major
@@ -319,7 +324,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
         *reinterpret_cast<uint2*>(dst + k_off<D>(N + r, byte >> 4)) = make_uint2(t1[0], t1[1]);
       }
       if (part == 0) {
-        const RowSees s = row_sees(a, w.q.L, w.base_p + tok, live, PART == Part::kOwn ? w.k.lo : 0);
+        const RowSees s = row_sees(a, w.q.L, w.base_p + tok, live, PART == Part::kOwn || PART == Part::kBoth ? w.k.lo : 0);
         rows.lscale[r] = fmaxf(a.scale_log2 / f, kTiny);
         rows.nref[r] = 0.f;
         rows.m[r] = -INFINITY;
@@ -348,9 +353,11 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
       const float4 cn = io.scales(j)[t >> 4];
       const float ks = fmaxf(cn.x, kTiny);
       const int tok = w.k.base(t_begin + j) + t, key0 = tok - t;
-      const bool whole = (a.causal ? key0 + kKeys <= p_lo + 1 : key0 + kKeys <= w.q.L) &&
-                         (a.window == 0 || key0 > p_hi - a.window || key0 + kKeys <= a.sinks) &&
-                         (PART != Part::kOwn || key0 >= w.k.lo);
+      const bool pre = PART == Part::kBoth && t_begin + j < w.k.n_a;  // of the prefix, which all rows see
+      const bool whole = pre ? key0 + kKeys <= w.k.lo
+                             : (a.causal ? key0 + kKeys <= p_lo + 1 : key0 + kKeys <= w.q.L) &&
+                                   (a.window == 0 || key0 > p_hi - a.window || key0 + kKeys <= a.sinks) &&
+                                   ((PART != Part::kOwn && PART != Part::kBoth) || key0 >= w.k.lo);
       // exponents relative to the rows' references
       float top = -INFINITY;
       tmem_wait_ld16f(z);
@@ -373,7 +380,8 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
       if (!whole) {
 #pragma unroll
         for (int r = 0; r < NG; ++r) {
-          const bool sees = tok <= rows.hi[g0 + r] && (tok >= rows.lo[g0 + r] || tok < a.sinks);
+          const bool sees = pre ? tok < w.k.lo && rows.hi[g0 + r] >= 0
+                                : tok <= rows.hi[g0 + r] && (tok >= rows.lo[g0 + r] || tok < a.sinks);
           z[r] = sees ? z[r] : -INFINITY;
         }
       }
@@ -441,7 +449,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
       if (grp == 0 && !whole) {
         // the values that no row sees are zero: a NaN code there would reach the rows through 0 * NaN
         ok = ok && mbar_wait(bar(kVFull + j % L_::kStages), (j / L_::kStages) & 1, c.err);
-        if (!(tok < w.k.hi && (tok >= w.k.lo || tok < a.sinks))) {
+        if (!(pre ? tok < w.k.lo : tok < w.k.hi && (tok >= w.k.lo || tok < a.sinks))) {
           uint4* v = reinterpret_cast<uint4*>(smem + L_::kV + (j % L_::kStages) * Io::kMat8 + t * D);
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) v[x] = make_uint4(0, 0, 0, 0);
@@ -495,7 +503,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
     }
     named_sync(1 + grp, 128);
     const int live = w.r1 - w.r0;
-    const size_t prow = PART == Part::kAll
+    const size_t prow = kWhole
                             ? (((static_cast<size_t>(b) * c.hkv + hk) * pl.row_tiles + rt) * pl.splits + split) * N
                             : part_row(c, a, w, split);
     if (t < NG && g0 + t < live) {
@@ -504,7 +512,7 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
       const float mm = rows.m[row] + (kLift - kFewLift);  // as the other kernel counts
       const bool any = ll > 0.f || ll != ll;
       rows.f[row] = any ? 1.f / ll : 0.f;
-      if (PART != Part::kAll || w.n_split > 1)
+      if (!kWhole || w.n_split > 1)
         ws.ml[prow + row] = make_float2(mm, ll);
       else if (a.lse)
         a.lse[rows.out[row]] = any ? (mm - kLift + log2f(ll)) * 0.693147180559945f : -INFINITY;
@@ -514,19 +522,19 @@ __global__ void __launch_bounds__(Lay<D, N>::kThreads, Lay<D, N>::kCtas)
     for (int r = 0; r < NG; ++r) {
       const int row = g0 + r;
       if (row < live && t < D) {
-        if (PART == Part::kAll && w.n_split == 1)
+        if (kWhole && w.n_split == 1)
           a.out[static_cast<size_t>(rows.out[row]) * D + t] = __float2bfloat16_rn(o[r] * rows.f[row]);
         else
           ws.o[(prow + row) * D + t] = o[r];
       }
     }
-    if (PART == Part::kAll && w.n_split > 1) __threadfence();
+    if (kWhole && w.n_split > 1) __threadfence();
   }
   __syncwarp();
   fence_before_sync();
   __syncthreads();
   if (warp == kMma) tmem_dealloc(tmem, L_::kTmem);
-  if constexpr (PART != Part::kAll) {
+  if constexpr (!kWhole) {
     end_of_part<PART>();
     return;
   }
@@ -637,20 +645,21 @@ cudaError_t launch_part(const KvView& c, const AttnArgs& a, const AttnWs& ws, co
                        c, a, ws, pl, sh, maps.k_tile, maps.v_tile);
 }
 
-template <int D, int N>
-cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const KvMaps& maps, int n_sm, cudaStream_t s) {
+template <int D, int N, Part PART = Part::kAll>
+cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const KvMaps& maps, int n_sm, cudaStream_t s,
+                   const Share& sh = Share{}) {
   Plan pl;
   const int64_t rows = static_cast<int64_t>(c.max_q) * a.G;
   pl.row_tiles = static_cast<int>((rows + N - 1) / N);
   const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
-  const int64_t tiles = max_key_tiles(c, a, N, kKeys);
+  const int64_t tiles = max_key_tiles(c, a, N, kKeys) + (PART == Part::kBoth ? 1 : 0);
   // (32 rows of 8000 keys and 8 kv heads of 128, splits of 8, 4 and 2 tiles:
   // 27.3, 23.3 and 27.2 us)
   const int64_t most = std::min<int64_t>(static_cast<int64_t>(ws.cap_rows) / (base * N), max_splits(N));
   const int64_t splits = best_splits(base, n_sm, tiles, most, c.n_seqs > 1, {Lay<D, N>::kCtas, 3., 0.25});
   pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
   pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
-  return launch_part<D, N, Part::kAll>(c, a, ws, pl, Share{}, maps, s);
+  return launch_part<D, N, PART>(c, a, ws, pl, sh, maps, s);
 }
 
 }  // namespace
@@ -661,8 +670,16 @@ cudaError_t attn_few_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws
   // head take 208 us in the first and 304 us in the second
   const int64_t rows = static_cast<int64_t>(c.max_q) * a.G;
   if (c.D == 128)
-    return (rows <= 16 ? launch<128, 16> : launch<128, 32>)(c, a, ws, maps, n_sm, s);
-  return (rows <= 16 ? launch<64, 16> : launch<64, 32>)(c, a, ws, maps, n_sm, s);
+    return (rows <= 16 ? launch<128, 16> : launch<128, 32>)(c, a, ws, maps, n_sm, s, Share{});
+  return (rows <= 16 ? launch<64, 16> : launch<64, 32>)(c, a, ws, maps, n_sm, s, Share{});
+}
+
+cudaError_t attn_few_both_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Share& sh, const KvMaps& maps,
+                                 int n_sm, cudaStream_t s) {
+  const bool n16 = static_cast<int64_t>(c.max_q) * a.G <= 16;
+  if (c.D == 128)
+    return (n16 ? launch<128, 16, Part::kBoth> : launch<128, 32, Part::kBoth>)(c, a, ws, maps, n_sm, s, sh);
+  return (n16 ? launch<64, 16, Part::kBoth> : launch<64, 32, Part::kBoth>)(c, a, ws, maps, n_sm, s, sh);
 }
 
 cudaError_t attn_few_part_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,

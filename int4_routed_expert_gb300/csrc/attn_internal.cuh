@@ -112,8 +112,8 @@ cudaError_t attn_few_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws
 // results of rows over their prefix and over their own tokens; nothing is launched where
 // it has fewer bytes than *need.
 size_t attn_shared_workspace(const KvView& c, const Share& sh, int G, int n_sm);
-cudaError_t attn_shared_launch(const KvView& c, const AttnArgs& a, const Share& sh, void* workspace, size_t have,
-                               size_t* need, const KvMaps& maps, int n_sm, cudaStream_t s);
+cudaError_t attn_shared_launch(const KvView& c, const AttnArgs& a, const Share& sh, const AttnWs& handle_ws, void* workspace,
+                               size_t have, size_t* need, const KvMaps& maps, int n_sm, cudaStream_t s);
 cudaError_t attn_tiles_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const KvMaps& maps,
                               int n_sm, cudaStream_t s);
 

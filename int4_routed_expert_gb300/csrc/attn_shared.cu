@@ -10,6 +10,16 @@
 // a last kernel joins them, own splits first, in their order.
 // The three launches overlap: the second does not need the first and begins as its
 // CTAs leave SMs, the third is in place when they end.
+//
+// Short prefixes and few keys take one launch instead, in which each sequence goes over its
+// prefix and its own tokens itself (Part::kBoth); the workspace is then the handle's, as for
+// attention without prefixes.  Whichever of the two is to take less, the host's 7 us for two
+// launches more counted (240 calls of 1 to 64 sequences of up to 1742 new tokens, prefixes of
+// 20 to 125000, captured: 0.92 of the three launches' time, one by one 0.40 to 1.42 of it; a
+// call of 3 tokens that is not captured: 14.7 us instead of 22.3).  24 tokens of 9 groups,
+// prefixes of 133, 96 / 8 heads of 64: 13.0 us in one launch, 31.7 us in three; 10 prompts'
+// last 536 tokens on 822, 24 / 8 heads: 88.8 and 155 us; 40 tokens of 3 groups on 2384, 8 / 8
+// heads: 54.6 and 26.4 us.
 #include <cmath>
 
 #include "attn_tc.cuh"
@@ -78,7 +88,24 @@ struct Sides {
   KvView prefix;
   Side own, shared;
   bool wide;  // few rows: the join has a CTA for each
+  bool one;   // neither: each sequence reads all of its keys, in one launch
 };
+// What one launch over all keys takes (Part::kBoth).
+double one_launch_time(const KvView& c, int G, const Side& x, double live, int n_sm) {
+  const int64_t tiles = (static_cast<int64_t>(c.max_kv) + kKeys - 1) / kKeys + 1;
+  const int64_t base = static_cast<int64_t>(x.pl.row_tiles) * c.n_seqs * c.hkv;
+  const CtaCost cost = cost_of(static_cast<int64_t>(c.max_q) * G);
+  int64_t n = best_splits(base, n_sm, tiles, 256, c.n_seqs > 1, x.few ? Costs{2, 3., 0.25} : Costs{1, 6., 1. / 32});
+  const int64_t per = (tiles + n - 1) / n;
+  n = (tiles + per - 1) / per;
+  const double cta = cost.tile * static_cast<double>(per) + cost.start;
+  double join = 0;
+  if (x.few && n > 1) join = 1.5 + 0.075 * cost.tile * static_cast<double>(n);
+  if (!x.few && x.parts * n > 1)
+    join = 2.5 + static_cast<double>(c.n_tokens) * c.hkv * G * static_cast<double>(x.parts * n) * c.D * 8 / 5e6;
+  const double ctas = std::max(live * static_cast<double>(n), 1.);
+  return static_cast<double>(static_cast<int64_t>((ctas - 1) / (n_sm * cost.per_sm)) + 1) * cta + join;
+}
 // How the keys are cut.  The launch over own tokens fills the SMs that the one over the
 // prefixes leaves, so that one's CTAs go by the time of both: that of the longest ones, or
 // all CTAs' time over the SMs, whichever is longer, and what a split more costs the join.
@@ -124,9 +151,17 @@ Sides sides_of(const KvView& c, const Share& sh, int G, int n_sm) {
     if (time < least) least = time, best = k;
   }
   set_splits(s.shared, c, G, tiles, best);
+  // The three launches as a whole: the longer of the two, what the own results cost the join,
+  // and two launches more (4 us where they are captured, 7 us of the host's where not).
+  const double one = one_launch_time(c, G, s.own, own_live, n_sm);
+  auto decide = [&](double prefix) {
+    const double own = own_cost.tile * s.own.pl.tiles_per_split + own_cost.start;
+    s.one = one < std::max(prefix, own) + static_cast<double>(s.own.cap) * c.D * 8 / 5e6 + 7.;
+    return s;
+  };
   if (s.shared.few || s.shared.parts > 1 || sh.n_groups > 32 ||
       (live + sh.n_groups * c.hkv) * static_cast<double>(tiles) > 1e9)  // (units are counted in 32 bits)
-    return s;
+    return decide(least);
   const double units = live * static_cast<double>(tiles);
   int64_t ctas = 0;
   // (splits that are alike are so of groups that are not)
@@ -146,11 +181,14 @@ Sides sides_of(const KvView& c, const Share& sh, int G, int n_sm) {
     s.shared.pl.splits = static_cast<int>(std::max<int64_t>(std::min(parts, kMost / rows), 2));
     s.shared.cap = static_cast<size_t>(s.shared.pl.splits) * rows;
   }
-  return s;
+  return decide(least);
 }
 
 size_t align(size_t x) { return (x + 255) / 256 * 256; }
 size_t side_bytes(const Side& x, int D) { return align(x.cap * D * 4) + align(x.cap * 8); }
+
+// (one launch keeps its partial results where attention without prefixes does)
+size_t bytes_of(const Sides& x, int D) { return x.one ? 16 : side_bytes(x.own, D) + side_bytes(x.shared, D); }
 
 AttnWs side_ws(const Side& x, int D, char* base) {
   return AttnWs{reinterpret_cast<float*>(base), reinterpret_cast<float2*>(base + align(x.cap * D * 4)), nullptr, x.cap};
@@ -265,15 +303,16 @@ __global__ void __launch_bounds__(kJoinThreads)
 }  // namespace
 
 size_t attn_shared_workspace(const KvView& c, const Share& sh, int G, int n_sm) {
-  const Sides x = sides_of(c, sh, G, n_sm);
-  return side_bytes(x.own, c.D) + side_bytes(x.shared, c.D);
+  return bytes_of(sides_of(c, sh, G, n_sm), c.D);
 }
 
-cudaError_t attn_shared_launch(const KvView& c, const AttnArgs& a, const Share& sh, void* workspace, size_t have,
-                               size_t* need, const KvMaps& maps, int n_sm, cudaStream_t s) {
+cudaError_t attn_shared_launch(const KvView& c, const AttnArgs& a, const Share& sh, const AttnWs& handle_ws, void* workspace,
+                               size_t have, size_t* need, const KvMaps& maps, int n_sm, cudaStream_t s) {
   const Sides x = sides_of(c, sh, a.G, n_sm);
-  *need = side_bytes(x.own, c.D) + side_bytes(x.shared, c.D);
+  *need = bytes_of(x, c.D);
   if (have < *need) return cudaErrorInvalidValue;
+  if (x.one)
+    return (x.own.few ? attn_few_both_launch : attn_tiles_both_launch)(c, a, handle_ws, sh, maps, n_sm, s);
   char* base = static_cast<char*>(workspace);
   const AttnWs own = side_ws(x.own, c.D, base), shared = side_ws(x.shared, c.D, base + side_bytes(x.own, c.D));
   AttnArgs all = a;

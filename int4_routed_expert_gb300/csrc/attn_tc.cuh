@@ -226,9 +226,11 @@ struct TileIo {
   // the softmax, which then also is through with the scales of the tile
   // kConstRing - KS before.
   // j0: tiles that the CTA has had before (of other rows).  False when a wait gave up.
+  // BOTH: the first tiles are those of the group's prefix, kt.lo tokens.
+  template <bool BOTH = false>
   __device__ __forceinline__ bool load(const KvView& c, const AttnArgs& a, const KeyTiles& kt, int b, int hk,
                                        int t_begin, int n, const CUtensorMap* k_map, const CUtensorMap* v_map,
-                                       int lane, int j0 = 0) const {
+                                       int lane, int j0 = 0, const int32_t* prefix_table = nullptr) const {
     static_assert(kConstRing > KS, "the ring outlives the key stages");
     const int t_end = t_begin + n, j_end = j0 + n;
     bool ok = true, bad = false, odd = false;
@@ -237,6 +239,10 @@ struct TileIo {
     auto entry = [&](int t) {  // INT_MIN where no row sees a key of the group's page
       if (t >= t_end) return INT_MIN;
       const int base_key = kt.base(t), tok = base_key + 16 * (lane & ~(per - 1));
+      if constexpr (BOTH) {
+        if (t < kt.n_a)
+          return tok < kt.lo ? __ldg(prefix_table + ((base_key + 16 * lane) >> c.page_log2)) : INT_MIN;
+      }
       if (!(tok < kt.hi && (tok + c.page > kt.lo || tok < a.sinks))) return INT_MIN;
       return raw_page(c, b, (base_key + 16 * lane) >> c.page_log2);
     };
@@ -300,7 +306,7 @@ struct TileIo {
   // CT threads: value codes to f16.  Thread t takes 16-byte chunk t % (D / 16)
   // of keys t / (D / 16) + 0, kPer, ...; a chunk becomes two of the operand's.
   // free(j) waits until the product that read the stage of tile j - VS is done.
-  template <typename Free>
+  template <bool BOTH = false, typename Free>
   __device__ __forceinline__ bool convert(const KvView& c, const AttnArgs& a, const KeyTiles& kt, int t_begin, int n,
                                           int tid, Free free, int j0 = 0) const {
     constexpr int kChunks = D / 16, kPer = CT / kChunks;
@@ -314,7 +320,9 @@ struct TileIo {
       const int rs = j % RS, vs = j % VS;
       if (!mbar_wait(r_full + 8 * rs, (j / RS) & 1, c.err) || (j >= VS && !free(j))) return false;
       const int base_key = kt.base(t_begin + j - j0);
-      const bool whole = base_key + kKeys <= kt.hi && (base_key >= kt.lo || base_key + kKeys <= a.sinks);
+      const bool pre = BOTH && t_begin + j - j0 < kt.n_a;
+      const bool whole = pre ? base_key + kKeys <= kt.lo
+                             : base_key + kKeys <= kt.hi && (base_key >= kt.lo || base_key + kKeys <= a.sinks);
       const char* src = smem + (raw - base) + rs * kMat8 + tid * 16;
       const char* src0 = src + (swap ? 8 : 0);
       const char* src1 = src + (swap ? 0 : 8);
@@ -326,7 +334,7 @@ struct TileIo {
         if (!whole) {
           // what no row sees is zero: a NaN there would reach the rows through 0 * NaN
           const int tok = base_key + p * kPer + row0;
-          if (!(tok < kt.hi && (tok >= kt.lo || tok < a.sinks))) u0 = u1 = make_uint2(0, 0);
+          if (!(pre ? tok < kt.lo : tok < kt.hi && (tok >= kt.lo || tok < a.sinks))) u0 = u1 = make_uint2(0, 0);
         }
         uint4 h0, h1;
         codes_to_half(u0.x, h0.x, h0.y);
@@ -362,8 +370,10 @@ struct Plan {
 
 // Which of a row's keys a launch is about: all; those behind its sequence's prefix; those
 // of the prefix, where a group of sequences takes the place of one; the same, dealt out
-// evenly (Dealt).  The last three leave partial results alone.
-enum class Part { kAll, kOwn, kPrefix, kDealt };
+// evenly (Dealt); all, where those of the prefix are looked up in its table and seen by
+// every row, and the tile in which it ends is met twice, once as its and once as the
+// sequence's.  kOwn, kPrefix and kDealt leave partial results alone.
+enum class Part { kAll, kOwn, kPrefix, kDealt, kBoth };
 
 // What a kernel's CTAs cost, in the time that a CTA with an SM of its own takes
 // for a tile of keys.
@@ -492,7 +502,7 @@ template <Part PART = Part::kAll>
 __device__ __forceinline__ bool work_of(const KvView& c, const AttnArgs& a, const Plan& pl, const Share& sh, int rows,
                                         int b, int hk, int rt, Work& w) {
   InGroup in{-1, 0};
-  if constexpr (PART == Part::kOwn) in = group_of(sh, b);
+  if constexpr (PART == Part::kOwn || PART == Part::kBoth) in = group_of(sh, b);
   if constexpr (PART == Part::kPrefix) {
     if (!load_group(c, sh, b, w.q)) return false;
   } else {
@@ -518,7 +528,19 @@ __device__ __forceinline__ bool work_of(const KvView& c, const AttnArgs& a, cons
     w.k.t_b = w.k.lo / kKeys;
     w.k.n_t = own_tiles(a, w.q.L, w.k.lo, w.p_hi);
   }
-  if constexpr (PART == Part::kAll) {
+  if constexpr (PART == Part::kBoth) {
+    w.k.lo = own_begin(sh, w.q, in);
+    w.k.group = in.g;
+    // (a prefix without room in its table is as bad as any that breaks its bounds)
+    if (w.k.lo > 0 && ((w.k.lo + c.page - 1) >> c.page_log2) > sh.table_stride) {
+      atomicOr(c.err, kErrBadBatch);
+      w.k.lo = 0;
+    }
+    w.k.n_a = (w.k.lo + kKeys - 1) / kKeys;
+    w.k.t_b = w.k.lo / kKeys;
+    w.k.n_t = w.k.n_a + own_tiles(a, w.q.L, w.k.lo, w.p_hi);
+  }
+  if constexpr (PART == Part::kAll || PART == Part::kBoth) {
     w.tiles_per_split = pl.tiles_per_split;
     w.n_split = max((w.k.n_t + pl.tiles_per_split - 1) / pl.tiles_per_split, 1);
   } else {
@@ -560,6 +582,13 @@ __device__ __forceinline__ Dealt deal_out(const KvView& c, const AttnArgs& a, co
   return d;
 }
 
+// Part::kBoth: whether the groups keep their bounds, looked at by a warp of each CTA, 32 groups at once.
+__device__ __forceinline__ void check_groups(const KvView& c, const Share& sh) {
+  Seq g;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + (threadIdx.x & 31); i < sh.n_groups; i += gridDim.x * int64_t{32})
+    load_group(c, sh, static_cast<int>(i), g);
+}
+
 // A launch over the rows' own keys may begin while the one over the prefixes runs, and does
 // not wait for it; the join behind both waits for this one alone.  So its last CTA ends
 // with the other launch.
@@ -587,6 +616,12 @@ cudaError_t launch_kernel(void (*kernel)(Params...), int64_t grid, int threads, 
 }
 
 // The two kernels' launches over parts of the keys (attn_shared.cu).
+//
+// All keys in one launch, those of the prefixes by their tables (Part::kBoth).
+cudaError_t attn_few_both_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Share& sh, const KvMaps& maps,
+                                 int n_sm, cudaStream_t s);
+cudaError_t attn_tiles_both_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Share& sh, const KvMaps& maps,
+                                   int n_sm, cudaStream_t s);
 cudaError_t attn_few_part_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,
                                  bool prefix, const KvMaps& maps, cudaStream_t s);
 // (ctas: prefixes of more than 128 rows a kv head dealt out to so many CTAs, at most pl.splits parts a row tile)

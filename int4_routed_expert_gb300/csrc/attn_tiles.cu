@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base_u = smem_u32(smem);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), wg = warp >> 2, lane = threadIdx.x & 31;
 
-  if constexpr (PART != Part::kAll) pdl_launch_dependents();
+  constexpr bool kWhole = PART == Part::kAll || PART == Part::kBoth;  // (else partial results alone)
+  if constexpr (!kWhole) pdl_launch_dependents();
   constexpr bool kDealt = PART == Part::kDealt;  // the CTA takes its piece of all groups' work
   __shared__ int4 s_group[kDealt ? 32 : 1];      // first token, tokens, length, units before
   __shared__ int s_per;
@@ -156,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     split = idx % pl.splits;
     rt = pl.row_tiles - 1 - idx / pl.splits;
     if (!work_of<PART>(c, a, pl, sh, kRows, b, hk, rt, w) || split >= w.n_split) {
+      if (PART == Part::kBoth && warp == 0) check_groups(c, sh);
       end_of_part<PART>();
       return;
     }
@@ -217,9 +219,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp + 1) {
     bool ok = true;
     do {
-      if (lane < 8 && n > 0) ok = io.load(c, a, w.k, b, hk, t_begin, n, &k_map, nullptr, lane, j0);
+      if (lane < 8 && n > 0)
+        ok = io.template load<PART == Part::kBoth>(c, a, w.k, b, hk, t_begin, n, &k_map, nullptr, lane, j0,
+                                                   PART == Part::kBoth
+                                                       ? sh.table + static_cast<size_t>(max(w.k.group, 0)) * sh.table_stride
+                                                       : nullptr);
     } while (go_on(kDealt && __all_sync(0xffffffffu, ok)));
   } else if (warp == kMmaWarp) {
+    if constexpr (PART == Part::kBoth) check_groups(c, sh);  // (while the first keys are on their way)
     bool ok = true;
     do {
       if (lane == 0 && n > 0) {
@@ -299,8 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (wg == 4) {
     bool ok = true;
     do {
-      ok = io.convert(c, a, w.k, t_begin, n, threadIdx.x - kSoftmax,
-                      [&](int j) { return mbar_wait(bar(kVEmpty + (j & 1)), ((j >> 1) & 1) ^ 1, c.err); }, j0);
+      ok = io.template convert<PART == Part::kBoth>(
+          c, a, w.k, t_begin, n, threadIdx.x - kSoftmax,
+          [&](int j) { return mbar_wait(bar(kVEmpty + (j & 1)), ((j >> 1) & 1) ^ 1, c.err); }, j0);
     } while (go_on(kDealt && __all_sync(0xffffffffu, ok)));
   } else if ((wg >> 1) < n_mt) {
     const int i = wg >> 1, half = wg & 1, row = threadIdx.x & 127;  // M tile, half of the keys
@@ -312,7 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tok = 0, head = 0;
       if (live) w.row(a, r - w.r0, tok, head);
       head += hk * a.G;
-      const RowSees sees = row_sees(a, w.q.L, w.base_p + tok, live, PART == Part::kOwn ? w.k.lo : 0);
+      const RowSees sees = row_sees(a, w.q.L, w.base_p + tok, live,
+                                      PART == Part::kOwn || PART == Part::kBoth ? w.k.lo : 0);
       const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 * (warp % 4)
       const uint32_t ts = tmem + i * 128 + lanes + half * 64, to = tmem + 256 + i * 128 + lanes + half * (D / 2);
       // What the row's two threads tell each other, two buffers in turn.  A warp
@@ -379,16 +388,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_after_sync();
         const float4* cn = io.scales(j) + 4 * half;
         const int base = w.k.base(t_begin + j - j0) + 64 * half;
-        const bool whole = (a.causal ? base + 64 <= p_lo + 1 : base + 64 <= w.q.L) &&
-                           (a.window == 0 || base > p_hi - a.window || base + 64 <= a.sinks) &&
-                           (PART != Part::kOwn || base >= w.k.lo);
+        const bool pre = PART == Part::kBoth && t_begin + j - j0 < w.k.n_a;  // of the prefix, which all rows see
+        const bool whole = pre ? base + 64 <= w.k.lo
+                               : (a.causal ? base + 64 <= p_lo + 1 : base + 64 <= w.q.L) &&
+                                     (a.window == 0 || base > p_hi - a.window || base + 64 <= a.sinks) &&
+                                     ((PART != Part::kOwn && PART != Part::kBoth) || base >= w.k.lo);
         // S is read in halves of 32 keys, the first of them twice: for the row's
         // largest logit (within 16 keys of one scale the largest product gives
         // it), then for the weights
         float s[32];
         float mt = -INFINITY;
         auto hide = [&](int x) {
-          const uint32_t seen = sees.bits(base + 32 * x);
+          const uint32_t seen = !pre ? sees.bits(base + 32 * x) : live ? RowSees::below(w.k.lo - base - 32 * x) : 0u;
 #pragma unroll
           for (int k = 0; k < 32; ++k) s[k] = seen & (1u << k) ? s[k] : -INFINITY;
         };
@@ -468,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_after_sync();
         const size_t orow = (static_cast<size_t>(w.q.q0) + tok) * a.hq + head;
         const size_t prow =
-            PART == Part::kAll
+            kWhole
                 ? (((static_cast<size_t>(b) * c.hkv + hk) * pl.row_tiles + rt) * pl.splits + split) * kRows + i * kM + row
                 : part_row(c, a, w, DUAL ? 2 * split + i : split) + (DUAL ? 0 : i * kM) + row;
         // A thread's half row goes through shared memory (the queries' room: the
@@ -479,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float f = any ? 1.f / l : 0.f;
         char* stage = smem + L_::kQ + warp * (32 * D);
         const uint32_t olo = static_cast<uint32_t>(orow);
-        const bool parts = PART != Part::kAll || DUAL || w.n_split > 1;
+        const bool parts = !kWhole || DUAL || w.n_split > 1;
         constexpr int kCols = D / 4;  // columns a round
 #pragma unroll 1
         for (int y = 0; y < 2; ++y) {
@@ -551,9 +562,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the splits (and the M tiles of DUAL) of every row that has more than one.
 constexpr int kJoinThreads = 256;
-template <int D, bool DUAL>
+template <int D, bool DUAL, Part PART>
 __global__ void __launch_bounds__(kJoinThreads)
-    attn_join_kernel(const KvView c, const AttnArgs a, const AttnWs ws, const Plan pl) {
+    attn_join_kernel(const KvView c, const AttnArgs a, const AttnWs ws, const Plan pl, const Share sh) {
   constexpr int kPer = kJoinThreads / (D / 4);  // rows of a block
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kPer + threadIdx.x / (D / 4);
   const int row = static_cast<int>(item % kRows);
@@ -562,7 +573,7 @@ __global__ void __launch_bounds__(kJoinThreads)
   const int64_t s = tile_id / pl.row_tiles;
   const int hk = static_cast<int>(s % c.hkv), b = static_cast<int>(s / c.hkv);
   Work w;
-  if (b >= c.n_seqs || !work_of(c, a, pl, Share{}, kRows, b, hk, rt, w) || (!DUAL && w.n_split == 1) || w.r0 + row >= w.r1) return;
+  if (b >= c.n_seqs || !work_of<PART>(c, a, pl, sh, kRows, b, hk, rt, w) || (!DUAL && w.n_split == 1) || w.r0 + row >= w.r1) return;
   int tok, head;
   w.row(a, row, tok, head);
   const size_t orow = (static_cast<size_t>(w.q.q0) + tok) * a.hq + hk * a.G + head;
@@ -582,23 +593,23 @@ cudaError_t launch_part(const KvView& c, const AttnArgs& a, const AttnWs& ws, co
                        pl, sh, k_map);
 }
 
-template <int D, bool DUAL>
+template <int D, bool DUAL, Part PART = Part::kAll>
 cudaError_t launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const CUtensorMap& k_map, int n_sm,
-                   cudaStream_t s) {
+                   cudaStream_t s, const Share& sh) {
   Plan pl;
   const int64_t rows = static_cast<int64_t>(c.max_q) * a.G;
   pl.row_tiles = static_cast<int>((rows + kRows - 1) / kRows);
   const int64_t base = static_cast<int64_t>(pl.row_tiles) * c.hkv * c.n_seqs;
-  const int64_t tiles = max_key_tiles(c, a, kRows, kKeys);
+  const int64_t tiles = max_key_tiles(c, a, kRows, kKeys) + (PART == Part::kBoth ? 1 : 0);
   // one CTA a SM: split the keys when the row tiles do not fill the SMs evenly
   const int64_t most = static_cast<int64_t>(ws.cap_rows) / (base * kRows);
   const int64_t splits = best_splits(base, n_sm, tiles, most, c.n_seqs > 1, {1, 6., 1. / 32});
   pl.tiles_per_split = static_cast<int>((tiles + splits - 1) / splits);
   pl.splits = static_cast<int>((tiles + pl.tiles_per_split - 1) / pl.tiles_per_split);
-  const cudaError_t e = launch_part<D, DUAL, Part::kAll>(c, a, ws, pl, Share{}, k_map, s);
+  const cudaError_t e = launch_part<D, DUAL, PART>(c, a, ws, pl, sh, k_map, s);
   if (e != cudaSuccess || (!DUAL && pl.splits == 1)) return e;
   const int64_t items = base * kRows, per = kJoinThreads / (D / 4);
-  attn_join_kernel<D, DUAL><<<static_cast<unsigned>((items + per - 1) / per), kJoinThreads, 0, s>>>(c, a, ws, pl);
+  attn_join_kernel<D, DUAL, PART><<<static_cast<unsigned>((items + per - 1) / per), kJoinThreads, 0, s>>>(c, a, ws, pl, sh);
   return cudaGetLastError();
 }
 
@@ -609,8 +620,17 @@ cudaError_t attn_tiles_launch(const KvView& c, const AttnArgs& a, const AttnWs& 
   // (the two M tiles' sums have to fit the workspace)
   const bool dual = static_cast<int64_t>(c.max_q) * a.G <= kM &&
                     static_cast<size_t>(c.n_seqs) * c.hkv * kRows <= ws.cap_rows;
-  if (c.D == 128) return (dual ? launch<128, true> : launch<128, false>)(c, a, ws, maps.k_tile, n_sm, s);
-  return (dual ? launch<64, true> : launch<64, false>)(c, a, ws, maps.k_tile, n_sm, s);
+  if (c.D == 128) return (dual ? launch<128, true> : launch<128, false>)(c, a, ws, maps.k_tile, n_sm, s, Share{});
+  return (dual ? launch<64, true> : launch<64, false>)(c, a, ws, maps.k_tile, n_sm, s, Share{});
+}
+
+cudaError_t attn_tiles_both_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Share& sh, const KvMaps& maps,
+                                   int n_sm, cudaStream_t s) {
+  const bool dual = static_cast<int64_t>(c.max_q) * a.G <= kM &&
+                    static_cast<size_t>(c.n_seqs) * c.hkv * kRows <= ws.cap_rows;
+  if (c.D == 128)
+    return (dual ? launch<128, true, Part::kBoth> : launch<128, false, Part::kBoth>)(c, a, ws, maps.k_tile, n_sm, s, sh);
+  return (dual ? launch<64, true, Part::kBoth> : launch<64, false, Part::kBoth>)(c, a, ws, maps.k_tile, n_sm, s, sh);
 }
 
 cudaError_t attn_tiles_part_launch(const KvView& c, const AttnArgs& a, const AttnWs& ws, const Plan& pl, const Share& sh,

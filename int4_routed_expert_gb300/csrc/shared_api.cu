@@ -71,7 +71,7 @@ moe_status_t moe_kv_attend_shared(moe_kv_t* h, const void* q, int64_t q_stride, 
   const OnDevice on(h->device);
   if (on.error != cudaSuccess) return launched(h, on.error, "moe_kv_attend_shared");
   size_t need = 0;
-  const cudaError_t e = attn_shared_launch(c, a, sh, const_cast<void*>(p[3]), workspace_bytes, &need, h->maps, h->n_sm,
+  const cudaError_t e = attn_shared_launch(c, a, sh, h->ws, const_cast<void*>(p[3]), workspace_bytes, &need, h->maps, h->n_sm,
                                            static_cast<cudaStream_t>(stream));
   if (workspace_bytes < need) {
     fail(h, "the workspace has %zu bytes, the call needs %zu", workspace_bytes, need);

@@ -29,9 +29,10 @@ struct KvView;
 struct AttnArgs;
 struct Share;
 struct KvMaps;
+struct AttnWs;
 size_t attn_shared_workspace(const KvView&, const Share&, int, int) { return 4096; }
-cudaError_t attn_shared_launch(const KvView&, const AttnArgs&, const Share&, void*, size_t have, size_t* need, const KvMaps&,
-                               int, cudaStream_t) {
+cudaError_t attn_shared_launch(const KvView&, const AttnArgs&, const Share&, const AttnWs&, void*, size_t have, size_t* need,
+                               const KvMaps&, int, cudaStream_t) {
   *need = 4096;
   return have < *need ? cudaErrorInvalidValue : note("shared");
 }

@@ -15,6 +15,16 @@ I32 = dict(dtype=torch.int32, device=DEV)
 NAN = 0x7f
 
 
+FAR = 1 << 17
+
+
+@pytest.fixture(params=["near", "far"], autouse=True)
+def bounds(request, monkeypatch):
+    """The host's bounds as the lengths are, or far above them: short calls are one launch over all keys in the first
+    case and launches over parts of them in the second."""
+    monkeypatch.setattr(Case, "far", request.param == "far")
+
+
 @pytest.fixture(scope="module")
 def m():
     from int4_routed_expert_gb300 import build as b
@@ -31,6 +41,8 @@ def t(x):
 class Case:
     """Groups of sequences [(prefix length, [(tokens behind the prefix, new tokens), ...]), ...]; a length below 0 is
     that of a sequence which does not take part.  Sequences before the first group and behind the last one: `lone`."""
+
+    far = False
 
     def __init__(self, m, groups, dim, hkv, hq, page, seed=0, lone=(), junk=True):
         self.m, self.page, self.dim, self.scale = m, page, dim, dim ** -0.5
@@ -71,13 +83,17 @@ class Case:
                 for i in range(p // page):
                     table[b][i] = (-1, bt.n_pages + 5, -2 ** 31)[i % 3]
             bt.b.page_table.copy_(t(table))
+        most = max(max(lens), max(p for p, _ in groups), 1)
+        if self.far:
+            most = FAR
+            bt.b = m.SeqBatch(bt.b.cu_q, bt.b.kv_len, bt.b.page_table, bt.cu[-1], max(max(news), 1), FAR)
         self.c = m.KVCache(*codes, *scales, n_q_heads=hq, max_seqs=len(lens), max_tokens=max(bt.cu[-1], 1),
-                           max_kv_len=max(max(lens), max(p for p, _ in groups), 1))
+                           max_kv_len=most)
         self.q = (1.5 * torch.randn(bt.cu[-1], hq, dim, device=DEV, generator=g)).bfloat16()
         tokens = [bt.cu[b] - bt.cu[a] for a, b in zip(cu, cu[1:])]
         self.cu_seq, self.lens = cu, [p for p, _ in groups]
         self.share = m.SharedPrefix(t(cu), t(self.lens), t(self.rows).view(len(groups), width), max(max(tokens), 1),
-                                    max(max(self.lens), 1))
+                                    FAR if self.far else max(max(self.lens), 1))
 
     def want(self, monkeypatch, causal=True):
         whole, bt = R.tokens, self.bt
@@ -136,6 +152,14 @@ GROUPS = {
 @pytest.mark.parametrize("dim,hkv,hq,page", [(64, 1, 1, 16), (128, 2, 12, 64), (64, 2, 32, 32), (128, 1, 7, 128)])
 def test_groups(m, monkeypatch, name, dim, hkv, hq, page):
     Case(m, GROUPS[name], dim, hkv, hq, page, seed=len(name)).check(monkeypatch)
+
+
+def test_the_bounds_choose_the_launches(m):
+    """One launch, which needs no workspace to speak of, and launches over parts of the keys."""
+    k = Case(m, GROUPS["verify"], 64, 2, 8, 16)
+    k.c.attend(k.q, k.bt.b, prefix=k.share)
+    (size,) = k.c._shared.values()
+    assert (size > 16) == Case.far
 
 
 @pytest.mark.parametrize("name", ["tokens", "mixed", "idle"])
@@ -217,7 +241,7 @@ def test_far_pages(m, monkeypatch, dim, new):
     for big, small in zip(codes + scales, (k.c.k_codes, k.c.v_codes, k.c.k_scale, k.c.v_scale)):
         big[far:] = small
     want = k.c.attend(k.q, k.bt.b, prefix=k.share)
-    c = m.KVCache(*codes, *scales, n_q_heads=8, max_seqs=3, max_tokens=k.bt.cu[-1], max_kv_len=512)
+    c = m.KVCache(*codes, *scales, n_q_heads=8, max_seqs=3, max_tokens=k.bt.cu[-1], max_kv_len=FAR)
     for table in (k.bt.b.page_table, k.share.page_table):
         table += far
     assert torch.equal(c.attend(k.q, k.bt.b, prefix=k.share), want) and c.device_status() == 0
@@ -270,7 +294,7 @@ def test_what_breaks_its_bounds_is_left_out(m, new):
     want = k.c.attend(k.q, k.bt.b, prefix=k.share)
     half = k.bt.cu[2]
     assert k.c.device_status() == 0
-    for tensor, i, bad in ((k.share.prefix_len, 1, 301), (k.share.prefix_len, 1, -1), (k.share.prefix_len, 1, 2 ** 31 - 1),
+    for tensor, i, bad in ((k.share.prefix_len, 1, k.share.bounds[2] + 1), (k.share.prefix_len, 1, -1), (k.share.prefix_len, 1, 2 ** 31 - 1),
                            (k.share.cu_seq, 2, 5), (k.share.cu_seq, 2, 2 ** 31 - 1), (k.share.cu_seq, 2, 1),
                            (k.share.cu_seq, 2, -2 ** 31),
                            (k.share.page_table.view(-1), 19, k.bt.n_pages), (k.share.page_table.view(-1), 19, -1)):
@@ -314,7 +338,7 @@ def test_refusals(m):
         k.c.attend(k.q, k.bt.b, prefix=k.share, window=100)
     rows = k.share.page_table
 
-    def prefix(cu=(0, 2), lens=(300,), table=rows, group=2, most=300):
+    def prefix(cu=(0, 2), lens=(300,), table=rows, group=2, most=k.share.bounds[2]):
         return m.SharedPrefix(t(list(cu)), t(list(lens)), table, group, most)
 
     assert torch.equal(k.c.attend(k.q, k.bt.b, prefix=prefix(group=99)), k.c.attend(k.q, k.bt.b, prefix=k.share))
@@ -341,9 +365,10 @@ def test_a_step_of_forked_sequences(m, dim, page, captured):
     g.manual_seed(dim)
     r = random.Random(dim)
     pages = slots * (prompt // page + 4)
+    most = FAR if Case.far else prompt + 4 * page
     pool = m.PagePool.empty(pages, page, slots, prompt + 4 * page, device=DEV)
     cache = m.KVCache.empty(pages, page, hkv, dim, n_q_heads=hq, max_seqs=slots, max_tokens=prompt + 4 * page,
-                            max_kv_len=prompt + 4 * page, device=DEV)
+                            max_kv_len=most, device=DEV)
 
     def randn(n, h):
         return torch.randn(n, h, dim, device=DEV, generator=g).bfloat16()
@@ -356,12 +381,12 @@ def test_a_step_of_forked_sequences(m, dim, page, captured):
     shared = prompt // page * page
     prefix_table = pool.table[:1, :shared // page].clone()
     pool.ref[prefix_table[0].long()] += 1
-    share = m.SharedPrefix(t([0, slots]), t([shared]), prefix_table, slots, shared)
+    share = m.SharedPrefix(t([0, slots]), t([shared]), prefix_table, slots, most if Case.far else shared)
 
     parent, added, keep = (torch.zeros(slots, **I32) for _ in range(3))
     q, k, v = randn(slots, hq), randn(slots, hkv), randn(slots, hkv)
     out = torch.zeros_like(q)
-    batch = pool.batch(slots, 1, prompt + 4 * page)
+    batch = pool.batch(slots, 1, most)
 
     def step():
         moves = pool.fork(parent, added, keep=keep)
