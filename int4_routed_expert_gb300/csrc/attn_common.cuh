@@ -18,7 +18,7 @@ struct KeyTiles {
   int lo, hi;  // seen: [lo, hi) and the sinks below lo
   int n_a, t_b, n_t;
   int tile;
-  int group;   // of the prefix, which the first n_a tiles hold (Part::kBoth)
+  int group, whole;  // Part::kBoth: of the prefix, whose are the first n_a tiles or the tokens below `whole`
   __device__ __forceinline__ int base(int t) const { return (t < n_a ? t : t_b + t - n_a) * tile; }
 };
 
