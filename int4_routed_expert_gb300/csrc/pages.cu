@@ -17,11 +17,12 @@
 // memory.
 // Figures (calls in a replayed graph): 16 slots of up to 1500 tokens 7.3 us; 777 slots of
 // up to 40000 tokens in a pool of 460,000 pages, a tenth of them forked, 15.8 us (one
-// cluster for all three steps: 35 us); 344,000 pages compacted 13.3 us (all in the cluster:
+// cluster for all three steps: 35 us); 344,000 pages compacted 11.5 us (all in the cluster:
 // 28 us).
 //
 // Compact.  With u pages in use, those from u on move, in their order, into the free ones
-// below u; a page's rank among its kind is the same prefix sum over the pool.
+// below u; a page's rank among its kind is the same prefix sum over the pool, kept as words of
+// 32 pages and the free ones before them.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -109,6 +110,67 @@ struct Segment {
       for (int k = 0; k < kBatch; ++k) n += (x[k].x == 0) + (x[k].y == 0) + (x[k].z == 0) + (x[k].w == 0);
     }
     return __reduce_add_sync(0xffffffffu, n);
+  }
+};
+
+// The same in words of free pages, 1024 pages at once: bits 4 g .. 4 g + 3 of a lane's are pages
+// 128 g + 4 lane ... Up to as many a segment (half a million in the pool) stay in registers
+// between the count and the list (344,000 pages compacted: 11.5 us, read again 13.3 us).
+struct FreeWords : Segment {
+  uint32_t kept;
+  __device__ __forceinline__ FreeWords(int n, int warp, int warps) : Segment(n, warp, warps), kept(0) {}
+  __device__ __forceinline__ uint32_t look(const int32_t* ref, int a) const {
+    constexpr int kBatch = 4;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int g0 = 0; g0 < 8; g0 += kBatch) {
+      if (a + 128 * g0 >= end) break;
+      int4 x[kBatch];
+#pragma unroll
+      for (int g = 0; g < kBatch; ++g) x[g] = load(ref, a + 128 * (g0 + g), 1);
+#pragma unroll
+      for (int g = 0; g < kBatch; ++g)
+        bits |= ((x[g].x == 0) + 2u * (x[g].y == 0) + 4u * (x[g].z == 0) + 8u * (x[g].w == 0)) << 4 * (g0 + g);
+    }
+    return bits;
+  }
+  __device__ __forceinline__ int count(const int32_t* ref) {
+    int n = 0;
+    for (int a = begin; a < end; a += 1024) {
+      kept = look(ref, a);
+      n += __popc(kept);
+    }
+    return __reduce_add_sync(0xffffffffu, n);
+  }
+  // each(a, four, rank, any) for every 128 pages a ..: which of a lane's four are free, how many
+  // free ones are before them (`at` of them before the segment), whether any of the 128 is.
+  template <typename F>
+  __device__ __forceinline__ void list(const int32_t* ref, int at, F each) const {
+    for (int a = begin; a < end; a += 1024) {
+      const uint32_t bits = end - begin <= 1024 ? kept : look(ref, a);
+      // counts of the eight 128s, a byte each: even ones, odd ones
+      uint32_t n = bits - (bits >> 1 & 0x55555555u);
+      n = (n & 0x33333333u) + (n >> 2 & 0x33333333u);
+      const uint32_t own[2] = {n & 0x0f0f0f0fu, n >> 4 & 0x0f0f0f0fu};
+      uint32_t sum[2] = {own[0], own[1]}, all[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, sum[h], o);
+          if ((threadIdx.x & 31) >= o) sum[h] += y;
+        }
+        all[h] = __shfl_sync(0xffffffffu, sum[h], 31);
+        sum[h] -= own[h];
+      }
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        if (a + 128 * g >= end) break;
+        const int shift = 8 * (g >> 1), any = all[g & 1] >> shift & 0xff;
+        each(a + 128 * g, bits >> 4 * g & 0xfu, at + static_cast<int>(sum[g & 1] >> shift & 0xff), any != 0);
+        at += any;
+      }
+    }
   }
 };
 
@@ -453,8 +515,8 @@ __device__ __forceinline__ void rank_pages(const PagesView& p, moe_page_move_t* 
   const int lane = threadIdx.x & 31;
   const int ctas = static_cast<int>(cl.num_blocks()), warps = ctas * kWarps;
   const int tid = static_cast<int>(cl.block_rank()) * kThreads + threadIdx.x, gw = tid >> 5;
-  const Segment seg(p.n_pages, gw, warps);
-  const int mine = seg.count_free(p.ref);
+  FreeWords seg(p.n_pages, gw, warps);
+  const int mine = seg.count(p.ref);
   if (threadIdx.x == 0) m.below = 0;
   if (ctas > 1) {
     cl.barrier_wait();
@@ -484,39 +546,41 @@ __device__ __forceinline__ void rank_pages(const PagesView& p, moe_page_move_t* 
   n_moves = m.below;
   if (tid == 0) *p.free_pages = n_free;
 
-  // (a lane's pages are 32 apart: neighbours' ranks go to neighbours in memory)
-  constexpr int kBatch = 8;
-  for (int a = seg.begin, at = free_before; a < seg.end; a += 32 * kBatch) {
-    int x[kBatch];
+  // what tells a page's rank, and the free pages below `used`
+  int2* words = reinterpret_cast<int2*>(p.ids);
+  seg.list(p.ref, free_before, [&](int a, uint32_t four, int to, bool any) {
+    uint32_t word = four << 4 * (lane & 7);
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) x[k] = a + 32 * k + lane < seg.end ? __ldcg(p.ref + a + 32 * k + lane) : 1;
+    for (int o = 1; o < 8; o <<= 1) word |= __shfl_xor_sync(0xffffffffu, word, o);
+    const int page = a + 4 * lane;
+    if ((lane & 7) == 0 && page < seg.end) words[page / 32] = make_int2(static_cast<int>(word), to);
+    if (!any || a >= used) return;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int page = a + 32 * k + lane;
-      const bool is_free = x[k] == 0;
-      const uint32_t all_free = __ballot_sync(0xffffffffu, is_free);
-      const int free_below = at + __popc(all_free & ((1u << lane) - 1));
-      at += __popc(all_free);
-      if (page >= seg.end) continue;
-      if (page < used) {
-        if (is_free) moves[free_below].dst = page;
-      } else {
-        const int r = is_free ? -1 : page - free_below - (used - n_moves);
-        p.ids[page] = r;
-        if (!is_free) moves[r].src = page, moves[r].tokens = p.page;
+    for (int i = 0; i < 4; ++i)
+      if (four & (1u << i)) {
+        if (page + i < used) moves[to].dst = page + i;
+        ++to;
       }
-    }
-  }
+  });
 }
 
 // The uses and the table's entries of pages that move.
 __device__ __forceinline__ void move_pages(const PagesView& p, moe_page_move_t* moves, int used, int n_moves, int chunks,
                                            int tid, int all) {
   const int lane = threadIdx.x & 31;
-  for (int r = tid; r < n_moves; r += all) {
-    const int src = __ldcg(&moves[r].src), dst = __ldcg(&moves[r].dst);
-    p.ref[dst] = __ldcg(p.ref + src);
-    p.ref[src] = 0;
+  const int2* words = reinterpret_cast<const int2*>(p.ids);
+  const int stay = used - n_moves;  // pages in use that do
+  auto rank = [&](int page, int2 w) {  // of a page from `used` on, -1 of a free one
+    const uint32_t free = static_cast<uint32_t>(w.x), bit = 1u << (page & 31);
+    return free & bit ? -1 : page - (w.y + __popc(free & (bit - 1))) - stay;
+  };
+  for (int page = used + tid; page < p.n_pages; page += all) {
+    const int r = rank(page, __ldcg(words + (page >> 5)));
+    if (r < 0) continue;
+    const int dst = __ldcg(&moves[r].dst);
+    moves[r].src = page, moves[r].tokens = p.page;
+    p.ref[dst] = __ldcg(p.ref + page);
+    p.ref[page] = 0;
   }
   no_moves(moves, n_moves, p.n_pages / 2, tid, all);
   const int64_t most = static_cast<int64_t>(p.stride) << p.page_log2;
@@ -539,7 +603,7 @@ __device__ __forceinline__ void move_pages(const PagesView& p, moe_page_move_t* 
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
             const bool in = static_cast<unsigned>(x[k]) < static_cast<unsigned>(p.n_pages);
-            r[k] = in && x[k] >= used ? __ldcg(p.ids + x[k]) : in ? INT_MIN : -1;
+            r[k] = in && x[k] >= used ? rank(x[k], __ldcg(words + (x[k] >> 5))) : in ? INT_MIN : -1;
           }
 #pragma unroll
           for (int k = 0; k < kBatch; ++k) {
@@ -612,7 +676,7 @@ int chunks_of(const PagesView& p, int warps) {
 }
 
 // CTAs of a cluster: 16 where the device runs so many together (8 are what every one does;
-// 344,000 pages compacted: 13.3 us, with 8 16.5 us).
+// 344,000 pages compacted, pages read twice: 13.3 us, with 8 16.5 us).
 int cluster_of(const void* kernel, std::atomic<int> (&known)[kMaxDevices]) {
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess || device >= kMaxDevices) return 8;

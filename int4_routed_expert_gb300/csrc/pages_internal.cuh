@@ -23,7 +23,7 @@ struct PagesView {
   int4* slot;          // [n_slots] parent, kept tokens, pages that it had, added tokens
   int4* place;         // [n_slots] first of its new pages, rank of its copy, page that it copies or -1
   int32_t* rows;       // [n_slots][stride] kept pages of slots whose parent is another
-  int32_t* ids;        // [n_pages] free pages, or the ranks of pages that move
+  int32_t* ids;        // [n_pages] free pages, or {free ones, free ones before} of every 32 pages
   int32_t* writers;    // [n_pages] slots that write into a page that is not full; 0 between calls
   int32_t* first;      // [n_pages] the lowest of them; kNoSlot between calls
 };

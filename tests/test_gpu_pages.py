@@ -189,7 +189,7 @@ def test_fork_refuses_on_the_device(m, slots):
 
 @pytest.mark.parametrize("pages,page,slots,width,used", [(1, 16, 1, 1, 1), (2, 16, 1, 2, 1), (33, 32, 3, 10, 20), (1000, 16, 7, 80, 300),
                                                          (8200, 64, 5, 900, 4000), (50001, 16, 300, 200, 30000),
-                                                         (300000, 16, 40, 6000, 100000)])
+                                                         (300000, 16, 40, 6000, 100000), (700001, 16, 40, 6000, 150000)])
 def test_compact(m, pages, page, slots, width, used):
     r = random.Random(pages)
     for fill in ("anywhere", "behind", "before", "none"):
