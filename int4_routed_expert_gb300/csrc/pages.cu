@@ -15,8 +15,8 @@
 // the rows are changed by the whole device, in launches before and behind a cluster of CTAs
 // that adds up what is needed and what is free, its totals by way of distributed shared
 // memory.
-// Figures (calls in a replayed graph): 16 slots of up to 1500 tokens 7.3 us; 777 slots of
-// up to 40000 tokens in a pool of 460,000 pages, a tenth of them forked, 14.1 us (one
+// Figures (calls in a replayed graph): 16 slots of up to 1500 tokens 7.0 us; 777 slots of
+// up to 40000 tokens in a pool of 460,000 pages, a tenth of them forked, 13.9 us (one
 // cluster for all three steps: 35 us); 344,000 pages compacted 11.5 us (all in the cluster:
 // 28 us).
 //
@@ -281,8 +281,9 @@ __device__ __forceinline__ bool change_uses(const ForkArgs& f, int gw, int warps
       [&](int i, int chunk, Slot& s) {
         bad |= !f.slot(i, s);
         const int kept = f.pages(s.kept);
+        int x = -1;
         if (chunk == 0 && s.added > 0 && (s.kept & (p.page - 1)) != 0) {
-          const int x = f.landing(s);
+          x = f.landing(s);
           if (!f.in_pool(x)) {
             bad = true;
           } else if (sign > 0) {
@@ -291,6 +292,10 @@ __device__ __forceinline__ bool change_uses(const ForkArgs& f, int gw, int warps
           } else {
             p.writers[x] = 0, p.first[x] = kNoSlot;
           }
+        }
+        if (chunk == 0 && sign > 0) {  // (for the sums)
+          p.slot[i] = make_int4(s.parent, s.kept, s.had, s.added);
+          p.place[i] = make_int4(0, 0, 0, x);
         }
         return s.parent == i ? kept + 32 * chunk < s.had : 32 * chunk < max(kept, s.had);
       },
@@ -338,13 +343,15 @@ __device__ __forceinline__ bool add_up(const ForkArgs& f, cg::cluster_group& cl,
   // a thread's slots: neighbours, one for most pools
   const int per = (p.n_slots + all - 1) / all;
   const int i0 = min(tid * per, p.n_slots), i1 = min(i0 + per, p.n_slots);
+  const bool good = wait();
+  auto slot = [&](int i, Slot& s, int& x) {  // as change_uses has left them
+    const int4 y = __ldcg(p.slot + i);
+    s = Slot{y.x, y.y, y.z, y.w};
+    x = __ldcg(&p.place[i].w);
+  };
   Slot s0{-1, 0, 0, 0};
   int x0 = -1, copy0 = -1;
-  if (i0 < i1) {
-    f.slot(i0, s0);
-    x0 = f.landing(s0);
-  }
-  const bool good = wait();
+  if (good && i0 < i1) slot(i0, s0, x0);
   auto count = [&](const Slot& s, int copy) {
     return (static_cast<uint64_t>(f.pages(s.kept + s.added) - f.pages(s.kept) + (copy >= 0)) << kShift) + (copy >= 0);
   };
@@ -352,10 +359,7 @@ __device__ __forceinline__ bool add_up(const ForkArgs& f, cg::cluster_group& cl,
   for (int i = i0; good && i < i1; ++i) {
     Slot s = s0;
     int x = x0, copy = -1;
-    if (i > i0) {
-      f.slot(i, s);
-      x = f.landing(s);
-    }
+    if (i > i0) slot(i, s, x);
     if (x >= 0) {
       const int uses = __ldcg(p.ref + x), n = __ldcg(p.writers + x), lowest = __ldcg(p.first + x);
       if (uses > 1 && !(n == uses && lowest == i)) copy = x;
@@ -437,11 +441,10 @@ __device__ __forceinline__ bool add_up(const ForkArgs& f, cg::cluster_group& cl,
     Slot s = s0;
     int x = x0, copy = copy0;
     if (i > i0) {
-      f.slot(i, s);
-      copy = p.place[i].z, x = p.place[i].w;
+      slot(i, s, x);
+      copy = p.place[i].z;
     }
     if (x >= 0) p.writers[x] = 0, p.first[x] = kNoSlot;  // (all have seen them)
-    p.slot[i] = make_int4(s.parent, s.kept, s.had, s.added);
     p.place[i] = make_int4(static_cast<int>(before.need >> kShift), static_cast<int>(before.need & ((1 << kShift) - 1)), copy, 0);
     before.need += count(s, copy);
     before.added += s.added;

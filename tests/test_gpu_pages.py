@@ -54,7 +54,7 @@ def fork(m, pool, ref, parent, added, keep=None):
 
 @pytest.mark.parametrize("pages,page,slots,width,steps", [
     (40, 16, 1, 30, 25), (60, 16, 5, 12, 60), (300, 32, 33, 17, 40), (2000, 64, 40, 61, 30), (9001, 16, 700, 41, 12),
-    (40000, 128, 2000, 15, 8), (12000, 16, 9000, 3, 6), (150001, 16, 40, 9000, 7), (300000, 64, 300, 2500, 7),
+    (40000, 128, 2000, 15, 8), (12000, 16, 9000, 3, 6), (30000, 16, 20000, 2, 5), (150001, 16, 40, 9000, 7), (300000, 64, 300, 2500, 7),
     (524288, 16, 20, 30000, 5), (524289, 16, 20, 30000, 5)])
 def test_fork_steps(m, pages, page, slots, width, steps):
     """Random steps: sequences go on, are cut back, forked at different points, ended, begun; some steps are refused."""
