@@ -218,7 +218,8 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
  * the rows see all of the prefix and of their own tokens.  window and sinks are not
  * supported: the rows of windowed layers do not see the whole prefix.
  * workspace: device memory of at least moe_kv_shared_workspace_bytes (0 when the arguments
- * are not valid), used until the call has run; it needs no preparation and keeps nothing.
+ * are not valid, or when the call needs none: workspace may then be NULL), used until the
+ * call has run; it needs no preparation and keeps nothing.
  * n_groups: 0 (which makes moe_kv_attend of it) to 65535. */
 typedef struct {
   int n_groups;

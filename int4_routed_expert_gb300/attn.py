@@ -517,10 +517,10 @@ class KVCache:
                 self._shared.clear()
             self._shared[key] = size
         # the call's own memory, of its stream: nothing else uses it while the call runs, nor in a graph
-        room = _results((max(size, 16),), torch.uint8, self.device, stream)
+        room = _results((size,), torch.uint8, self.device, stream) if size else None
         self._check(_lib.moe_kv_attend_shared(self.h, q.data_ptr(), qs, out.data_ptr(),
-                                              lse.data_ptr() if lse is not None else None, mask, b, p, room.data_ptr(),
-                                              size, _stream(stream, self._index)))
+                                              lse.data_ptr() if lse is not None else None, mask, b, p,
+                                              room.data_ptr() if size else None, size, _stream(stream, self._index)))
         return out
 
     def device_status(self) -> int:

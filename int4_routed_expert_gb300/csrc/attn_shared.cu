@@ -188,7 +188,7 @@ size_t align(size_t x) { return (x + 255) / 256 * 256; }
 size_t side_bytes(const Side& x, int D) { return align(x.cap * D * 4) + align(x.cap * 8); }
 
 // (one launch keeps its partial results where attention without prefixes does)
-size_t bytes_of(const Sides& x, int D) { return x.one ? 16 : side_bytes(x.own, D) + side_bytes(x.shared, D); }
+size_t bytes_of(const Sides& x, int D) { return x.one ? 0 : side_bytes(x.own, D) + side_bytes(x.shared, D); }
 
 AttnWs side_ws(const Side& x, int D, char* base) {
   return AttnWs{reinterpret_cast<float*>(base), reinterpret_cast<float2*>(base + align(x.cap * D * 4)), nullptr, x.cap};

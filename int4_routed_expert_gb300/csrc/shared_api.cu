@@ -63,7 +63,7 @@ moe_status_t moe_kv_attend_shared(moe_kv_t* h, const void* q, int64_t q_stride, 
   Share sh = share_of(batch, prefix);
   const void *p[4] = {sh.cu_seq, sh.prefix_len, sh.table, workspace};
   const char* name[4] = {"cu_seq", "prefix_len", "the prefix's page_table", "workspace"};
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < (workspace ? 4 : 3); ++i)
     if ((st = tensor(h, &h->device, name[i], &p[i])) != MOE_OK) return st;
   sh.cu_seq = static_cast<const int32_t*>(p[0]);
   sh.prefix_len = static_cast<const int32_t*>(p[1]);
@@ -71,8 +71,12 @@ moe_status_t moe_kv_attend_shared(moe_kv_t* h, const void* q, int64_t q_stride, 
   const OnDevice on(h->device);
   if (on.error != cudaSuccess) return launched(h, on.error, "moe_kv_attend_shared");
   size_t need = 0;
-  const cudaError_t e = attn_shared_launch(c, a, sh, h->ws, const_cast<void*>(p[3]), workspace_bytes, &need, h->maps, h->n_sm,
-                                           static_cast<cudaStream_t>(stream));
+  const cudaError_t e = attn_shared_launch(c, a, sh, h->ws, const_cast<void*>(p[3]), workspace ? workspace_bytes : 0, &need,
+                                           h->maps, h->n_sm, static_cast<cudaStream_t>(stream));
+  if (need && !workspace) {
+    fail(h, "workspace is NULL, the call needs %zu bytes", need);
+    return MOE_ERR_INVALID_ARG;
+  }
   if (workspace_bytes < need) {
     fail(h, "the workspace has %zu bytes, the call needs %zu", workspace_bytes, need);
     return MOE_ERR_CAPACITY;

@@ -155,11 +155,11 @@ def test_groups(m, monkeypatch, name, dim, hkv, hq, page):
 
 
 def test_the_bounds_choose_the_launches(m):
-    """One launch, which needs no workspace to speak of, and launches over parts of the keys."""
+    """One launch, which needs no workspace, and launches over parts of the keys."""
     k = Case(m, GROUPS["verify"], 64, 2, 8, 16)
     k.c.attend(k.q, k.bt.b, prefix=k.share)
     (size,) = k.c._shared.values()
-    assert (size > 16) == Case.far
+    assert (size > 0) == Case.far
 
 
 @pytest.mark.parametrize("name", ["tokens", "mixed", "idle"])
