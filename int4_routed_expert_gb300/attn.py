@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes as C
 import math
+from operator import index
 from threading import get_ident
 
 from . import moe
@@ -491,13 +492,13 @@ class KVCache:
         if lse is not None and (lse.shape != shape[:2] or lse.dtype != torch.float32 or not lse.is_contiguous()
                                 or lse.device != dev):
             raise ValueError(f"lse must be a contiguous fp32 tensor {shape[:2]} on {dev}")
-        key = (scale, causal, window, sinks)
+        # (plain numbers: a tensor would be looked up by its identity, whatever it holds by now)
+        key = (float(self.default_scale if scale is None else scale), 1 if causal else 0, index(window), index(sinks))
         mask = self._mask.get(key)
         if mask is None:
             if len(self._mask) >= 64:
                 self._mask.clear()
-            mask = self._mask[key] = moe_kv_mask_t(self.default_scale if scale is None else scale, 1 if causal else 0,
-                                                   window, sinks)
+            mask = self._mask[key] = moe_kv_mask_t(*key)
         if prefix is not None:
             return self._attend_shared(q, qs, out, lse, mask, batch, prefix, stream)
         self._check(_lib.moe_kv_attend(self.h, q.data_ptr(), qs, out.data_ptr(),
