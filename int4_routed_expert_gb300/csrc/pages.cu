@@ -4,7 +4,8 @@
 // Fork.  Slot i keeps the first k_i = min(keep_i, len[parent_i]) tokens of its parent,
 // in ceil(k_i / S) pages, and gets pages up to ceil((k_i + added_i) / S).  Uses of a
 // page change by +1 for every row that keeps it and -1 for every row that had it;
-// rows that go on (parent_i = i) change what they drop alone.  A slot writes into
+// rows that go on (parent_i = i) change what they drop alone, and what they keep is looked at
+// (777 slots: 0.6 us of the call's 14.0).  A slot writes into
 // the page of its last kept token where k_i is no multiple of S and added_i > 0; it
 // copies the page when others use it: ref > 1, and the slot is not the lowest of ref
 // writers.  New pages: the d-th page needed, in order of the slots, is the d-th free
@@ -274,8 +275,10 @@ struct ForkArgs {
 // of it taken back.  False where the arrays break their bounds.
 __device__ __forceinline__ bool change_uses(const ForkArgs& f, int gw, int warps, int sign) {
   const PagesView& p = f.p;
+  constexpr int kBatch = 4;
   const int lane = threadIdx.x & 31;
   bool bad = false;
+  int late[kBatch] = {};  // what rows that go on keep: looked at when the next entries are on their way
   each_part<Slot>(
       p.n_slots, f.chunks, gw, warps,
       [&](int i, int chunk, Slot& s) {
@@ -297,14 +300,21 @@ __device__ __forceinline__ bool change_uses(const ForkArgs& f, int gw, int warps
           p.slot[i] = make_int4(s.parent, s.kept, s.had, s.added);
           p.place[i] = make_int4(0, 0, 0, x);
         }
-        return s.parent == i ? kept + 32 * chunk < s.had : 32 * chunk < max(kept, s.had);
+        return s.parent == i ? kept + 32 * chunk < s.had || (sign > 0 && 32 * chunk < kept) : 32 * chunk < max(kept, s.had);
       },
       [&](int i, int chunk, const Slot& s) {
         const int kept = f.pages(s.kept), step = 32 * f.chunks;
         const bool goes_on = s.parent == i;
         const int32_t *from = f.row(max(s.parent, 0)), *old = f.row(i);
         const int n_from = goes_on || s.parent < 0 ? 0 : kept;
-        constexpr int kBatch = 4;
+        if (goes_on && sign > 0)
+          for (int j = 32 * chunk + lane; j < kept; j += kBatch * step) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              bad |= !f.in_pool(late[k]);
+              late[k] = j + k * step < kept ? old[j + k * step] : 0;
+            }
+          }
         for (int j = (goes_on ? kept : 0) + 32 * chunk + lane; j < max(n_from, s.had); j += kBatch * step) {
           int x[kBatch], y[kBatch];
 #pragma unroll
@@ -323,6 +333,8 @@ __device__ __forceinline__ bool change_uses(const ForkArgs& f, int gw, int warps
           }
         }
       });
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) bad |= !f.in_pool(late[k]);
   return !bad;
 }
 
