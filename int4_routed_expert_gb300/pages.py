@@ -60,8 +60,8 @@ def _load() -> C.CDLL:
 class PagePool:
     """The page pool (moe_pages_*): wraps table [slots, width] (page ids, -1 for none), kv_len [slots] and ref [pages]
     (uses of each page), int32 CUDA tensors that it changes in place; ``PagePool.empty`` allocates them.  cu_q
-    [slots + 1] and free [1] (free pages) are its own results; so are the moves that fork and compact return, which
-    the next call of the same kind writes over."""
+    [slots + 1] and free [1] (free pages: counted here, then as of the last fork or compact) are its own results; so are
+    the moves that fork and compact return, which the next call of the same kind writes over."""
 
     def __init__(self, table, kv_len, ref, page_size: int):
         self.h = None
@@ -76,7 +76,7 @@ class PagePool:
         self.n_slots, self.n_pages, self.device, self._index = n, ref.shape[0], table.device, table.get_device()
         i32 = dict(dtype=torch.int32, device=self.device)
         self.cu_q = torch.zeros(n + 1, **i32)
-        self.free = torch.zeros(1, **i32)
+        self.free = (ref == 0).sum(dtype=torch.int32).view(1)
         self._forked = torch.full((n, 3), -1, **i32)
         self._compacted = torch.full((self.n_pages // 2, 3), -1, **i32)
         cfg = moe_pages_config_t(self.n_pages, page_size, n, table.shape[1])
@@ -92,10 +92,8 @@ class PagePool:
     def empty(cls, n_pages: int, page_size: int, n_slots: int, max_kv_len: int, device="cuda"):
         _load()
         i32 = dict(dtype=torch.int32, device=device)
-        pool = cls(torch.full((n_slots, -(-max_kv_len // page_size)), -1, **i32), torch.zeros(n_slots, **i32),
+        return cls(torch.full((n_slots, -(-max_kv_len // page_size)), -1, **i32), torch.zeros(n_slots, **i32),
                    torch.zeros(n_pages, **i32), page_size)
-        pool.free.fill_(n_pages)
-        return pool
 
     def _check(self, st):
         if st != MOE_OK:

@@ -62,3 +62,25 @@ def test_a_bad_entry_of_a_slot_that_goes_on(m, slots, width, cut):
                     pool.device_status()
             pool.table[slot, at] = good
     fork(go_on, added, keep)
+
+
+@pytest.mark.parametrize("uses", [[0], [3], [0, 1, 0, -1, 2, 0], [1, 0] * 3000])
+def test_free_pages_of_a_pool_that_no_call_has_changed(m, uses):
+    """The count is right before the first call, and stays when that one is refused."""
+    pool = m.PagePool(t([[-1, -1], [-1, -1]]), t([0, 0]), t(uses), 16)
+    free = uses.count(0)
+    assert pool.free.shape == (1,) and pool.free.dtype == torch.int32 and pool.free.item() == free
+    pool.fork(t([-1, 2]), t([1, 0]))
+    with pytest.raises(m.MoeError, match="bounds"):
+        pool.device_status()
+    assert pool.free.item() == free
+    if free:
+        pool.fork(t([-1, -1]), t([1, 0]))
+        assert pool.free.item() == free - 1 and pool.device_status() == 0
+    pool = m.PagePool.empty(len(uses), 16, 3, 100, device=DEV)
+    assert pool.free.item() == len(uses) and pool.table.shape == (3, 7)
+    parent, added, side = t([-1, -1, -1]), t([1, 0, 0]), torch.cuda.Stream()
+    pool = m.PagePool.empty(len(uses), 16, 3, 100, device=DEV)
+    pool.fork(parent, added, stream=side)  # on another stream, straight behind
+    torch.cuda.synchronize()
+    assert pool.free.item() == len(uses) - 1
