@@ -26,8 +26,8 @@ __global__ void __launch_bounds__(kThreads)
   const int d_log2 = c.D == 128 ? 7 : 6;
   const int step = gridDim.x / slices;
   bool bad = false;
-  // the CTA's next 32 moves, a lane each
-  for (int m0 = blockIdx.x / slices; m0 < n; m0 += 32 * step) {
+  // the CTA's next 32 moves, a lane each (in 64 bits: the round behind the last one may begin above 2^31)
+  for (int64_t m0 = blockIdx.x / slices; m0 < n; m0 += 32LL * step) {
     const int64_t at = m0 + static_cast<int64_t>(lane) * step;
     int src = -1, dst = -1, tokens = 0;
     if (at < n) src = __ldg(&moves[at].src), dst = __ldg(&moves[at].dst), tokens = __ldg(&moves[at].tokens);

@@ -84,3 +84,24 @@ def test_free_pages_of_a_pool_that_no_call_has_changed(m, uses):
     pool.fork(parent, added, stream=side)  # on another stream, straight behind
     torch.cuda.synchronize()
     assert pool.free.item() == len(uses) - 1
+
+
+def test_copy_of_the_longest_list(m):
+    """2^31 - 1 moves (26 GB), most of which are none: the first, some in between and the last are made."""
+    n = 2 ** 31 - 1
+    codes = [torch.randint(0, 256, (16, 2, 16, 64), device=DEV, dtype=torch.uint8) for _ in range(2)]
+    scales = [torch.rand(16, 2, device=DEV) for _ in range(2)]
+    c = m.KVCache(*codes, *scales, n_q_heads=2, max_seqs=1, max_tokens=1, max_kv_len=1)
+    want = [x.clone() for x in codes + scales]
+    moves = torch.full((n, 3), -1, **I32)
+    for i, (at, tokens) in enumerate(((0, 16), (38911, 16), (38912, 3), (2 ** 30 + 5, 16), (n - 38913, 16), (n - 2, 16), (n - 1, 9))):
+        moves[at] = t([i, 15 - i, tokens])
+        for x in want[:2]:
+            x[15 - i, :, :tokens] = x[i, :, :tokens]
+        for x in want[2:]:
+            x[15 - i] = x[i]
+    c.copy(moves)
+    assert c.device_status() == 0
+    assert all(torch.equal(x, y) for x, y in zip(want, codes + scales))
+    del moves
+    torch.cuda.empty_cache()
