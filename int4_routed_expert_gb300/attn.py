@@ -465,8 +465,8 @@ class KVCache:
         """Copies pages: moves [n, 3] int32 (source page, destination page, tokens), such as PagePool.fork and
         PagePool.compact give; a negative source is no move."""
         if moves.dtype is not torch.int32 or moves.dim() != 2 or moves.shape[1] != 3 or not moves.is_contiguous() \
-                or moves.get_device() != self._index:
-            raise ValueError(f"moves must be a contiguous int32 tensor [n, 3] on {self.device}, got {moves.dtype} "
+                or moves.shape[0] >= 1 << 31 or moves.get_device() != self._index:
+            raise ValueError(f"moves must be a contiguous int32 tensor [n, 3], n below 2^31, on {self.device}, got {moves.dtype} "
                              f"{tuple(moves.shape)} on {moves.device}")
         self._check(_lib.moe_kv_copy(self.h, moves.data_ptr(), moves.shape[0], _stream(stream, self._index)))
 
