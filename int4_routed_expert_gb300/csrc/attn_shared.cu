@@ -159,8 +159,9 @@ Sides sides_of(const KvView& c, const Share& sh, int G, int n_sm) {
     s.one = one < std::max(prefix, own) + static_cast<double>(s.own.cap) * c.D * 8 / 5e6 + 7.;
     return s;
   };
+  // (units are counted in 32 bits: room for those of groups whose offsets do not ascend, which are of the same rows)
   if (s.shared.few || s.shared.parts > 1 || sh.n_groups > 32 ||
-      (live + sh.n_groups * c.hkv) * static_cast<double>(tiles) > 1e9)  // (units are counted in 32 bits)
+      static_cast<double>(s.shared.pl.row_tiles) * sh.n_groups * c.hkv * static_cast<double>(tiles) > 1e9)
     return decide(least);
   const double units = live * static_cast<double>(tiles);
   int64_t ctas = 0;
