@@ -219,7 +219,10 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
  * supported: the rows of windowed layers do not see the whole prefix.
  * workspace: device memory of at least moe_kv_shared_workspace_bytes (0 when the arguments
  * are not valid, or when the call needs none: workspace may then be NULL), used until the
- * call has run; it needs no preparation and keeps nothing.
+ * call has run; it needs no preparation and keeps nothing.  It holds fp32 sums of every row,
+ * over the prefix and over its own tokens, and so grows with the call:
+ *   at most max(4 * n_tokens * n_q_heads, 2^21) * (4 * head_dim + 8) bytes and 1 KB
+ * (64 tokens of 64 heads of 128 on a prefix of 16384: 13 MB; 16384 of them: 1.6 GB).
  * n_groups: 0 (which makes moe_kv_attend of it) to 65535. */
 typedef struct {
   int n_groups;

@@ -476,7 +476,8 @@ class KVCache:
         tokens (write the new ones first).  window > 0: a token sees the last ``window`` tokens, itself
         included, and the first ``sinks`` ones.  Returns out [tokens, q heads, head_dim] bf16; lse, when given,
         is filled with the natural logarithms of the softmax denominators [tokens, q heads] fp32.  prefix: tokens that
-        sequences share, read once for all of them (not with a window)."""
+        sequences share, read once for all of them (not with a window); such a call takes memory of its own for the time
+        that it runs, up to 4 fp32 rows of head_dim for each row of out where those are many (moe_kv_shared_workspace_bytes)."""
         dev, H = self.device, self.n_q_heads
         qs = self._tokens(q, "q", H, batch)
         bf16 = torch.bfloat16

@@ -52,3 +52,24 @@ def test_dealt_out_units_fit_32_bits_whatever_the_arrays_hold(plan):
             units = groups * -(-tokens * g // ROWS) * kv_heads * -(-prefix // KEYS)
             assert units + max(units // p["ctas"] + 1, -(-prefix // KEYS)) < 2 ** 31, (s, p)
     assert dealt > 300
+
+
+def test_the_workspace_stays_below_what_the_header_says(plan):
+    r, most = random.Random(2), 0.0
+    sizes = [(64, 64, 1, 17884, 8, 128, 8, 1, 64, 16384), (4, 16384, 4096, 34096, 8, 128, 8, 1, 16384, 30000),
+             (42, 218, 7, 3485842, 256, 128, 16, 1, 87, 2644173)]
+    for _ in range(3000):
+        kv_heads, g = r.choice((1, 2, 4, 8, 64, 256)), r.choice((1, 2, 4, 8, 12, 16))
+        tokens = int(2 ** r.uniform(0, 24))
+        if tokens * kv_heads * g > 2 ** 31 - 1:
+            continue
+        kv, seqs = int(2 ** r.uniform(0, 30)), r.randint(1, min(r.choice((64, 65535)), tokens))
+        sizes.append((seqs, tokens, r.choice((1, tokens, r.randint(1, tokens))), kv, kv_heads, r.choice((64, 128)), g,
+                      r.choice((1, 1, 2, 5, 32, 33, seqs)), r.randint(1, tokens), r.randint(1, kv)))
+    for s in sizes:
+        p, size = plan(*s)
+        bound = max(4 * s[1] * s[4] * s[6], 1 << 21) * (4 * s[5] + 8) + 1024
+        assert size <= bound and (size == 0) == bool(p["one"]), (s, p, size)
+        most = max(most, size / bound)
+    assert most > 0.9
+    assert [plan(*s)[1] >> 20 for s in sizes[:2]] == [12, 1560]  # MiB, of the sizes that the header gives
