@@ -215,8 +215,12 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
  * handle's max_kv_len).  A group whose arrays break them (cu_seq not ascending within
  * [0, n_seqs], a length outside [0, max_prefix_len], a needed page id outside [0, n_pages))
  * sets bit 1 of moe_kv_device_status, and its rows are not valid.  With mask->causal == 0
- * the rows see all of the prefix and of their own tokens.  window and sinks are not
- * supported: the rows of windowed layers do not see the whole prefix.
+ * the rows see all of the prefix and of their own tokens.  window and
+ * sinks are not supported: the rows of windowed layers do not see the whole prefix.
+ * The work is cut for sequences of about max_kv_len - max_prefix_len tokens of their own.  One
+ * that has many more (that no group holds, or whose prefix is much shorter) has its results
+ * all the same, but few CTAs go over its keys, which can take longer than moe_kv_attend
+ * does; bounds far above the lengths cost time, too.
  * workspace: device memory of at least moe_kv_shared_workspace_bytes (0 when the arguments
  * are not valid, or when the call needs none: workspace may then be NULL), used until the
  * call has run; it needs no preparation and keeps nothing.  It holds fp32 sums of every row,

@@ -220,8 +220,8 @@ class Rope:
 
     def apply(self, q, positions, k=None, q_out=None, k_out=None, stream=None):
         """Rotates q [tokens, heads, head_dim] (and k) at positions [tokens] int32 ([axes, tokens] with axes, whose
-        rows may be further apart); returns q's result, or (q's, k's) when k is given.  Tokens may be strided (parts of one projection); q_out is q rotates in
-        place."""
+        rows may be further apart); returns q's result, or (q's, k's) when k is given.  Tokens may be strided (parts of
+        one projection); q_out is q rotates in place."""
         if q_out is None and k_out is None:
             # the checks of a layout (shapes, strides, types) once: a call is a few microseconds; the argument
             # structs are a thread's own
@@ -477,7 +477,9 @@ class KVCache:
         included, and the first ``sinks`` ones.  Returns out [tokens, q heads, head_dim] bf16; lse, when given,
         is filled with the natural logarithms of the softmax denominators [tokens, q heads] fp32.  prefix: tokens that
         sequences share, read once for all of them (not with a window); such a call takes memory of its own for the time
-        that it runs, up to 4 fp32 rows of head_dim for each row of out where those are many (moe_kv_shared_workspace_bytes)."""
+        that it runs, up to 4 fp32 rows of head_dim for each row of out where those are many (moe_kv_shared_workspace_bytes).
+        It is made for sequences whose own tokens are about as many as the bounds say, max_kv_len less max_prefix_len: where
+        one has many more, or the prefix has a few hundred tokens, attention without it can take less time."""
         dev, H = self.device, self.n_q_heads
         qs = self._tokens(q, "q", H, batch)
         bf16 = torch.bfloat16

@@ -124,7 +124,9 @@ Sides sides_of(const KvView& c, const Share& sh, int G, int n_sm) {
   double own_live, live;
   s.own = side_of(c, G, own_live);
   s.shared = side_of(s.prefix, G, live);
-  // the host knows no bound of a sequence's own tokens; where prefixes are alike it is this
+  // The host knows no bound of a sequence's own tokens; where prefixes are alike it is this.  A
+  // sequence that has many more gets no more splits (8 single tokens on a prefix of 65961, 64 / 8
+  // heads: 54 us; with a ninth of 66001 own tokens 435 us, and 157 us as attention of each).
   const int64_t own_tiles = (std::max(c.max_kv - sh.max_len, 1) + kKeys - 1) / kKeys;
   const int64_t tiles = (sh.max_len + kKeys - 1) / kKeys;
   const CtaCost own_cost = cost_of(static_cast<int64_t>(c.max_q) * G), cost = cost_of(static_cast<int64_t>(s.prefix.max_q) * G);

@@ -91,7 +91,7 @@ enum Bar {
 // are the same rows then, each with every other tile of keys and with sums of
 // its own, which the join takes for two splits: one's softmax still runs under
 // the other's products.  48 rows a kv head (four sequences of up to 131072
-// keys, 4 kv heads): 142 us, and 198 us as one M tile.
+// keys, 4 kv heads): 143 us, and 198 us as one M tile.
 // Part::kDealt: a CTA goes from one piece of the dealt out work to the next; the load warp
 // brings the next piece's keys while the last one's results are written.
 template <int D, bool DUAL, Part PART>

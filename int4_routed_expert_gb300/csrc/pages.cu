@@ -5,7 +5,7 @@
 // in ceil(k_i / S) pages, and gets pages up to ceil((k_i + added_i) / S).  Uses of a
 // page change by +1 for every row that keeps it and -1 for every row that had it;
 // rows that go on (parent_i = i) change what they drop alone, and what they keep is looked at
-// (777 slots: 0.6 us of the call's 14.0).  A slot writes into
+// (777 slots: 0.5 us of the call's 14.0).  A slot writes into
 // the page of its last kept token where k_i is no multiple of S and added_i > 0; it
 // copies the page when others use it: ref > 1, and the slot is not the lowest of ref
 // writers.  New pages: the d-th page needed, in order of the slots, is the d-th free
@@ -16,8 +16,8 @@
 // the rows are changed by the whole device, in launches before and behind a cluster of CTAs
 // that adds up what is needed and what is free, its totals by way of distributed shared
 // memory.
-// Figures (calls in a replayed graph): 16 slots of up to 1500 tokens 7.0 us; 777 slots of
-// up to 40000 tokens in a pool of 460,000 pages, a tenth of them forked, 13.9 us (one
+// Figures (calls in a replayed graph): 16 slots of up to 1500 tokens 7.9 us; 777 slots of
+// up to 40000 tokens in a pool of 460,000 pages, a tenth of them forked, 14.0 us (one
 // cluster for all three steps: 35 us); 344,000 pages compacted 11.5 us (all in the cluster:
 // 28 us).
 //
