@@ -213,8 +213,9 @@ moe_status_t moe_kv_attend(moe_kv_t* h, const void* q, int64_t q_stride, void* o
  * gives bounds: max_group_tokens new tokens of any group (their rows are those from its
  * first sequence's to its last one's), max_prefix_len tokens of any prefix (at most the
  * handle's max_kv_len).  A group whose arrays break them (cu_seq not ascending within
- * [0, n_seqs], a length outside [0, max_prefix_len], a needed page id outside [0, n_pages))
- * sets bit 1 of moe_kv_device_status, and its rows are not valid.  With mask->causal == 0
+ * [0, n_seqs], a length outside [0, max_prefix_len], a needed page id outside [0, n_pages), the
+ * offset in cu_q of its first or behind its last sequence) sets bit 1 of moe_kv_device_status,
+ * and its rows are not valid; other groups' are.  With mask->causal == 0
  * the rows see all of the prefix and of their own tokens.  window and
  * sinks are not supported: the rows of windowed layers do not see the whole prefix.
  * The work is cut for sequences of about max_kv_len - max_prefix_len tokens of their own.  One

@@ -233,10 +233,14 @@ __global__ void __launch_bounds__(kJoinThreads)
                 const AttnWs shared_ws, int slices) {
   constexpr int kPer = kJoinThreads / (D / 4), kBatch = 8;
   const int t = blockIdx.x / slices, slice = blockIdx.x % slices;
-  const int b = last_not_above(c.cu_q, c.n_seqs, t);
+  bool odd = false, covered;
   Seq q, g{0, 0, 0};
-  InGroup in = group_of(sh, b);
-  const bool covered = load_seq(c, b, q) && t >= q.q0 && t < q.q0 + q.n;
+  InGroup in;
+  for (int b = last_not_above(c.cu_q, c.n_seqs, t, odd), other = -1;; b = other) {
+    in = group_of(sh, b);
+    covered = load_seq(c, b, q) && t >= q.q0 && t < q.q0 + q.n;
+    if (covered || other >= 0 || (other = range_of(c.cu_q, c.n_seqs, t, c.n_tokens, b, odd)) < 0) break;
+  }
   const int begin = covered ? own_begin(sh, q, in) : 0;
   int n_shared = 0, per, before = 0, g_tiles = 0, g_per = 1;
   if constexpr (DEALT) {

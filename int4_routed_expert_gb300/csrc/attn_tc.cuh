@@ -438,19 +438,42 @@ __device__ __forceinline__ bool load_group(const KvView& c, const Share& sh, int
   return ok;
 }
 
+// Whether range i of the offsets v holds x, and lies within [0, most].
+__device__ __forceinline__ bool holds(int begin, int end, int x, int most) {
+  return begin >= 0 && begin <= x && x < end && end <= most;
+}
+
 // The last of n ascending numbers that is not above x, looked for by the whole warp, 32
-// places at once; 0 where all are above it.
-__device__ __forceinline__ int last_not_above(const int32_t* v, int n, int x) {
+// places at once; 0 where all are above it.  `odd`: they turned out not to ascend.
+__device__ __forceinline__ int last_not_above(const int32_t* v, int n, int x, bool& odd) {
   const int lane = threadIdx.x & 31;
   int lo = 0;
   for (int step = n; step > 1;) {
     step = (n + 31) / 32;
     const int at = lane * step;
-    const int k = max(__popc(__ballot_sync(0xffffffffu, at < n && __ldg(v + lo + at) <= x)), 1);
+    const uint32_t below = __ballot_sync(0xffffffffu, at < n && __ldg(v + lo + at) <= x);
+    const int k = max(__popc(below), 1);
+    odd |= (below & (below + 1)) != 0;
     lo += (k - 1) * step;
     n = min(step, n - (k - 1) * step);
   }
   return lo;
+}
+
+// Where the range `lo` that was found so does not hold x: which of the n does; -1 for none.  Where
+// x is not before all of them or behind, an offset breaks its bounds, and the ranges that do
+// not begin or end with it are found by looking at all.
+__device__ __forceinline__ int range_of(const int32_t* v, int n, int x, int most, int lo, bool odd) {
+  const int begin = __ldg(v + lo), end = __ldg(v + lo + 1), lane = threadIdx.x & 31;
+  if (holds(begin, end, x, most)) return lo;
+  if (!odd && begin >= 0 && end >= begin && end <= most && (x < begin ? lo == 0 : lo == n - 1)) return -1;
+  int found = -1;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t in = __ballot_sync(0xffffffffu, i < n && holds(__ldg(v + i), __ldg(v + i + 1), x, most));
+    if (in) found = i0 + 31 - __clz(in);
+  }
+  return found;
 }
 
 // A sequence's group and its prefix's length; g is -1 where no group holds it.  Up to 32
@@ -462,13 +485,16 @@ __device__ __forceinline__ InGroup group_of(const Share& sh, int b) {
   if (sh.n_groups <= 32) {
     const int lane = threadIdx.x & 31, g = min(lane, sh.n_groups - 1);
     const int s0 = __ldg(sh.cu_seq + g), s1 = __ldg(sh.cu_seq + g + 1), p = __ldg(sh.prefix_len + g);
-    const uint32_t in = __ballot_sync(0xffffffffu, lane < sh.n_groups && s0 <= b && b < s1);
+    const uint32_t in = __ballot_sync(0xffffffffu, lane < sh.n_groups && holds(s0, s1, b, sh.n_seqs));
     const int at = in ? 31 - __clz(in) : 0;
     return {in ? at : -1, __shfl_sync(0xffffffffu, p, at)};
   }
-  const int g = last_not_above(sh.cu_seq, sh.n_groups, b);
+  bool odd = false;
+  int g = last_not_above(sh.cu_seq, sh.n_groups, b, odd);
   const int s0 = __ldg(sh.cu_seq + g), s1 = __ldg(sh.cu_seq + g + 1), p = __ldg(sh.prefix_len + g);
-  return {s0 <= b && b < s1 ? g : -1, p};
+  if (holds(s0, s1, b, sh.n_seqs)) return {g, p};
+  g = range_of(sh.cu_seq, sh.n_groups, b, sh.n_seqs, g, odd);
+  return {g, __ldg(sh.prefix_len + max(g, 0))};
 }
 
 // The first of a sequence's own keys: its prefix's length when all of its new tokens lie
