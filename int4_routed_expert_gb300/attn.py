@@ -188,7 +188,7 @@ def rope_axes(rot_dim: int, sections, turns: bool = False):
 class Rope:
     """Rotary positions (moe_rope_*).  Frequencies by rope_frequencies, or given (radians per position).  axes: the
     axis (0 .. 3) of each pair, for tokens that have several positions (time, height and width of a patch), as
-    rope_axes makes it; positions are then [axes, tokens]."""
+    rope_axes makes it; positions are then [axes, tokens], a row for each axis up to the highest that a pair has."""
 
     def __init__(self, rot_dim: int, theta: float = 10000.0, interleaved: bool = False, scaling: str | None = None,
                  factor: float = 1.0, original_len: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
